@@ -140,6 +140,29 @@ DSA_API dsa_status_t dsa_topk(const float* scores, int rows, int64_t ld, const i
 DSA_API dsa_status_t dsa_sparse_mla_attn(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx, int T,
                                  int H, int k, float scale, uint16_t* out, float* lse, void* stream);
 
+/* Workspace bytes of dsa_sparse_mla_attn_backward (0 for unsupported shapes). */
+DSA_API size_t dsa_sparse_mla_attn_backward_workspace_size(int T, int S, int H, int k);
+
+/*
+ * Backward pass of dsa_sparse_mla_attn: the gradients of its queries and latent entries from the gradient of its
+ * output.  With P = exp(scale * q . c_s - lse) over the selected entries, dP = dout . c_s[:512] and
+ * dS = scale * P * (dP - dout . out):
+ *   dq[t,h] = sum over selected s of dS c_s,     dc[s] = sum over the (t, h) that selected s of dS q + [P dout, 0].
+ *   q, c, idx, H, k, scale: the forward's inputs; out [T, H, 512] bf16 and lse [T, H] fp32: its outputs (a selection
+ *     spread over several calls may pass the joined out and lse); dout [T, H, 512] bf16: the gradient of out;
+ *   dq [T, H, 576] bf16 (out), dc [S, 576] bf16 (out): every row is written (rows that no token selected get 0), so
+ *     a caller that accumulates adds them itself.  The selection and lse pass no gradient on.
+ * A row of c selected twice by a token counts twice, as in the forward.  A token without entries (lse = -INFINITY)
+ * has dq = 0.  An entry outside [-1, S) is treated as -1 and recorded as DSA_ERR_BAD_INDEX.
+ * P, dS and each entry's contribution to dc are rounded to bf16 once; every sum is fp32.
+ *   ws: dsa_sparse_mla_attn_backward_workspace_size() bytes, 16-byte aligned.  Long T are worked through in chunks of
+ *     tokens (about 2 GiB of workspace).
+ */
+DSA_API dsa_status_t dsa_sparse_mla_attn_backward(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx,
+                                                  const uint16_t* out, const float* lse, const uint16_t* dout, int T,
+                                                  int H, int k, float scale, uint16_t* dq, uint16_t* dc, void* ws,
+                                                  size_t ws_bytes, void* stream);
+
 /*
  * The indexer's training objective (velog.io page, Stage 1 Dense Warm-up): for each query token t,
  *   kl[t] = KL(p_t || Softmax(I_t)),  p_t = the heads' attention probabilities summed and L1-normalised,
@@ -155,6 +178,22 @@ DSA_API dsa_status_t dsa_sparse_mla_attn(const uint16_t* q, const uint16_t* c, i
 DSA_API dsa_status_t dsa_indexer_kl(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx,
                                     const float* sel_scores, const float* lse, int T, int H, int k, float scale,
                                     float* kl, void* stream);
+
+/* Workspace bytes of dsa_indexer_kl_backward. */
+DSA_API size_t dsa_indexer_kl_backward_workspace_size(int T);
+
+/*
+ * Gradient of dsa_indexer_kl with respect to the index scores of the selected entries:
+ *   dsel[t][i] = dkl[t] * (Softmax(I_t)_i - p_t,i) over the token's selected entries, 0 where idx is -1.
+ * The target p_t is a constant of the objective: no gradient reaches q, c or lse.
+ *   q, c, S, idx, sel_scores, lse, T, H, k, scale: as in dsa_indexer_kl;
+ *   dkl [T] fp32 or NULL (1 for every token): the gradient of kl;
+ *   dsel [T, k] fp32 (out);
+ *   ws: dsa_indexer_kl_backward_workspace_size() bytes, 16-byte aligned.
+ */
+DSA_API dsa_status_t dsa_indexer_kl_backward(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx,
+                                             const float* sel_scores, const float* lse, const float* dkl, int T, int H,
+                                             int k, float scale, float* dsel, void* ws, size_t ws_bytes, void* stream);
 
 /* Workspace bytes of dsa_forward_prefill_kl. */
 DSA_API size_t dsa_prefill_kl_workspace_size(int L, int H_I, int d_I, int H, int k);

@@ -33,7 +33,11 @@ SIGNATURES = {
     "dsa_indexer_scores": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
     "dsa_topk": (_I, [_P, _I, _I64, _P, _I, _I, _P, _P]),
     "dsa_sparse_mla_attn": (_I, [_P, _P, _I, _P, _I, _I, _I, _F, _P, _P, _P]),
+    "dsa_sparse_mla_attn_backward_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "dsa_sparse_mla_attn_backward": (_I, [_P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]),
     "dsa_indexer_kl": (_I, [_P, _P, _I, _P, _P, _P, _I, _I, _I, _F, _P, _P]),
+    "dsa_indexer_kl_backward_workspace_size": (_SZ, [_I]),
+    "dsa_indexer_kl_backward": (_I, [_P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _SZ, _P]),
     "dsa_prefill_kl_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "dsa_forward_prefill_kl": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _SZ,
                                     _P]),
@@ -177,6 +181,29 @@ def dsa_sparse_mla_attn(q, c, idx, scale: float, out=None, lse=None, want_lse: b
     return out, lse
 
 
+def dsa_sparse_mla_attn_backward_workspace_size(T: int, S: int, H: int, k: int) -> int:
+    return int(_lib.dsa_sparse_mla_attn_backward_workspace_size(T, S, H, k))
+
+
+def dsa_sparse_mla_attn_backward(q, c, idx, out, lse, dout, scale: float, dq=None, dc=None, ws=None, stream=None):
+    """Gradients (dq [T, H, 576], dc [S, 576]) of dsa_sparse_mla_attn's queries and latent entries, from its inputs,
+    its outputs out and lse, and the gradient dout [T, H, 512] of out."""
+    T, H, _ = q.shape
+    S = c.shape[0]
+    k = idx.shape[1]
+    if dq is None:
+        dq = torch.empty((T, H, 576), dtype=torch.bfloat16, device=q.device)
+    if dc is None:
+        dc = torch.empty((S, 576), dtype=torch.bfloat16, device=q.device)
+    if ws is None:
+        ws = torch.empty((dsa_sparse_mla_attn_backward_workspace_size(T, S, H, k),), dtype=torch.uint8,
+                         device=q.device)
+    _check("dsa_sparse_mla_attn_backward", _lib.dsa_sparse_mla_attn_backward(
+        _ptr(q), _ptr(c), S, _ptr(idx), _ptr(out), _ptr(lse), _ptr(dout), T, H, k, float(scale), _ptr(dq), _ptr(dc),
+        _ptr(ws), ws.numel(), _stream(stream)))
+    return dq, dc
+
+
 def dsa_indexer_kl(q, c, idx, sel_scores, lse, scale: float, kl=None, stream=None):
     """KL(p_t || Softmax(I_t)) [T] of each token over its selected entries, from the attention's lse [T, H] and the
     selected entries' index scores sel_scores [T, k]."""
@@ -189,6 +216,26 @@ def dsa_indexer_kl(q, c, idx, sel_scores, lse, scale: float, kl=None, stream=Non
         _ptr(q), _ptr(c), S, _ptr(idx), _ptr(sel_scores), _ptr(lse), T, H, k, float(scale), _ptr(kl),
         _stream(stream)))
     return kl
+
+
+def dsa_indexer_kl_backward_workspace_size(T: int) -> int:
+    return int(_lib.dsa_indexer_kl_backward_workspace_size(T))
+
+
+def dsa_indexer_kl_backward(q, c, idx, sel_scores, lse, dkl, scale: float, dsel=None, ws=None, stream=None):
+    """Gradient dsel [T, k] of dsa_indexer_kl with respect to the selected entries' index scores, from the gradient
+    dkl [T] of its divergences (None: 1)."""
+    T, H, _ = q.shape
+    S = c.shape[0]
+    k = idx.shape[1]
+    if dsel is None:
+        dsel = torch.empty((T, k), dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = torch.empty((dsa_indexer_kl_backward_workspace_size(T),), dtype=torch.uint8, device=q.device)
+    _check("dsa_indexer_kl_backward", _lib.dsa_indexer_kl_backward(
+        _ptr(q), _ptr(c), S, _ptr(idx), _ptr(sel_scores), _ptr(lse), _ptr(dkl), T, H, k, float(scale), _ptr(dsel),
+        _ptr(ws), ws.numel(), _stream(stream)))
+    return dsel
 
 
 def dsa_prefill_kl_workspace_size(L: int, H_I: int, d_I: int, H: int, k: int) -> int:

@@ -13,7 +13,9 @@
 
 #include "common.cuh"
 #include "indexer.cuh"
+#include "scatter.cuh"
 #include "sparse_mla.cuh"
+#include "sparse_mla_bwd.cuh"
 #include "topk.cuh"
 #include "topk_cluster.cuh"
 
@@ -634,6 +636,208 @@ dsa_status_t run_decode(int B, const DecodeLayout& lay, const int32_t* ctx_len, 
   if (e != DSA_OK) return e;
   return run_mla(q, c_cache, lay.cache_rows, idx, lay.cache_off, B, H, k, scale, out, lse, st, kMlaCounts, len1,
                  lay.page_table, lay.max_pages, lay.page_rows);
+}
+
+// ------------------------------------------------------------------------------------------ backward passes
+// Hands out 256-byte aligned pieces of a workspace (null base: only counts).
+struct Carve {
+  char* base;
+  size_t at = 0;
+  template <typename X>
+  X* take(size_t n) {
+    X* r = base ? reinterpret_cast<X*>(base + at) : nullptr;
+    at += align_up(n * sizeof(X), 256);
+    return r;
+  }
+};
+
+// Tokens that a backward pass handles at once: as many as keep the per-entry buffers (`per_entry` bytes for each of
+// kp slots) and the scatter table (2 bytes for each of S rows) of a chunk within 2 GiB, at least 64, and equal chunks.
+// Measured for the attention's pass over 2048 tokens of k = 2048: see the chunk sizes in the table of design notes.
+int bwd_chunk(int T, int64_t S, int kp, size_t per_entry) {
+  const size_t each = size_t(kp) * per_entry + 2 * size_t(S);
+  const size_t cap = std::min<size_t>(sct::MAX_T, std::max<size_t>(64, (size_t(2) << 30) / each));
+  if (size_t(T) <= cap) return T > 0 ? T : 1;
+  const size_t chunks = (size_t(T) + cap - 1) / cap;
+  return static_cast<int>((size_t(T) + chunks - 1) / chunks);
+}
+
+int round_up(int n, int m) { return (n + m - 1) / m * m; }
+
+// Scatter of a chunk's contributions: the table and what goes with it.
+struct ScatterWs {
+  int *n_end, *fill;
+  uint16_t *table, *mult, *contrib;
+  float* acc;
+  int ld;
+};
+ScatterWs carve_scatter(Carve& w, int Tc, int64_t S, int k, int kp, int width, bool many) {
+  ScatterWs s{};
+  s.ld = round_up(Tc, 8);
+  s.n_end = w.take<int>(Tc);
+  s.fill = w.take<int>(Tc);
+  s.mult = w.take<uint16_t>(size_t(Tc) * k);
+  s.table = w.take<uint16_t>(size_t(S) * s.ld);
+  s.contrib = w.take<uint16_t>(size_t(Tc) * kp * width);
+  s.acc = many ? w.take<float>(size_t(S) * width) : nullptr;
+  return s;
+}
+
+dsa_status_t scatter_begin(const ScatterWs& w, const int* idx, int T, int64_t S, int k, cudaStream_t st) {
+  const long long n = static_cast<long long>(S) * w.ld / 8;
+  const int grid = static_cast<int>(std::min<long long>((n + 255) / 256, 8ll * num_sms()));
+  if (launch_pdl(scatter_clear_kernel, dim3(grid), dim3(256), 0, st, reinterpret_cast<uint4*>(w.table), n) !=
+      cudaSuccess)
+    return DSA_ERR_CUDA;
+  dsa_status_t e = last_launch_status();
+  if (e != DSA_OK) return e;
+  if (launch_pdl(scatter_build_kernel, dim3(T), dim3(256), 0, st, idx, k, static_cast<long long>(S), w.n_end, w.fill,
+                 w.table, w.ld, w.mult) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  return last_launch_status();
+}
+
+template <int W>
+dsa_status_t scatter_end(const ScatterWs& w, int T, int64_t S, int k, int kp, bool first, bool last, uint16_t* out,
+                         cudaStream_t st) {
+  const ScatterParams p{w.contrib, w.table, w.mult, T, w.ld, k, kp, w.acc, first ? 1 : 0, last ? 1 : 0, out};
+  if (launch_pdl(scatter_sum_kernel<W>, dim3(static_cast<unsigned>(S)), dim3(ScatterCfg<W>::THREADS), 0, st, p) !=
+      cudaSuccess)
+    return DSA_ERR_CUDA;
+  return last_launch_status();
+}
+
+// rank-3 map of [T, H, width] bf16 with boxes of 64 dims x 64 heads
+bool make_heads_map(CUtensorMap* m, const uint16_t* base, int T, int H, int width) {
+  const cuuint64_t d[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
+  const cuuint64_t s[2] = {static_cast<cuuint64_t>(width) * 2, static_cast<cuuint64_t>(H) * width * 2};
+  const cuuint32_t b[3] = {64, 64, 1};
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// rank-2 map of [rows, width] bf16 with boxes of 64 columns x box_rows
+bool make_rows_map(CUtensorMap* m, const uint16_t* base, long long rows, int width, int box_rows) {
+  const cuuint64_t d[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t s[1] = {static_cast<cuuint64_t>(width) * 2};
+  const cuuint32_t b[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Workspace of the attention's backward pass.
+struct AttnBwdWs {
+  int Tc, HP, kp;
+  ScatterWs sc;
+  float* delta;
+  uint16_t* pds;
+  size_t bytes;
+};
+AttnBwdWs attn_bwd_ws(void* ws, int T, int64_t S, int H, int k) {
+  AttnBwdWs a{};
+  a.HP = round_up(H, 64);
+  a.kp = round_up(k, 128);
+  a.Tc = bwd_chunk(T, S, a.kp, mbw::D * 2 + 4 * size_t(a.HP));
+  Carve w{static_cast<char*>(ws)};
+  a.sc = carve_scatter(w, a.Tc, S, k, a.kp, mbw::D, a.Tc < T);
+  a.delta = w.take<float>(size_t(a.Tc) * H);
+  a.pds = w.take<uint16_t>(size_t(a.Tc) * a.kp * 2 * a.HP);
+  a.bytes = w.at;
+  return a;
+}
+
+dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx, const uint16_t* out,
+                          const float* lse, const uint16_t* dout, int T, int H, int k, float scale, uint16_t* dq,
+                          uint16_t* dc, const AttnBwdWs& w, cudaStream_t st) {
+  CUtensorMap tq, tdo, tc, tp128, tp64, tout;
+  const size_t rows = size_t(w.Tc) * w.kp;
+  if (!make_heads_map(&tq, q, T, H, mbw::D) || !make_heads_map(&tdo, dout, T, H, mbw::DV) ||
+      !make_rows_map(&tc, c, S, mbw::D, 1) || !make_rows_map(&tp128, w.pds, rows, 2 * w.HP, 128) ||
+      !make_rows_map(&tp64, w.pds, rows, 2 * w.HP, 64) || !make_rows_map(&tout, w.sc.contrib, rows, mbw::D, 128))
+    return DSA_ERR_CUDA;
+  if (set_smem(mla_bwd_p_kernel<false>, mbw::p::Map<false>::SMEM) != cudaSuccess ||
+      set_smem(mla_bwd_dc_kernel, mbw::dc::SMEM) != cudaSuccess ||
+      set_smem(mla_bwd_dq_kernel, mbw::dq::SMEM) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  const int sms = num_sms();
+  for (int t0 = 0; t0 < T; t0 += w.Tc) {
+    const int n = std::min(w.Tc, T - t0);
+    const size_t o = static_cast<size_t>(t0);
+    MlaBwdParams p{};
+    p.idx = idx + o * k;
+    p.n_end = w.sc.n_end;
+    p.fill = w.sc.fill;
+    p.lse = lse + o * H;
+    p.delta = w.delta;
+    p.pds = w.pds;
+    p.dq = dq + o * H * mbw::D;
+    p.T = n;
+    p.t0 = t0;
+    p.H = H;
+    p.HP = w.HP;
+    p.k = k;
+    p.kp = w.kp;
+    p.S = S;
+    p.scale = scale;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    dsa_status_t e = scatter_begin(w.sc, p.idx, n, S, k, st);
+    if (e != DSA_OK) return e;
+    const long long dr = static_cast<long long>(n) * H;
+    if (launch_pdl(mla_bwd_delta_kernel, dim3(static_cast<unsigned>((dr + 7) / 8)), dim3(256), 0, st,
+                   dout + o * H * mbw::DV, out + o * H * mbw::DV, dr, w.delta) != cudaSuccess)
+      return DSA_ERR_CUDA;
+    if ((e = last_launch_status()) != DSA_OK) return e;
+    if (launch_pdl(mla_bwd_p_kernel<false>, dim3(std::min(sms, n * (w.HP / 64))), dim3(mbw::p::THREADS),
+                   mbw::p::Map<false>::SMEM, st, tq, tdo, tc, p) != cudaSuccess)
+      return DSA_ERR_CUDA;
+    if ((e = last_launch_status()) != DSA_OK) return e;
+    if (launch_pdl(mla_bwd_dc_kernel, dim3(std::min(sms, 3 * n)), dim3(mbw::dc::THREADS), mbw::dc::SMEM, st, tp128,
+                   tq, tdo, tout, p) != cudaSuccess)
+      return DSA_ERR_CUDA;
+    if ((e = last_launch_status()) != DSA_OK) return e;
+    if (launch_pdl(mla_bwd_dq_kernel, dim3(std::min(sms, 3 * n)), dim3(mbw::dq::THREADS), mbw::dq::SMEM, st, tp64, tc,
+                   p) != cudaSuccess)
+      return DSA_ERR_CUDA;
+    if ((e = last_launch_status()) != DSA_OK) return e;
+    e = scatter_end<mbw::D>(w.sc, n, S, k, w.kp, t0 == 0, t0 + n >= T, dc, st);
+    if (e != DSA_OK) return e;
+  }
+  return DSA_OK;
+}
+
+size_t kl_bwd_ws_bytes(int T) { return 2 * align_up(size_t(T) * 4, 256); }
+
+dsa_status_t run_kl_bwd(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx, const float* sel,
+                        const float* lse, const float* dkl, int T, int H, int k, float scale, float* dsel, void* ws,
+                        cudaStream_t st) {
+  CUtensorMap tq, tc;
+  if (!make_heads_map(&tq, q, T, H, mbw::D) || !make_rows_map(&tc, c, S, mbw::D, 1)) return DSA_ERR_CUDA;
+  Carve w{static_cast<char*>(ws)};
+  MlaBwdParams p{};
+  int* n_end = w.take<int>(T);
+  int* fill = w.take<int>(T);
+  p.idx = idx;
+  p.n_end = n_end;
+  p.fill = fill;
+  p.lse = lse;
+  p.T = T;
+  p.H = H;
+  p.HP = round_up(H, 64);
+  p.k = k;
+  p.kp = round_up(k, 128);
+  p.S = S;
+  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.sel = sel;
+  p.dkl = dkl;
+  p.dsel = dsel;
+  if (launch_pdl(scatter_build_kernel, dim3(T), dim3(256), 0, st, idx, k, static_cast<long long>(S), n_end, fill,
+                 nullptr, 0, nullptr) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  const dsa_status_t e = last_launch_status();
+  if (e != DSA_OK) return e;
+  if (set_smem(mla_bwd_p_kernel<true>, mbw::p::Map<true>::SMEM) != cudaSuccess) return DSA_ERR_CUDA;
+  if (launch_pdl(mla_bwd_p_kernel<true>, dim3(std::min(num_sms(), T)), dim3(mbw::p::THREADS),
+                 mbw::p::Map<true>::SMEM, st, tq, tq, tc, p) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  return last_launch_status();
 }
 
 }  // namespace
@@ -1290,6 +1494,43 @@ dsa_status_t dsa_forward_decode_noalloc(int B, const int64_t* cache_off, const i
   return dsa_forward_decode(B, cache_off, ctx_len, q_idx, q_scale, w, q, k_new, k_scale_new, c_new, k_cache,
                             k_scale_cache, c_cache, cache_rows, H_I, d_I, H, k, scale, idx_out, out, lse, scratch,
                             kNoAllocScratchBytes, stream);
+}
+
+size_t dsa_sparse_mla_attn_backward_workspace_size(int T, int S, int H, int k) {
+  if (T <= 0 || S <= 0 || H <= 0 || H > 128 || !mla_k_ok(k)) return 0;
+  return attn_bwd_ws(nullptr, T, S, H, k).bytes;
+}
+
+dsa_status_t dsa_sparse_mla_attn_backward(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx,
+                                          const uint16_t* out, const float* lse, const uint16_t* dout, int T, int H,
+                                          int k, float scale, uint16_t* dq, uint16_t* dc, void* ws, size_t ws_bytes,
+                                          void* stream) {
+  if (T < 0 || S <= 0 || H <= 0 || k <= 0 || !dc || (T > 0 && (!q || !c || !idx || !out || !lse || !dout || !dq)))
+    return DSA_ERR_INVALID_ARG;
+  if (H > 128 || !mla_k_ok(k)) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(q) || !aligned16(c) || !aligned16(idx) || !aligned16(out) || !aligned16(dout) || !aligned16(dq) ||
+      !aligned16(dc) || !aligned16(ws))
+    return DSA_ERR_ALIGNMENT;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0)
+    return cudaMemsetAsync(dc, 0, size_t(S) * mbw::D * 2, st) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  const AttnBwdWs w = attn_bwd_ws(ws, T, S, H, k);
+  if (!ws || ws_bytes < w.bytes) return DSA_ERR_WORKSPACE;
+  return run_attn_bwd(q, c, S, idx, out, lse, dout, T, H, k, scale, dq, dc, w, st);
+}
+
+size_t dsa_indexer_kl_backward_workspace_size(int T) { return T > 0 ? kl_bwd_ws_bytes(T) : 0; }
+
+dsa_status_t dsa_indexer_kl_backward(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx,
+                                     const float* sel_scores, const float* lse, const float* dkl, int T, int H, int k,
+                                     float scale, float* dsel, void* ws, size_t ws_bytes, void* stream) {
+  if (T < 0 || S <= 0 || H <= 0 || k <= 0 || (T > 0 && (!q || !c || !idx || !sel_scores || !lse || !dsel)))
+    return DSA_ERR_INVALID_ARG;
+  if (H > 128 || !mla_k_ok(k)) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(q) || !aligned16(c) || !aligned16(idx) || !aligned16(ws)) return DSA_ERR_ALIGNMENT;
+  if (T == 0) return DSA_OK;
+  if (!ws || ws_bytes < kl_bwd_ws_bytes(T)) return DSA_ERR_WORKSPACE;
+  return run_kl_bwd(q, c, S, idx, sel_scores, lse, dkl, T, H, k, scale, dsel, ws, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

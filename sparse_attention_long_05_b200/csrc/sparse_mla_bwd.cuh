@@ -1,0 +1,802 @@
+// Backward pass of the sparse MLA attention (sparse_mla.cuh) and the gradient of the indexer's objective.
+//
+// For token t, head h and selected entry i (row s = idx[t][i] of c), with the forward's out and lse:
+//   P  = exp(scale q_h . c_s - lse_h)            the probabilities, recomputed from q, c and lse
+//   dP = dout_h . c_s[:512]
+//   dS = scale P (dP - delta_h),  delta_h = dout_h . out_h
+//   dq_h = sum_i dS c_s                          dc_s = sum over (t, i) with idx[t][i] = s of
+//                                                       sum_h dS q_h + [sum_h P dout_h, 0 over the position dims]
+// Five products of 2 x 128 heads x 2048 entries x (576, 512, 576, 576, 512) per token: bound by the tensor cores.
+//
+// One SM cannot hold a token's q and dout (272 KB) beside its keys, nor dq's and dc's accumulators together (576 of
+// the 512 columns of tensor memory each), so the pass runs as three tensor-core kernels over a chunk of tokens, each
+// with a resident operand that fits, and P and dS (bf16, 1 MB a token) between them:
+//   mla_bwd_p_kernel   (token, 64 heads): keys are the M dimension; q and dout rows of the 64 heads, stacked to
+//                      N = 128, stay in shared memory; every gathered chunk of 128 keys x 64 dims meets both at once;
+//   mla_bwd_dc_kernel  (token, 192 dims): [dS | P] (128 keys x heads) times [q ; dout] (heads x 192 dims), resident;
+//                      writes each entry's own contribution to dc (bf16);
+//   mla_bwd_dq_kernel  (token, 192 dims): dS^T (heads x keys) times the gathered keys (keys x 192 dims), accumulated
+//                      over the token's keys in tensor memory.
+// A last kernel (scatter.cuh) sums the contributions of each row of c in token order: the result does not depend on
+// the order of execution, which atomics would not give.
+//
+// P, dS and the contributions are rounded to bf16, each by at most 2^-9 of its value: the operands of the second
+// products have to be bf16, and a sum of independently rounded contributions is off by no more than one of them is,
+// relative to the sum of their sizes (half the bf16 step that the results are rounded to anyway).  All sums are fp32.
+#pragma once
+#include "common.cuh"
+#include "sparse_mla.cuh"
+
+namespace dsa {
+
+struct MlaBwdParams {
+  const int* idx;              // [T, k] selections of the chunk's tokens
+  const int* n_end;            // [T] slots up to the token's last valid entry
+  const int* fill;             // [T] a row of c that the token selects (what its invalid slots read)
+  const float* lse;            // [T, H]
+  const float* delta;          // [T, H]
+  uint16_t* pds;               // [T * kp, 2 HP] bf16: dS of HP heads, then P of HP heads, for every slot
+  uint16_t* dq;                // [T, H, 576]
+  int T, t0;                   // tokens of the chunk; the first one's index in q and dout
+  int H, HP;                   // heads; heads rounded up to 64
+  int k, kp;                   // slots of a token; rounded up to 128
+  long long S;
+  float scale, scale_log2;
+  const float* sel;            // objective's gradient: index scores of the selected entries [T, k]
+  const float* dkl;            // [T] or null (1)
+  float* dsel;                 // [T, k]
+};
+
+// Instruction descriptor of bf16 operands, each K-major or MN-major (A: bit 15, B: bit 16).
+__host__ __device__ constexpr uint32_t idesc_bf16_major(int M, int N, bool a_mn, bool b_mn) {
+  return idesc_bf16(M, N, b_mn) | (a_mn ? 1u << 15 : 0u);
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
+               :: "l"(map), "r"(src), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// the committed stores have read their shared memory / have been written
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The threads of a named barrier agree on an outcome (all of them have to be true): the warps that meet at it leave
+// their loops together, so none is left waiting when a wait of another one runs out.
+__device__ __forceinline__ bool named_bar_all(int id, int nthreads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+      "bar.red.and.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r) : "r"(id), "r"(nthreads), "r"(static_cast<uint32_t>(v)) : "memory");
+  return r != 0;
+}
+
+namespace mbw {
+constexpr int NK = 128;                 // keys per tile (the M dimension of P and dC)
+constexpr int D = 576, DV = 512;
+constexpr int DCH = D / 64;             // 9 chunks of 64 dims
+constexpr int CHUNK = 128 * 128;        // 128 rows x 64 bf16
+constexpr int HCHUNK = 64 * 128;        // 64 rows x 64 bf16
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int BAR_BYTES = 1024;         // barriers, the tensor-memory address, the abort flag, small arrays
+constexpr int OFF_TMEM = 512, OFF_ABORT = 516;
+
+// ---- mla_bwd_p_kernel
+namespace p {
+constexpr int THREADS = 448, GATHER_WARPS = 8;
+constexpr int NS = 4;                   // ring stages of one gathered chunk (16 KB)
+constexpr int NACC = 4;                 // accumulators of 128 columns
+constexpr int B_IDX_FULL = 0, B_IDX_EMPTY = 2, B_RES_FULL = 4, B_RES_EMPTY = B_RES_FULL + DCH;
+constexpr int B_RING_FULL = B_RES_EMPTY + DCH, B_RING_EMPTY = B_RING_FULL + NS;
+constexpr int B_ACC_FULL = B_RING_EMPTY + NS, B_ACC_EMPTY = B_ACC_FULL + NACC;
+constexpr int B_COUNT = B_ACC_EMPTY + NACC;
+static_assert(B_COUNT * 8 <= OFF_TMEM, "barrier area");
+constexpr int OFF_HEADS = BAR_BYTES;                          // lse and delta of the item's heads, 2 buffers x 1 KB
+constexpr int OFF_IDX = OFF_HEADS + 2048;                     // 2 x 8 KB index rows
+constexpr int OFF_RED = OFF_IDX;                              // (objective: see IDXB)
+constexpr int RES_BYTES = DCH * CHUNK;                        // objective: 128 heads x 576; backward uses 8.5 chunks
+template <bool KL> struct Map {
+  // the objective's gradient keeps all 128 heads of q (144 KB) and has room for one index row
+  static constexpr int IDXB = KL ? 1 : 2;
+  static constexpr int RES = KL ? DCH * CHUNK : 8 * CHUNK + HCHUNK;
+  static constexpr int OFF_RES = (OFF_IDX + IDXB * mla::KMAX * 4 + 1023) / 1024 * 1024;
+  static constexpr int OFF_RING = OFF_RES + RES;
+  static constexpr int SMEM = OFF_RING + NS * CHUNK + 1024;
+};
+static_assert(Map<false>::SMEM <= 232448 && Map<true>::SMEM <= 232448, "shared memory per CTA");
+static_assert(Map<false>::OFF_RING % 1024 == 0 && Map<true>::OFF_RING % 1024 == 0, "1 KB aligned tiles");
+}  // namespace p
+
+// ---- mla_bwd_dc_kernel
+namespace dc {
+constexpr int THREADS = 256;
+constexpr int NS = 5;                   // ring stages of [dS | P]: 128 keys x 64 heads (16 KB)
+constexpr int UNIT = 3 * HCHUNK;        // resident operand of 64 heads: 64 heads x 192 dims (24 KB)
+constexpr int NU = 4;                   // units: q of heads 0..63, 64..127, dout of the same
+constexpr int B_RES_FULL = 0, B_RES_EMPTY = B_RES_FULL + NU, B_RING_FULL = B_RES_EMPTY + NU;
+constexpr int B_RING_EMPTY = B_RING_FULL + NS, B_ACC_FULL = B_RING_EMPTY + NS, B_ACC_EMPTY = B_ACC_FULL + 2;
+static_assert((B_ACC_EMPTY + 2) * 8 <= OFF_TMEM, "barrier area");
+constexpr int OFF_RES = BAR_BYTES, OFF_RING = OFF_RES + NU * UNIT, OFF_OUT = OFF_RING + NS * CHUNK;
+constexpr int SMEM = OFF_OUT + 3 * CHUNK + 1024;
+static_assert(SMEM <= 232448, "shared memory per CTA");
+}  // namespace dc
+
+// ---- mla_bwd_dq_kernel
+namespace dq {
+constexpr int THREADS = 448, GATHER_WARPS = 8;
+constexpr int KT = 64;                  // keys per stage
+constexpr int A_BYTES = 2 * HCHUNK, STAGE = A_BYTES + 3 * HCHUNK;   // dS: 64 keys x 128 heads; keys: 64 x 192 dims
+constexpr int NS = 4;
+constexpr int G4 = 3 * KT / 4;          // gather4 instructions per stage
+constexpr int B_IDX_FULL = 0, B_IDX_EMPTY = 2, B_RING_FULL = 4, B_RING_EMPTY = B_RING_FULL + NS;
+constexpr int B_ACC_FULL = B_RING_EMPTY + NS, B_ACC_EMPTY = B_ACC_FULL + 2;
+static_assert((B_ACC_EMPTY + 2) * 8 <= OFF_TMEM, "barrier area");
+constexpr int OFF_IDX = BAR_BYTES, OFF_RING = (OFF_IDX + 2 * mla::KMAX * 4 + 1023) / 1024 * 1024;
+constexpr int SMEM = OFF_RING + NS * STAGE + 1024;
+static_assert(SMEM <= 232448 && G4 % GATHER_WARPS == 0 && STAGE % 1024 == 0, "stage split");
+}  // namespace dq
+}  // namespace mbw
+
+// Shared start and end of the three kernels: barriers, tensor memory, launch order.
+struct BwdCta {
+  uint8_t* smem;
+  uint32_t sbase;
+  volatile int* abort_flag;
+  uint32_t tmem;
+  __device__ __forceinline__ uint32_t bar(int slot) const { return sbase + 8 * slot; }
+};
+__device__ __forceinline__ BwdCta bwd_base(uint8_t* raw) {
+  BwdCta c;
+  c.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  c.sbase = smem_u32(c.smem);
+  c.abort_flag = reinterpret_cast<volatile int*>(c.smem + mbw::OFF_ABORT);
+  c.tmem = 0;
+  return c;
+}
+// after the barriers are initialised by thread 0: tensor memory by warp 1, then the predecessor's results
+__device__ __forceinline__ void bwd_begin(BwdCta& c) {
+  if (threadIdx.x == 0) {
+    *c.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp_id() == 1) {
+    tmem_alloc(c.sbase + mbw::OFF_TMEM, mbw::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  c.tmem = *reinterpret_cast<volatile uint32_t*>(c.smem + mbw::OFF_TMEM);
+  pdl_allow_next();
+  pdl_wait();
+}
+__device__ __forceinline__ void bwd_end(BwdCta& c) {
+  tc_fence_before();
+  __syncthreads();
+  if (warp_id() == 1) {
+    tc_fence_after();
+    tmem_dealloc(c.tmem, mbw::TMEM_COLS);
+  }
+}
+
+// Row of c read for slot `slot` of a token: its entry, or the token's fill row for an empty or invalid one (its dS
+// and P are zero; a row of the token's own cannot bring in a NaN that the token does not already see).
+__device__ __forceinline__ int bwd_row(const MlaBwdParams& p, const int* ids, int slot, int fill) {
+  const int e = slot < p.k ? ids[slot] : -1;
+  return (e >= 0 && e < p.S) ? e : fill;
+}
+
+// P and dS of one (token, 64 heads) per item, or (KL) the gradient of the objective of one token per item.
+//
+// M = 128 keys, N = 128: columns 0..63 are S^T and 64..127 dP^T of the 64 heads (KL: S^T of all heads, N = HP).  The
+// resident operand is released chunk by chunk during the last tile, so the next item's loads overlap it.
+template <bool KL>
+__global__ void __launch_bounds__(mbw::p::THREADS, 1)
+mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                 const __grid_constant__ CUtensorMap tm_c, const MlaBwdParams p) {
+  using namespace mbw;
+  using namespace mbw::p;
+  using M = Map<KL>;
+  extern __shared__ uint8_t smem_raw[];
+  BwdCta cta = bwd_base(smem_raw);
+  const uint32_t sbase = cta.sbase;
+  volatile int* abort_flag = cta.abort_flag;
+  const int warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(cta.bar(B_IDX_FULL + i), 1);
+      mbar_init(cta.bar(B_IDX_EMPTY + i), GATHER_WARPS + 4);
+    }
+    for (int i = 0; i < DCH; ++i) { mbar_init(cta.bar(B_RES_FULL + i), 1); mbar_init(cta.bar(B_RES_EMPTY + i), 1); }
+    for (int i = 0; i < NS; ++i) { mbar_init(cta.bar(B_RING_FULL + i), 2); mbar_init(cta.bar(B_RING_EMPTY + i), 1); }
+    for (int i = 0; i < NACC; ++i) { mbar_init(cta.bar(B_ACC_FULL + i), 1); mbar_init(cta.bar(B_ACC_EMPTY + i), 4); }
+  }
+  bwd_begin(cta);
+  const uint32_t tmem = cta.tmem;
+  const uint32_t res = sbase + M::OFF_RES, ring = sbase + M::OFF_RING;
+  const int halves = KL ? 1 : p.HP / 64;
+  const int items = p.T * halves;
+  bool ok = true;
+  int n = 0;                              // items with at least one tile, walked so far
+
+  if (warp == 0) {
+    // ===================================================================== loader: index rows, q and dout rows
+    if (lane == 0) {
+      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        const int t = item / halves, hf = item % halves;
+        if (p.n_end[t] <= 0) continue;
+        const int ib = n % M::IDXB;
+        if (!(ok = mbar_wait(cta.bar(B_IDX_EMPTY + ib), ((n / M::IDXB) & 1) ^ 1, abort_flag))) break;
+        mbar_arrive_expect_tx(cta.bar(B_IDX_FULL + ib), p.k * 4);
+        bulk_load(sbase + OFF_IDX + ib * mla::KMAX * 4, p.idx + static_cast<long long>(t) * p.k, p.k * 4,
+                  cta.bar(B_IDX_FULL + ib));
+        for (int c = 0; c < DCH; ++c) {
+          if (!(ok = mbar_wait(cta.bar(B_RES_EMPTY + c), (n & 1) ^ 1, abort_flag))) break;
+          const uint32_t dst = res + c * CHUNK, full = cta.bar(B_RES_FULL + c);
+          if constexpr (KL) {
+            mbar_arrive_expect_tx(full, (p.HP / 64) * HCHUNK);
+            for (int i = 0; i < p.HP / 64; ++i) tma_load_3d(dst + i * HCHUNK, &tm_q, full, 64 * c, 64 * i, p.t0 + t);
+          } else {
+            mbar_arrive_expect_tx(full, c < 8 ? CHUNK : HCHUNK);
+            tma_load_3d(dst, &tm_q, full, 64 * c, 64 * hf, p.t0 + t);
+            if (c < 8) tma_load_3d(dst + HCHUNK, &tm_do, full, 64 * c, 64 * hf, p.t0 + t);
+          }
+        }
+        ++n;
+      }
+      if (*abort_flag && n > 0) {          // leave no load in flight into this CTA's shared memory
+        for (int i = 0; i < M::IDXB; ++i) mbar_wait_drain(cta.bar(B_IDX_FULL + i), ((n - 1) / M::IDXB) & 1);
+        for (int c = 0; c < DCH; ++c) mbar_wait_drain(cta.bar(B_RES_FULL + c), (n - 1) & 1);
+      }
+    }
+  } else if (warp == 2 || warp == 3 || warp >= 8) {
+    // ===================================================================== gathers
+    // Two warps share a ring stage (64 rows each, one gather4 of four rows per lane): with a stage of its own, a
+    // warp meets the stage's barriers once per 64 KB of the CTA's traffic.
+    const int gw = (warp < 8) ? warp - 2 : warp - 6;
+    const int st = gw >> 1, rg = (gw & 1) * 16 + lane;
+    int m = 0;                             // chunks gathered by the CTA before this tile
+    uint32_t uses = 0;                     // chunks this warp has gathered
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const int t = item / halves, tiles = (p.n_end[t] + NK - 1) / NK;
+      if (tiles <= 0) continue;
+      const int ib = n % M::IDXB, fill = p.fill[t];
+      if (!(ok = warp_wait(cta.bar(B_IDX_FULL + ib), (n / M::IDXB) & 1, abort_flag))) break;
+      const int* ids = reinterpret_cast<const int*>(cta.smem + OFF_IDX + ib * mla::KMAX * 4);
+      for (int j = 0; j < tiles && ok; ++j, m += DCH) {
+        int r[4] = {0, 0, 0, 0};
+        if (lane < 16) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) r[u] = bwd_row(p, ids, j * NK + 4 * rg + u, fill);
+        }
+        for (int c = (st - m % NS + NS) % NS; c < DCH; c += NS) {
+          bool got = true;
+          if (lane == 0) {
+            got = mbar_wait(cta.bar(B_RING_EMPTY + st), (uses & 1) ^ 1, abort_flag);
+            if (got) mbar_arrive_expect_tx(cta.bar(B_RING_FULL + st), 64 * 128);
+          }
+          if (!(ok = __shfl_sync(0xffffffffu, got, 0))) break;
+          if (lane < 16)
+            tma_gather4(ring + st * CHUNK + rg * 512, &tm_c, cta.bar(B_RING_FULL + st), 64 * c, r[0], r[1], r[2], r[3]);
+          ++uses;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(cta.bar(B_IDX_EMPTY + ib));
+      ++n;
+    }
+    if (lane == 0 && *abort_flag && uses > 0) mbar_wait_drain(cta.bar(B_RING_FULL + st), (uses - 1) & 1);
+  } else if (warp == 1) {
+    // ===================================================================== MMA issue
+    Pipe<NS> rp;
+    int g = 0;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const int t = item / halves, tiles = (p.n_end[t] + NK - 1) / NK;
+      if (tiles <= 0) continue;
+      for (int j = 0; j < tiles && ok; ++j, ++g) {
+        const int ab = g % NACC;
+        if (!(ok = warp_wait(cta.bar(B_ACC_EMPTY + ab), ((g / NACC) & 1) ^ 1, abort_flag))) break;
+        tc_fence_after();
+        for (int c = 0; c < DCH; ++c, rp.advance()) {
+          if (j == 0 && !(ok = warp_wait(cta.bar(B_RES_FULL + c), n & 1, abort_flag))) break;
+          if (!(ok = warp_wait(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
+          tc_fence_after();
+          const uint64_t ad = smem_desc(ring + rp.stage * CHUNK, 16, 1024, kLayoutSW128);
+          const uint64_t bd = smem_desc(res + c * CHUNK, 16, 1024, kLayoutSW128);
+          const uint32_t idesc = KL ? idesc_bf16(128, p.HP, false) : idesc_bf16(128, c < 8 ? 128 : 64, false);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_ss(tmem + 128 * ab, ad + 2 * k, bd + 2 * k, idesc, (c | k) ? 1u : 0u);
+            mma_commit(cta.bar(B_RING_EMPTY + rp.stage));
+            if (j == tiles - 1) mma_commit(cta.bar(B_RES_EMPTY + c));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) mma_commit(cta.bar(B_ACC_FULL + ab));
+        __syncwarp();
+      }
+      ++n;
+    }
+  } else {
+    // ===================================================================== probabilities (warps 4..7, one key a thread)
+    const int quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+    constexpr float kLog2e = 1.4426950408889634f;
+    int g = 0, heads_at = 0;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const int t = item / halves, hf = item % halves, tiles = (p.n_end[t] + NK - 1) / NK;
+      if constexpr (KL) {
+        for (int i = tiles * NK + row; i < p.k; i += NK) p.dsel[static_cast<long long>(t) * p.k + i] = 0.f;
+      }
+      if (tiles <= 0) continue;
+      const int ib = n % M::IDXB;
+      // the item's lse (in log2 units) and delta, or KL: the lse of all heads.  A head without any probability mass
+      // (lse = -inf) and the heads that only fill up the tile get +inf: P = 0.
+      float* hs = reinterpret_cast<float*>(cta.smem + OFF_HEADS) + heads_at * 256;
+      heads_at ^= 1;
+      {
+        const int h = KL ? row : 64 * hf + (row & 63);
+        float v = KL || row < 64 ? INFINITY : 0.f;
+        if (h < p.H) {
+          const long long at = static_cast<long long>(t) * p.H + h;
+          if (KL || row < 64) {
+            const float l = p.lse[at];
+            v = l == -INFINITY ? INFINITY : l * kLog2e;
+          } else {
+            v = p.delta[at];
+          }
+        }
+        hs[row] = v;
+      }
+      ok = warp_wait(cta.bar(B_IDX_FULL + ib), (n / M::IDXB) & 1, abort_flag);
+      if (!(ok = named_bar_all(1, 128, ok))) break;
+      const int* ids = reinterpret_cast<const int*>(cta.smem + OFF_IDX + ib * mla::KMAX * 4);
+      [[maybe_unused]] float m_i = -INFINITY, z_i = 0.f, s_a = 0.f;
+      for (int j = 0; j < tiles; ++j, ++g) {
+        const int ab = g % NACC, slot = j * NK + row;
+        const int e = slot < p.k ? ids[slot] : -1;
+        const bool valid = e >= 0 && e < p.S;
+        if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), (g / NACC) & 1, abort_flag))) break;
+        tc_fence_after();
+        const uint32_t acc = lane_addr + tmem + 128 * ab;
+        if constexpr (KL) {
+          float a0 = 0.f, a1 = 0.f;
+          for (int c = 0; c < p.HP / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld32(acc + 32 * c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              a0 += ex2_approx(fmaf(__uint_as_float(v[i]), p.scale_log2, -hs[32 * c + i]));
+              a1 += ex2_approx(fmaf(__uint_as_float(v[i + 1]), p.scale_log2, -hs[32 * c + i + 1]));
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(cta.bar(B_ACC_EMPTY + ab));
+          if (slot < p.k) {
+            const long long at = static_cast<long long>(t) * p.k + slot;
+            const float a = valid ? a0 + a1 : 0.f;
+            p.dsel[at] = a;                // the same thread reads it back below
+            if (valid) {
+              const float x = p.sel[at];
+              s_a += a;
+              if (x > m_i) {
+                z_i = z_i * ex2_approx((m_i - x) * kLog2e) + 1.f;
+                m_i = x;
+              } else if (x > -INFINITY) {
+                z_i += ex2_approx((x - m_i) * kLog2e);
+              }
+            }
+          }
+        } else {
+          uint16_t* out = p.pds + (static_cast<long long>(t) * p.kp + slot) * (2 * p.HP) + 64 * hf;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t s[32], d[32];
+            tmem_ld32(acc + 32 * c, s);
+            tmem_ld32(acc + 64 + 32 * c, d);
+            tmem_wait_ld();
+            if (c == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(cta.bar(B_ACC_EMPTY + ab));
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float pr = ex2_approx(fmaf(__uint_as_float(s[i]), p.scale_log2, -hs[32 * c + i]));
+              const float ds = pr * (__uint_as_float(d[i]) - hs[64 + 32 * c + i]) * p.scale;
+              s[i] = __float_as_uint(valid ? pr : 0.f);
+              d[i] = __float_as_uint(valid ? ds : 0.f);
+            }
+            uint4* ds4 = reinterpret_cast<uint4*>(out + 32 * c);
+            uint4* p4 = reinterpret_cast<uint4*>(out + p.HP + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              auto pk = [&](const uint32_t (&v)[32], int q) {
+                return pack_bf16(__uint_as_float(v[8 * i + 2 * q]), __uint_as_float(v[8 * i + 2 * q + 1]));
+              };
+              ds4[i] = make_uint4(pk(d, 0), pk(d, 1), pk(d, 2), pk(d, 3));
+              p4[i] = make_uint4(pk(s, 0), pk(s, 1), pk(s, 2), pk(s, 3));
+            }
+          }
+        }
+      }
+      if (!(ok = named_bar_all(1, 128, ok))) break;
+      if (lane == 0) mbar_arrive(cta.bar(B_IDX_EMPTY + ib));
+      if constexpr (KL) {
+        // the token's sums over its 128 threads, then g (softmax(I) - p) for each slot
+        float mm = m_i;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+        float* rs = hs + 128;              // [4 warps][max, sum of exp, sum of a]
+        float z = m_i == -INFINITY ? 0.f : z_i * ex2_approx((m_i - mm) * kLog2e);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+          z += __shfl_xor_sync(0xffffffffu, z, d);
+          s_a += __shfl_xor_sync(0xffffffffu, s_a, d);
+        }
+        if (lane == 0) { rs[3 * quad] = mm; rs[3 * quad + 1] = z; rs[3 * quad + 2] = s_a; }
+        named_bar_sync(1, 128);
+        const float m_all = fmaxf(fmaxf(rs[0], rs[3]), fmaxf(rs[6], rs[9]));
+        float z_all = 0.f, a_all = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          if (rs[3 * w] > -INFINITY) z_all += rs[3 * w + 1] * ex2_approx((rs[3 * w] - m_all) * kLog2e);
+          a_all += rs[3 * w + 2];
+        }
+        const float up = p.dkl ? p.dkl[t] : 1.f;
+        const float iz = z_all > 0.f ? 1.f / z_all : 0.f, ia = a_all > 0.f ? 1.f / a_all : 0.f;
+        for (int i = row; i < min(tiles * NK, p.k); i += NK) {
+          const long long at = static_cast<long long>(t) * p.k + i;
+          // reading the entry again decides validity as above (its index row may have been replaced by now)
+          const int e = p.idx[at];
+          const float x = p.sel[at];
+          const float soft = x > -INFINITY ? ex2_approx((x - m_all) * kLog2e) * iz : 0.f;
+          p.dsel[at] = (e >= 0 && e < p.S) ? up * (soft - p.dsel[at] * ia) : 0.f;
+        }
+      }
+      ++n;
+    }
+  }
+  bwd_end(cta);
+}
+
+// Contributions to dc: out[t kp + slot][d] = sum_h dS q[t][h][d] + P dout[t][h][d] for 192 dims d per item.
+__global__ void __launch_bounds__(mbw::dc::THREADS, 1)
+mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_constant__ CUtensorMap tm_q,
+                  const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_out,
+                  const MlaBwdParams p) {
+  using namespace mbw;
+  using namespace mbw::dc;
+  extern __shared__ uint8_t smem_raw[];
+  BwdCta cta = bwd_base(smem_raw);
+  const uint32_t sbase = cta.sbase;
+  volatile int* abort_flag = cta.abort_flag;
+  const int warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NU; ++i) { mbar_init(cta.bar(B_RES_FULL + i), 1); mbar_init(cta.bar(B_RES_EMPTY + i), 1); }
+    for (int i = 0; i < NS; ++i) { mbar_init(cta.bar(B_RING_FULL + i), 1); mbar_init(cta.bar(B_RING_EMPTY + i), 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(cta.bar(B_ACC_FULL + i), 1); mbar_init(cta.bar(B_ACC_EMPTY + i), 4); }
+  }
+  bwd_begin(cta);
+  const uint32_t tmem = cta.tmem;
+  const uint32_t res = sbase + OFF_RES, ring = sbase + OFF_RING;
+  const int hb = p.HP / 64, units = 2 * hb;        // 64-head blocks of dS, then of P
+  const int items = 3 * p.T;
+  bool ok = true;
+  int n = 0;
+
+  if (warp == 0) {
+    // ===================================================================== resident q and dout
+    if (lane == 0) {
+      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        const int t = item / 3, d3 = item % 3;
+        if (p.n_end[t] <= 0) continue;
+        for (int u = 0; u < units; ++u) {
+          if (!(ok = mbar_wait(cta.bar(B_RES_EMPTY + u), (n & 1) ^ 1, abort_flag))) break;
+          const int boxes = (u >= hb && d3 == 2) ? 2 : 3;          // dout ends at dim 512
+          const uint32_t full = cta.bar(B_RES_FULL + u);
+          mbar_arrive_expect_tx(full, boxes * HCHUNK);
+          for (int i = 0; i < boxes; ++i)
+            tma_load_3d(res + u * UNIT + i * HCHUNK, u < hb ? &tm_q : &tm_do, full, 192 * d3 + 64 * i, 64 * (u % hb),
+                        p.t0 + t);
+        }
+        ++n;
+      }
+      if (*abort_flag && n > 0)
+        for (int u = 0; u < units; ++u) mbar_wait_drain(cta.bar(B_RES_FULL + u), (n - 1) & 1);
+    }
+  } else if (warp == 2) {
+    // ===================================================================== dS and P tiles
+    if (lane == 0) {
+      Pipe<NS> rp;
+      int issued = 0;
+      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        const int t = item / 3, tiles = (p.n_end[t] + NK - 1) / NK;
+        for (int i = 0; i < tiles * units; ++i, rp.advance(), ++issued) {
+          if (!(ok = mbar_wait(cta.bar(B_RING_EMPTY + rp.stage), rp.phase ^ 1, abort_flag))) break;
+          mbar_arrive_expect_tx(cta.bar(B_RING_FULL + rp.stage), CHUNK);
+          tma_load_2d(ring + rp.stage * CHUNK, &tm_pds, cta.bar(B_RING_FULL + rp.stage), 64 * (i % units),
+                      t * p.kp + (i / units) * NK);
+        }
+      }
+      if (*abort_flag)
+        for (int i = max(0, issued - NS); i < issued; ++i)
+          mbar_wait_drain(cta.bar(B_RING_FULL + i % NS), (i / NS) & 1);
+    }
+  } else if (warp == 1) {
+    // ===================================================================== MMA issue
+    Pipe<NS> rp;
+    int g = 0;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const int t = item / 3, d3 = item % 3, tiles = (p.n_end[t] + NK - 1) / NK;
+      if (tiles <= 0) continue;
+      for (int j = 0; j < tiles && ok; ++j, ++g) {
+        const int ab = g & 1;
+        if (!(ok = warp_wait(cta.bar(B_ACC_EMPTY + ab), ((g >> 1) & 1) ^ 1, abort_flag))) break;
+        tc_fence_after();
+        for (int u = 0; u < units; ++u, rp.advance()) {
+          if (j == 0 && !(ok = warp_wait(cta.bar(B_RES_FULL + u), n & 1, abort_flag))) break;
+          if (!(ok = warp_wait(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
+          tc_fence_after();
+          const uint64_t ad = smem_desc(ring + rp.stage * CHUNK, 16, 1024, kLayoutSW128);
+          // heads x dims, dims contiguous (MN-major): 64-dim atoms 8 KB apart, 8-head groups 1 KB apart
+          const uint64_t bd = smem_desc(res + u * UNIT, HCHUNK, 1024, kLayoutSW128);
+          const uint32_t idesc = idesc_bf16(128, (u >= hb && d3 == 2) ? 128 : 192, true);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_ss(tmem + 256 * ab, ad + 2 * k, bd + ((k * 2048) >> 4), idesc, (u | k) ? 1u : 0u);
+            mma_commit(cta.bar(B_RING_EMPTY + rp.stage));
+            if (j == tiles - 1) mma_commit(cta.bar(B_RES_EMPTY + u));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) mma_commit(cta.bar(B_ACC_FULL + ab));
+        __syncwarp();
+      }
+      ++n;
+    }
+  } else if (warp >= 4) {
+    // ===================================================================== contributions out (one key a thread)
+    const int quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+    int g = 0;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const int t = item / 3, d3 = item % 3, tiles = (p.n_end[t] + NK - 1) / NK;
+      for (int j = 0; j < tiles; ++j, ++g) {
+        const int ab = g & 1;
+        // the previous tile's stores have read the staging area
+        if (warp == 4 && lane == 0) bulk_wait_read();
+        ok = warp_wait(cta.bar(B_ACC_FULL + ab), (g >> 1) & 1, abort_flag);
+        if (!(ok = named_bar_all(1, 128, ok))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 6; ++c) {
+          uint32_t v[32];
+          tmem_ld32(lane_addr + tmem + 256 * ab + 32 * c, v);
+          tmem_wait_ld();
+          if (c == 5) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(cta.bar(B_ACC_EMPTY + ab));
+          }
+          // 128-byte swizzled rows of 64 dims: 16-byte unit u of row r at unit u ^ (r % 8)
+          uint8_t* line = cta.smem + OFF_OUT + (c >> 1) * CHUNK + row * 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            auto pk = [&](int q) { return pack_bf16(__uint_as_float(v[8 * i + 2 * q]), __uint_as_float(v[8 * i + 2 * q + 1])); };
+            *reinterpret_cast<uint4*>(line + (((4 * (c & 1) + i) ^ (row & 7)) << 4)) =
+                make_uint4(pk(0), pk(1), pk(2), pk(3));
+          }
+        }
+        fence_proxy_async_smem();
+        named_bar_sync(1, 128);
+        if (warp == 4 && lane == 0) {
+          for (int c = 0; c < 3; ++c)
+            tma_store_2d(&tm_out, sbase + OFF_OUT + c * CHUNK, 192 * d3 + 64 * c, t * p.kp + j * NK);
+          bulk_commit();
+        }
+      }
+    }
+    if (warp == 4 && lane == 0) bulk_wait_all();
+  }
+  bwd_end(cta);
+}
+
+// dq[t][:, 192 dims] = dS^T . C per item, accumulated over the token's keys in tensor memory (lane = head).
+__global__ void __launch_bounds__(mbw::dq::THREADS, 1)
+mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const __grid_constant__ CUtensorMap tm_c,
+                  const MlaBwdParams p) {
+  using namespace mbw;
+  using namespace mbw::dq;
+  extern __shared__ uint8_t smem_raw[];
+  BwdCta cta = bwd_base(smem_raw);
+  const uint32_t sbase = cta.sbase;
+  volatile int* abort_flag = cta.abort_flag;
+  const int warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(cta.bar(B_IDX_FULL + i), 1);
+      mbar_init(cta.bar(B_IDX_EMPTY + i), GATHER_WARPS);
+      mbar_init(cta.bar(B_ACC_FULL + i), 1);
+      mbar_init(cta.bar(B_ACC_EMPTY + i), 4);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(cta.bar(B_RING_FULL + i), GATHER_WARPS + 1);
+      mbar_init(cta.bar(B_RING_EMPTY + i), 1);
+    }
+  }
+  bwd_begin(cta);
+  const uint32_t tmem = cta.tmem;
+  const uint32_t ring = sbase + OFF_RING;
+  const int items = 3 * p.T;
+  bool ok = true;
+  int n = 0;
+
+  if (warp == 0) {
+    // ===================================================================== index rows and dS tiles
+    if (lane == 0) {
+      Pipe<NS> rp;
+      int issued = 0;
+      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        const int t = item / 3, tiles = (p.n_end[t] + KT - 1) / KT;
+        if (tiles <= 0) continue;
+        const int ib = n & 1;
+        if (!(ok = mbar_wait(cta.bar(B_IDX_EMPTY + ib), ((n >> 1) & 1) ^ 1, abort_flag))) break;
+        mbar_arrive_expect_tx(cta.bar(B_IDX_FULL + ib), p.k * 4);
+        bulk_load(sbase + OFF_IDX + ib * mla::KMAX * 4, p.idx + static_cast<long long>(t) * p.k, p.k * 4,
+                  cta.bar(B_IDX_FULL + ib));
+        ++n;
+        for (int j = 0; j < tiles; ++j, rp.advance(), ++issued) {
+          if (!(ok = mbar_wait(cta.bar(B_RING_EMPTY + rp.stage), rp.phase ^ 1, abort_flag))) break;
+          const uint32_t full = cta.bar(B_RING_FULL + rp.stage), dst = ring + rp.stage * STAGE;
+          mbar_arrive_expect_tx(full, A_BYTES);
+          for (int i = 0; i < 2; ++i)      // HP = 64: the second block is P's columns, its products are not stored
+            tma_load_2d(dst + i * HCHUNK, &tm_ds, full, 64 * i, t * p.kp + j * KT);
+        }
+      }
+      if (*abort_flag) {
+        if (n > 0) mbar_wait_drain(cta.bar(B_IDX_FULL + ((n - 1) & 1)), ((n - 1) >> 1) & 1);
+        for (int i = max(0, issued - NS); i < issued; ++i)
+          mbar_wait_drain(cta.bar(B_RING_FULL + i % NS), (i / NS) & 1);
+      }
+    }
+  } else if (warp == 2 || warp == 3 || warp >= 8) {
+    // ===================================================================== gathers
+    const int gw = (warp < 8) ? warp - 2 : warp - 6;
+    constexpr int kPer = G4 / GATHER_WARPS;                  // 6 gather4 a warp and stage
+    const int gi = gw * kPer + lane, cc = gi / (KT / 4), rg = gi % (KT / 4);
+    const bool active = lane < kPer;
+    Pipe<NS> rp;
+    int issued = 0;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const int t = item / 3, d3 = item % 3, tiles = (p.n_end[t] + KT - 1) / KT;
+      if (tiles <= 0) continue;
+      const int ib = n & 1, fill = p.fill[t];
+      if (!(ok = warp_wait(cta.bar(B_IDX_FULL + ib), (n >> 1) & 1, abort_flag))) break;
+      const int* ids = reinterpret_cast<const int*>(cta.smem + OFF_IDX + ib * mla::KMAX * 4);
+      for (int j = 0; j < tiles; ++j, rp.advance(), ++issued) {
+        int r[4] = {0, 0, 0, 0};
+        if (active) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) r[u] = bwd_row(p, ids, j * KT + 4 * rg + u, fill);
+        }
+        bool got = true;
+        if (lane == 0) {
+          got = mbar_wait(cta.bar(B_RING_EMPTY + rp.stage), rp.phase ^ 1, abort_flag);
+          if (got) mbar_arrive_expect_tx(cta.bar(B_RING_FULL + rp.stage), kPer * 512);
+        }
+        if (!(ok = __shfl_sync(0xffffffffu, got, 0))) break;
+        if (active)
+          tma_gather4(ring + rp.stage * STAGE + A_BYTES + cc * HCHUNK + rg * 512, &tm_c,
+                      cta.bar(B_RING_FULL + rp.stage), 192 * d3 + 64 * cc, r[0], r[1], r[2], r[3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(cta.bar(B_IDX_EMPTY + ib));
+      ++n;
+    }
+    if (lane == 0 && *abort_flag)
+      for (int i = max(0, issued - NS); i < issued; ++i)
+        mbar_wait_drain(cta.bar(B_RING_FULL + i % NS), (i / NS) & 1);
+  } else if (warp == 1) {
+    // ===================================================================== MMA issue
+    Pipe<NS> rp;
+    constexpr uint32_t idesc = idesc_bf16_major(128, 192, true, true);
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const int t = item / 3, tiles = (p.n_end[t] + KT - 1) / KT;
+      if (tiles <= 0) continue;
+      const int ab = n & 1;
+      if (!(ok = warp_wait(cta.bar(B_ACC_EMPTY + ab), ((n >> 1) & 1) ^ 1, abort_flag))) break;
+      tc_fence_after();
+      for (int j = 0; j < tiles; ++j, rp.advance()) {
+        if (!(ok = warp_wait(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
+        tc_fence_after();
+        const uint32_t at = ring + rp.stage * STAGE;
+        const uint64_t ad = smem_desc(at, HCHUNK, 1024, kLayoutSW128);
+        const uint64_t bd = smem_desc(at + A_BYTES, HCHUNK, 1024, kLayoutSW128);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k)
+            mma_bf16_ss(tmem + 256 * ab, ad + ((k * 2048) >> 4), bd + ((k * 2048) >> 4), idesc, (j | k) ? 1u : 0u);
+          mma_commit(cta.bar(B_RING_EMPTY + rp.stage));
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (elect_one()) mma_commit(cta.bar(B_ACC_FULL + ab));
+      __syncwarp();
+      ++n;
+    }
+  } else {
+    // ===================================================================== dq out (one head a thread)
+    const int quad = warp & 3, h = quad * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const int t = item / 3, d3 = item % 3;
+      uint4* dst = reinterpret_cast<uint4*>(p.dq + (static_cast<long long>(t) * p.H + h) * D + 192 * d3);
+      if (p.n_end[t] <= 0) {               // nothing selected: dq = 0
+        if (h < p.H)
+          for (int i = 0; i < 24; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      const int ab = n & 1;
+      if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), (n >> 1) & 1, abort_flag))) break;
+      tc_fence_after();
+      for (int c = 0; c < 6; ++c) {
+        uint32_t v[32];
+        tmem_ld32(lane_addr + tmem + 256 * ab + 32 * c, v);
+        tmem_wait_ld();
+        if (h < p.H) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            auto pk = [&](int q) { return pack_bf16(__uint_as_float(v[8 * i + 2 * q]), __uint_as_float(v[8 * i + 2 * q + 1])); };
+            dst[4 * c + i] = make_uint4(pk(0), pk(1), pk(2), pk(3));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(cta.bar(B_ACC_EMPTY + ab));
+      ++n;
+    }
+  }
+  bwd_end(cta);
+}
+
+// delta[t][h] = dout . out over the 512 value dims, one warp a row.
+__global__ void __launch_bounds__(256) mla_bwd_delta_kernel(const uint16_t* dout, const uint16_t* out, long long rows,
+                                                            float* delta) {
+  pdl_allow_next();
+  pdl_wait();
+  const long long r = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  if (r >= rows) return;
+  const uint4* a = reinterpret_cast<const uint4*>(dout + r * mbw::DV);
+  const uint4* b = reinterpret_cast<const uint4*>(out + r * mbw::DV);
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 x = a[lane_id() + 32 * i], y = b[lane_id() + 32 * i];
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      s = fmaf(__uint_as_float(xs[u] << 16), __uint_as_float(ys[u] << 16), s);
+      s = fmaf(__uint_as_float(xs[u] & 0xffff0000u), __uint_as_float(ys[u] & 0xffff0000u), s);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if (lane_id() == 0) delta[r] = s;
+}
+
+}  // namespace dsa
