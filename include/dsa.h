@@ -195,6 +195,66 @@ DSA_API dsa_status_t dsa_indexer_kl_backward(const uint16_t* q, const uint16_t* 
                                              const float* sel_scores, const float* lse, const float* dkl, int T, int H,
                                              int k, float scale, float* dsel, void* ws, size_t ws_bytes, void* stream);
 
+/* Workspace bytes of dsa_indexer_scores_backward (0 for unsupported shapes). */
+DSA_API size_t dsa_indexer_scores_backward_workspace_size(int T, int S, int H_I, int d_I, int k);
+
+/*
+ * Backward pass of the index scores (velog.io section 1.1) at the selected entries: from the gradient dsel of
+ * I[t, idx[t][i]] = sum_j w_j ReLU(q_j . k_s), with q_j and k_s the dequantised operands,
+ *   dw[t,j] = sum_i dsel ReLU(q_j . k_s)      dq[t,j] = sum_i dsel w_j 1[q_j . k_s > 0] k_s
+ *   dk[s] = sum over the (t, j, i) with idx[t][i] = s of dsel w_j 1[q_j . k_s > 0] q_j.
+ * dq and dk are the gradients of the dequantised values: what reaches the values before the quantisation when that is
+ * taken as the identity.  Scales and indices get no gradient.
+ *   q_idx [T, H_I, d_I] e4m3, q_scale [T] or NULL, k_idx [S, d_I] e4m3, k_scale [S] or NULL, w [T, H_I] fp32: the
+ *     forward's inputs; idx [T, k] int32 and dsel [T, k] fp32: the selection and the gradient of its scores (ignored
+ *     where idx is -1), as dsa_indexer_kl_backward writes it;
+ *   dq [T, H_I, d_I] bf16, dk [S, d_I] bf16, dw [T, H_I] fp32 (out); every row is written.
+ * k as in dsa_sparse_mla_attn; entries outside [-1, S) count as -1 and are recorded as DSA_ERR_BAD_INDEX.  The weights
+ * dsel w_j (and their product with k_scale) and each entry's contribution to dk are rounded to bf16 once; sums are fp32.
+ *   ws: dsa_indexer_scores_backward_workspace_size() bytes, 16-byte aligned.
+ */
+DSA_API dsa_status_t dsa_indexer_scores_backward(const uint8_t* q_idx, const float* q_scale, const uint8_t* k_idx,
+                                                 const float* k_scale, const float* w, const int32_t* idx,
+                                                 const float* dsel, int T, int S, int H_I, int d_I, int k,
+                                                 uint16_t* dq, uint16_t* dk, float* dw, void* ws, size_t ws_bytes,
+                                                 void* stream);
+
+/* Element types of dsa_rope. */
+enum { DSA_BF16 = 0, DSA_FP32 = 1 };
+
+/*
+ * Rotation per position of each pair of a rotary embedding (host function): inv_freq[i] = base^(-2 i / rot_dim),
+ * i < rot_dim / 2 (HOST array).  factor > 1 scales them for contexts `factor` times as long as the orig_len positions
+ * a model was trained on: pairs that turn less than turns_slow times over orig_len positions are slowed by factor,
+ * pairs that turn more than turns_fast times are kept, those between are blended linearly in i (usual values: 32 and
+ * 1).  *mscale (may be NULL) receives 0.1 ln(factor) + 1, the usual factor on rotated values, or 1 when factor is 1.
+ */
+DSA_API dsa_status_t dsa_rope_frequencies(int rot_dim, double base, double factor, int orig_len, double turns_fast,
+                                          double turns_slow, double* inv_freq, float* mscale);
+
+/*
+ * Rotary positions of the queries and latent entries (their last 64 dims) or of indexer queries and keys before
+ * quantisation: dims [rot_off, rot_off + rot_dim) of each head are turned pairwise by theta_i = position * inv_freq[i],
+ *   out_a = mscale (x_a cos theta_i - x_b sin theta_i),   out_b = mscale (x_a sin theta_i + x_b cos theta_i),
+ * (a, b) = (2 i, 2 i + 1) when interleaved is non-zero, else (i, i + rot_dim / 2); the other dims are copied.
+ * dsa_rope_backward is the transpose: dx from the gradient dout, with the same mscale.
+ *   x, out: T tokens x H heads x D dims of `dtype` (DSA_BF16, DSA_FP32); the dims of a head are adjacent, tokens and
+ *     heads at the given strides in elements (x may repeat rows with stride 0; rows of out must not meet).  out may be
+ *     x itself (same strides: only the rotated dims are touched) and may otherwise share no element with it
+ *     (DSA_ERR_INVALID_ARG).
+ *   positions [T] int32 (device), or NULL: token t is at position pos0 + t.  inv_freq [rot_dim / 2] fp64 (DEVICE).
+ * Angles are formed in fp64.  Pieces of 16 bytes are moved where pointers, strides and offsets allow, single elements
+ * otherwise.  Needs no workspace.
+ */
+DSA_API dsa_status_t dsa_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, void* out, int64_t out_stride_t,
+                              int64_t out_stride_h, const int32_t* positions, int pos0, const double* inv_freq, int T,
+                              int H, int D, int rot_off, int rot_dim, int interleaved, float mscale, int dtype,
+                              void* stream);
+DSA_API dsa_status_t dsa_rope_backward(const void* dout, int64_t dout_stride_t, int64_t dout_stride_h, void* dx,
+                                       int64_t dx_stride_t, int64_t dx_stride_h, const int32_t* positions, int pos0,
+                                       const double* inv_freq, int T, int H, int D, int rot_off, int rot_dim,
+                                       int interleaved, float mscale, int dtype, void* stream);
+
 /* Workspace bytes of dsa_forward_prefill_kl. */
 DSA_API size_t dsa_prefill_kl_workspace_size(int L, int H_I, int d_I, int H, int k);
 

@@ -22,6 +22,7 @@ _STATUS = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED_SHAPE"
 
 # exported symbols and their C signatures
 _P, _I, _I64, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+_D = ctypes.c_double
 SIGNATURES = {
     "dsa_status_string": (ctypes.c_char_p, [_I]),
     "dsa_get_device_status": (_I, [_P, ctypes.POINTER(ctypes.c_int)]),
@@ -38,6 +39,11 @@ SIGNATURES = {
     "dsa_indexer_kl": (_I, [_P, _P, _I, _P, _P, _P, _I, _I, _I, _F, _P, _P]),
     "dsa_indexer_kl_backward_workspace_size": (_SZ, [_I]),
     "dsa_indexer_kl_backward": (_I, [_P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _SZ, _P]),
+    "dsa_indexer_scores_backward_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "dsa_indexer_scores_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
+    "dsa_rope_frequencies": (_I, [_I, _D, _D, _I, _D, _D, _P, _P]),
+    "dsa_rope": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
+    "dsa_rope_backward": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
     "dsa_prefill_kl_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "dsa_forward_prefill_kl": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _SZ,
                                     _P]),
@@ -128,6 +134,42 @@ def _check(fn: str, code: int):
         raise DsaError(fn, code)
 
 
+def _want(fn: str, device, **args):
+    """Each argument name=(tensor or None, dtype, shape): a contiguous tensor of that type and shape on `device`."""
+    for name, (t, dtype, shape) in args.items():
+        if t is None:
+            continue
+        if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
+            raise ValueError(f"{fn}: {name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {shape} on "
+                             f"{device}")
+
+
+class _On:
+    """The device of a call's tensors and the stream it runs on: the given one, or the device's current one.  Buffers
+    allocated inside belong to that stream."""
+
+    def __init__(self, fn: str, device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"{fn}: libdsa takes device tensors")
+        self.device = device
+        self.own = stream is None
+        self.stream = torch.cuda.current_stream(device) if self.own else stream
+        if self.stream.device != device:
+            raise ValueError(f"{fn}: the stream is on {self.stream.device}, the tensors on {device}")
+        self.guard = None
+
+    def __enter__(self):
+        if not self.own or torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.stream(self.stream)       # also makes its device current
+            self.guard.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
 def dsa_num_sms() -> int:
     return _lib.dsa_num_sms()
 
@@ -188,19 +230,23 @@ def dsa_sparse_mla_attn_backward_workspace_size(T: int, S: int, H: int, k: int) 
 def dsa_sparse_mla_attn_backward(q, c, idx, out, lse, dout, scale: float, dq=None, dc=None, ws=None, stream=None):
     """Gradients (dq [T, H, 576], dc [S, 576]) of dsa_sparse_mla_attn's queries and latent entries, from its inputs,
     its outputs out and lse, and the gradient dout [T, H, 512] of out."""
+    fn = "dsa_sparse_mla_attn_backward"
     T, H, _ = q.shape
-    S = c.shape[0]
-    k = idx.shape[1]
-    if dq is None:
-        dq = torch.empty((T, H, 576), dtype=torch.bfloat16, device=q.device)
-    if dc is None:
-        dc = torch.empty((S, 576), dtype=torch.bfloat16, device=q.device)
-    if ws is None:
-        ws = torch.empty((dsa_sparse_mla_attn_backward_workspace_size(T, S, H, k),), dtype=torch.uint8,
-                         device=q.device)
-    _check("dsa_sparse_mla_attn_backward", _lib.dsa_sparse_mla_attn_backward(
-        _ptr(q), _ptr(c), S, _ptr(idx), _ptr(out), _ptr(lse), _ptr(dout), T, H, k, float(scale), _ptr(dq), _ptr(dc),
-        _ptr(ws), ws.numel(), _stream(stream)))
+    S, k, dev = c.shape[0], idx.shape[1], q.device
+    bf16 = torch.bfloat16
+    _want(fn, dev, q=(q, bf16, (T, H, 576)), c=(c, bf16, (S, 576)), idx=(idx, torch.int32, (T, k)),
+          out=(out, bf16, (T, H, 512)), lse=(lse, torch.float32, (T, H)), dout=(dout, bf16, (T, H, 512)),
+          dq=(dq, bf16, (T, H, 576)), dc=(dc, bf16, (S, 576)))
+    with _On(fn, dev, stream) as st:
+        if dq is None:
+            dq = torch.empty((T, H, 576), dtype=bf16, device=dev)
+        if dc is None:
+            dc = torch.empty((S, 576), dtype=bf16, device=dev)
+        if ws is None:
+            ws = torch.empty((dsa_sparse_mla_attn_backward_workspace_size(T, S, H, k),), dtype=torch.uint8, device=dev)
+        _check(fn, _lib.dsa_sparse_mla_attn_backward(
+            _ptr(q), _ptr(c), S, _ptr(idx), _ptr(out), _ptr(lse), _ptr(dout), T, H, k, float(scale), _ptr(dq), _ptr(dc),
+            _ptr(ws), ws.numel(), st))
     return dq, dc
 
 
@@ -225,17 +271,100 @@ def dsa_indexer_kl_backward_workspace_size(T: int) -> int:
 def dsa_indexer_kl_backward(q, c, idx, sel_scores, lse, dkl, scale: float, dsel=None, ws=None, stream=None):
     """Gradient dsel [T, k] of dsa_indexer_kl with respect to the selected entries' index scores, from the gradient
     dkl [T] of its divergences (None: 1)."""
+    fn = "dsa_indexer_kl_backward"
     T, H, _ = q.shape
-    S = c.shape[0]
-    k = idx.shape[1]
-    if dsel is None:
-        dsel = torch.empty((T, k), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = torch.empty((dsa_indexer_kl_backward_workspace_size(T),), dtype=torch.uint8, device=q.device)
-    _check("dsa_indexer_kl_backward", _lib.dsa_indexer_kl_backward(
-        _ptr(q), _ptr(c), S, _ptr(idx), _ptr(sel_scores), _ptr(lse), _ptr(dkl), T, H, k, float(scale), _ptr(dsel),
-        _ptr(ws), ws.numel(), _stream(stream)))
+    S, k, dev = c.shape[0], idx.shape[1], q.device
+    f32 = torch.float32
+    _want(fn, dev, q=(q, torch.bfloat16, (T, H, 576)), c=(c, torch.bfloat16, (S, 576)), idx=(idx, torch.int32, (T, k)),
+          sel_scores=(sel_scores, f32, (T, k)), lse=(lse, f32, (T, H)), dkl=(dkl, f32, (T,)), dsel=(dsel, f32, (T, k)))
+    with _On(fn, dev, stream) as st:
+        if dsel is None:
+            dsel = torch.empty((T, k), dtype=f32, device=dev)
+        if ws is None:
+            ws = torch.empty((dsa_indexer_kl_backward_workspace_size(T),), dtype=torch.uint8, device=dev)
+        _check(fn, _lib.dsa_indexer_kl_backward(
+            _ptr(q), _ptr(c), S, _ptr(idx), _ptr(sel_scores), _ptr(lse), _ptr(dkl), T, H, k, float(scale), _ptr(dsel),
+            _ptr(ws), ws.numel(), st))
     return dsel
+
+
+def dsa_indexer_scores_backward_workspace_size(T: int, S: int, H_I: int, d_I: int, k: int) -> int:
+    return int(_lib.dsa_indexer_scores_backward_workspace_size(T, S, H_I, d_I, k))
+
+
+def dsa_indexer_scores_backward(q_idx, q_scale, k_idx, k_scale, w, idx, dsel, dq=None, dk=None, dw=None, ws=None,
+                                stream=None):
+    """Gradients (dq [T, H_I, d_I] bf16, dk [S, d_I] bf16, dw [T, H_I] fp32) of the dequantised indexer queries and keys
+    and of the head weights, from the gradient dsel [T, k] of the selected entries' index scores."""
+    fn = "dsa_indexer_scores_backward"
+    T, H_I, d_I = q_idx.shape
+    S, k, dev = k_idx.shape[0], idx.shape[1], q_idx.device
+    f32, bf16, e4m3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+    _want(fn, dev, q_idx=(q_idx, e4m3, (T, H_I, d_I)), q_scale=(q_scale, f32, (T,)), k_idx=(k_idx, e4m3, (S, d_I)),
+          k_scale=(k_scale, f32, (S,)), w=(w, f32, (T, H_I)), idx=(idx, torch.int32, (T, k)), dsel=(dsel, f32, (T, k)),
+          dq=(dq, bf16, (T, H_I, d_I)), dk=(dk, bf16, (S, d_I)), dw=(dw, f32, (T, H_I)))
+    with _On(fn, dev, stream) as st:
+        if dq is None:
+            dq = torch.empty((T, H_I, d_I), dtype=bf16, device=dev)
+        if dk is None:
+            dk = torch.empty((S, d_I), dtype=bf16, device=dev)
+        if dw is None:
+            dw = torch.empty((T, H_I), dtype=f32, device=dev)
+        if ws is None:
+            ws = torch.empty((dsa_indexer_scores_backward_workspace_size(T, S, H_I, d_I, k),), dtype=torch.uint8,
+                             device=dev)
+        _check(fn, _lib.dsa_indexer_scores_backward(
+            _ptr(q_idx), _ptr(q_scale), _ptr(k_idx), _ptr(k_scale), _ptr(w), _ptr(idx), _ptr(dsel), T, S, H_I, d_I, k,
+            _ptr(dq), _ptr(dk), _ptr(dw), _ptr(ws), ws.numel(), st))
+    return dq, dk, dw
+
+
+_ROPE_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def dsa_rope_frequencies(rot_dim: int, base: float = 10000.0, factor: float = 1.0, orig_len: int = 0,
+                         turns_fast: float = 32.0, turns_slow: float = 1.0):
+    """(inv_freq [rot_dim / 2] fp64 on the host, mscale) of a rotary embedding, scaled for long contexts when
+    factor > 1.  dsa_rope takes inv_freq on the device."""
+    f = torch.empty((max(rot_dim, 0) // 2,), dtype=torch.float64)
+    m = ctypes.c_float(0.0)
+    _check("dsa_rope_frequencies", _lib.dsa_rope_frequencies(
+        rot_dim, base, factor, orig_len, turns_fast, turns_slow, ctypes.c_void_p(f.data_ptr()), ctypes.byref(m)))
+    return f, m.value
+
+
+def _rope(fn: str, x, inv_freq, positions, pos0, rot_off, interleaved, mscale, out, stream):
+    if x.dim() != 3 or (out is not None and out.shape != x.shape):
+        raise ValueError(f"{fn}: takes [T, H, D] tensors")
+    T, H, D = x.shape
+    dev = x.device
+    if x.dtype not in _ROPE_DTYPES or (out is not None and (out.dtype != x.dtype or out.device != dev)):
+        raise ValueError(f"{fn}: takes bf16 or fp32 tensors, both of one type and device")
+    if (D > 1 and x.stride(2) != 1) or (out is not None and D > 1 and out.stride(2) != 1):
+        raise ValueError(f"{fn}: the dims of a head must be adjacent")
+    _want(fn, dev, inv_freq=(inv_freq, torch.float64, (inv_freq.numel(),)), positions=(positions, torch.int32, (T,)))
+    with _On(fn, dev, stream) as st:
+        if out is None:
+            out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+        _check(fn, getattr(_lib, fn)(
+            ctypes.c_void_p(x.data_ptr()), x.stride(0), x.stride(1), ctypes.c_void_p(out.data_ptr()), out.stride(0),
+            out.stride(1), _ptr(positions), pos0, _ptr(inv_freq), T, H, D, rot_off, 2 * inv_freq.numel(),
+            1 if interleaved else 0, float(mscale), _ROPE_DTYPES[x.dtype], st))
+    return out
+
+
+def dsa_rope(x, inv_freq, positions=None, pos0: int = 0, rot_off: int = 0, interleaved: bool = True,
+             mscale: float = 1.0, out=None, stream=None):
+    """x [T, H, D] (any token and head strides) with dims rot_off .. rot_off + 2 len(inv_freq) - 1 of each head turned
+    to the tokens' positions ([T] int32, or pos0 + t) -> out (may be x)."""
+    return _rope("dsa_rope", x, inv_freq, positions, pos0, rot_off, interleaved, mscale, out, stream)
+
+
+def dsa_rope_backward(dout, inv_freq, positions=None, pos0: int = 0, rot_off: int = 0, interleaved: bool = True,
+                      mscale: float = 1.0, dx=None, out=None, stream=None):
+    """Gradient of dsa_rope's x from the gradient dout of its result -> dx (may be dout; `out` is another name of it)."""
+    return _rope("dsa_rope_backward", dout, inv_freq, positions, pos0, rot_off, interleaved, mscale,
+                 out if dx is None else dx, stream)
 
 
 def dsa_prefill_kl_workspace_size(L: int, H_I: int, d_I: int, H: int, k: int) -> int:

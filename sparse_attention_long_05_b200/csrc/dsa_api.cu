@@ -13,6 +13,8 @@
 
 #include "common.cuh"
 #include "indexer.cuh"
+#include "indexer_bwd.cuh"
+#include "rope.cuh"
 #include "scatter.cuh"
 #include "sparse_mla.cuh"
 #include "sparse_mla_bwd.cuh"
@@ -840,6 +842,150 @@ dsa_status_t run_kl_bwd(const uint16_t* q, const uint16_t* c, int S, const int32
   return last_launch_status();
 }
 
+// Workspace of the index scores' backward pass.
+struct IndexBwdWs {
+  int Tc, kp;
+  ScatterWs sc;
+  size_t bytes;
+};
+IndexBwdWs index_bwd_ws(void* ws, int T, int64_t S, int d_I, int k) {
+  IndexBwdWs a{};
+  a.kp = round_up(k, 128);
+  a.Tc = bwd_chunk(T, S, a.kp, size_t(d_I) * 2);
+  Carve w{static_cast<char*>(ws)};
+  a.sc = carve_scatter(w, a.Tc, S, k, a.kp, d_I, a.Tc < T);
+  a.bytes = w.at;
+  return a;
+}
+
+template <int HI, int DI>
+dsa_status_t run_index_bwd(IndexerBwdParams p, int T, uint16_t* dk, const IndexBwdWs& w, cudaStream_t st) {
+  CUtensorMap tout;
+  if (!make_rows_map(&tout, w.sc.contrib, static_cast<long long>(w.Tc) * w.kp, DI, 128)) return DSA_ERR_CUDA;
+  if (set_smem(indexer_bwd_kernel<HI, DI>, ixb::SMEM) != cudaSuccess) return DSA_ERR_CUDA;
+  p.n_end = w.sc.n_end;
+  p.kp = w.kp;
+  const IndexerBwdParams all = p;
+  for (int t0 = 0; t0 < T; t0 += w.Tc) {
+    const size_t o = static_cast<size_t>(t0);
+    p.T = std::min(w.Tc, T - t0);
+    p.q_idx = all.q_idx + o * HI * DI;
+    p.q_scale = all.q_scale ? all.q_scale + o : nullptr;
+    p.w = all.w + o * HI;
+    p.idx = all.idx + o * p.k;
+    p.dsel = all.dsel + o * p.k;
+    p.dq = all.dq + o * HI * DI;
+    p.dw = all.dw + o * HI;
+    dsa_status_t e = scatter_begin(w.sc, p.idx, p.T, p.S, p.k, st);
+    if (e != DSA_OK) return e;
+    if (launch_pdl(indexer_bwd_kernel<HI, DI>, dim3(std::min(num_sms(), p.T)), dim3(ixb::THREADS), ixb::SMEM, st, tout,
+                   p) != cudaSuccess)
+      return DSA_ERR_CUDA;
+    if ((e = last_launch_status()) != DSA_OK) return e;
+    e = scatter_end<DI>(w.sc, p.T, p.S, p.k, w.kp, t0 == 0, t0 + p.T >= T, dk, st);
+    if (e != DSA_OK) return e;
+  }
+  return DSA_OK;
+}
+
+// ------------------------------------------------------------------------------------------ rotary positions
+template <typename E>
+dsa_status_t launch_rope(RopeParams p, bool vec, bool inter, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(E);
+  const int n = vec ? V : 1;
+  const bool in_place = p.x == p.out;
+  p.rot_units = vec && inter ? p.R / V : p.R / 2 / n;
+  p.units = p.rot_units + (in_place ? 0 : (p.D - p.R) / n);
+  // one head a thread until the GPU's resident threads are covered, then up to eight (their loads in flight together;
+  // the angles are formed once for them)
+  const long long one = static_cast<long long>(p.T) * p.units * p.H, resident = 2048ll * num_sms();
+  p.heads_per = static_cast<int>(std::min<long long>(8, std::max<long long>(1, one / resident)));
+  p.head_groups = (p.H + p.heads_per - 1) / p.heads_per;
+  const long long per = static_cast<long long>(p.units) * p.head_groups;
+  const int step = static_cast<int>(std::min<long long>(p.T, std::max<long long>(1, (1ll << 31) / per - 1)));
+  const int T = p.T;
+  const RopeParams all = p;
+  auto kern = vec ? (inter ? rope_kernel<E, V, true> : rope_kernel<E, V, false>)
+                  : (inter ? rope_kernel<E, 1, true> : rope_kernel<E, 1, false>);
+  for (int t0 = 0; t0 < T; t0 += step) {
+    p.T = std::min(step, T - t0);
+    p.x = static_cast<const E*>(all.x) + t0 * all.x_st;
+    p.out = static_cast<E*>(all.out) + t0 * all.o_st;
+    p.positions = all.positions ? all.positions + t0 : nullptr;
+    p.pos0 = all.pos0 + t0;
+    const long long threads = per * p.T;
+    if (launch_pdl(kern, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, st, p) != cudaSuccess)
+      return DSA_ERR_CUDA;
+    const dsa_status_t e = last_launch_status();
+    if (e != DSA_OK) return e;
+  }
+  return DSA_OK;
+}
+
+// Elements [0, D) of each of T x H rows at the given strides do not meet each other.
+bool rope_rows_apart(int T, int H, int D, int64_t st, int64_t sh) {
+  if (H == 1) return T == 1 || st >= D;
+  if (T == 1) return sh >= D;
+  return (sh >= D && st >= (H - 1) * sh + D) || (st >= D && sh >= (T - 1) * st + D);
+}
+
+dsa_status_t run_rope(const void* x, int64_t x_st, int64_t x_sh, void* out, int64_t o_st, int64_t o_sh,
+                      const int32_t* positions, int pos0, const double* inv_freq, int T, int H, int D, int rot_off,
+                      int rot_dim, int interleaved, float mscale, int dtype, bool backward, void* stream) {
+  if (T < 0 || H <= 0 || D <= 0 || rot_dim <= 0 || rot_dim % 2 || rot_off < 0 || rot_off > D - rot_dim ||
+      (T > 0 && (!x || !out || !inv_freq)) || x_st < 0 || x_sh < 0 || (dtype != DSA_BF16 && dtype != DSA_FP32))
+    return DSA_ERR_INVALID_ARG;
+  if (T == 0) return DSA_OK;
+  if (!positions && pos0 > INT32_MAX - (T - 1)) return DSA_ERR_INVALID_ARG;
+  const int es = dtype == DSA_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(x) % es || reinterpret_cast<uintptr_t>(out) % es ||
+      reinterpret_cast<uintptr_t>(inv_freq) % 8 || reinterpret_cast<uintptr_t>(positions) % 4)
+    return DSA_ERR_ALIGNMENT;
+  // a single token's or head's stride does not matter
+  if (T == 1) x_st = o_st = 0;
+  if (H == 1) x_sh = o_sh = 0;
+  if (!rope_rows_apart(T, H, D, o_st, o_sh)) return DSA_ERR_INVALID_ARG;
+  // the result replaces its input exactly, or shares no element with it: apart in memory, or (equal strides) lying
+  // in the gaps between the other's rows
+  if (x == out) {
+    if (x_st != o_st || x_sh != o_sh) return DSA_ERR_INVALID_ARG;
+  } else {
+    const char *xb = static_cast<const char*>(x), *ob = static_cast<const char*>(out);
+    const int64_t xe = ((T - 1) * x_st + (H - 1) * x_sh + D) * es, oe = ((T - 1) * o_st + (H - 1) * o_sh + D) * es;
+    if (xb < ob + oe && ob < xb + xe) {
+      const int64_t unit = H > 1 ? (T > 1 ? std::min(x_st, x_sh) : x_sh) : x_st, delta = (ob - xb) / es;
+      const bool lattice = x_st == o_st && x_sh == o_sh && unit > 0 && x_st % unit == 0 && x_sh % unit == 0 &&
+                           (ob - xb) % es == 0;
+      const int64_t r = lattice ? ((delta % unit) + unit) % unit : 0;
+      if (!lattice || r < D || r > unit - D) return DSA_ERR_INVALID_ARG;
+    }
+  }
+  RopeParams p{};
+  p.x = x;
+  p.out = out;
+  p.x_st = x_st;
+  p.x_sh = x_sh;
+  p.o_st = o_st;
+  p.o_sh = o_sh;
+  p.positions = positions;
+  p.freq = inv_freq;
+  p.pos0 = pos0;
+  p.T = T;
+  p.H = H;
+  p.D = D;
+  p.off = rot_off;
+  p.R = rot_dim;
+  p.m = mscale;
+  p.backward = backward ? 1 : 0;
+  // 16-byte pieces where every row, the rotated part and its halves start on them
+  const int64_t v = 16 / es;
+  const bool vec = aligned16(x) && aligned16(out) && x_st % v == 0 && x_sh % v == 0 && o_st % v == 0 &&
+                   o_sh % v == 0 && D % v == 0 && rot_off % v == 0 && (interleaved ? rot_dim : rot_dim / 2) % v == 0;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return dtype == DSA_BF16 ? launch_rope<__nv_bfloat16>(p, vec, interleaved != 0, st)
+                           : launch_rope<float>(p, vec, interleaved != 0, st);
+}
+
 }  // namespace
 }  // namespace dsa
 
@@ -1531,6 +1677,82 @@ dsa_status_t dsa_indexer_kl_backward(const uint16_t* q, const uint16_t* c, int S
   if (T == 0) return DSA_OK;
   if (!ws || ws_bytes < kl_bwd_ws_bytes(T)) return DSA_ERR_WORKSPACE;
   return run_kl_bwd(q, c, S, idx, sel_scores, lse, dkl, T, H, k, scale, dsel, ws, static_cast<cudaStream_t>(stream));
+}
+
+size_t dsa_indexer_scores_backward_workspace_size(int T, int S, int H_I, int d_I, int k) {
+  if (T <= 0 || S <= 0 || !indexer_shape_ok(H_I, d_I) || !mla_k_ok(k)) return 0;
+  return index_bwd_ws(nullptr, T, S, d_I, k).bytes;
+}
+
+dsa_status_t dsa_indexer_scores_backward(const uint8_t* q_idx, const float* q_scale, const uint8_t* k_idx,
+                                         const float* k_scale, const float* w, const int32_t* idx, const float* dsel,
+                                         int T, int S, int H_I, int d_I, int k, uint16_t* dq, uint16_t* dk, float* dw,
+                                         void* ws, size_t ws_bytes, void* stream) {
+  if (T < 0 || S <= 0 || k <= 0 || !dk || (T > 0 && (!q_idx || !k_idx || !w || !idx || !dsel || !dq || !dw)))
+    return DSA_ERR_INVALID_ARG;
+  if (!indexer_shape_ok(H_I, d_I) || !mla_k_ok(k)) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(q_idx) || !aligned16(k_idx) || !aligned16(idx) || !aligned16(dq) || !aligned16(dk) || !aligned16(ws))
+    return DSA_ERR_ALIGNMENT;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0)
+    return cudaMemsetAsync(dk, 0, size_t(S) * d_I * 2, st) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  const IndexBwdWs a = index_bwd_ws(ws, T, S, d_I, k);
+  if (!ws || ws_bytes < a.bytes) return DSA_ERR_WORKSPACE;
+  IndexerBwdParams p{};
+  p.q_idx = q_idx;
+  p.q_scale = q_scale;
+  p.k_idx = k_idx;
+  p.k_scale = k_scale;
+  p.w = w;
+  p.idx = idx;
+  p.dsel = dsel;
+  p.dq = dq;
+  p.dw = dw;
+  p.k = k;
+  p.S = S;
+  return H_I == 64 ? run_index_bwd<64, 128>(p, T, dk, a, st) : run_index_bwd<4, 64>(p, T, dk, a, st);
+}
+
+dsa_status_t dsa_rope_frequencies(int rot_dim, double base, double factor, int orig_len, double turns_fast,
+                                  double turns_slow, double* inv_freq, float* mscale) {
+  if (rot_dim <= 0 || rot_dim % 2 || !(base > 1.0) || !(factor >= 1.0) || !inv_freq || !std::isfinite(base) ||
+      !std::isfinite(factor))
+    return DSA_ERR_INVALID_ARG;
+  if (factor > 1.0 && (orig_len <= 0 || !(turns_slow > 0.0) || !(turns_fast > turns_slow) || !std::isfinite(turns_fast)))
+    return DSA_ERR_INVALID_ARG;
+  const int n = rot_dim / 2;
+  double low = 0.0, high = 0.0;
+  if (factor > 1.0) {
+    // pair index whose wavelength makes `turns` turns over orig_len positions
+    auto pair_of = [&](double turns) {
+      return rot_dim * std::log(orig_len / (turns * 6.283185307179586)) / (2.0 * std::log(base));
+    };
+    low = std::max(0.0, std::floor(pair_of(turns_fast)));
+    high = std::min(n - 1.0, std::ceil(pair_of(turns_slow)));
+  }
+  for (int i = 0; i < n; ++i) {
+    const double f = std::pow(base, -2.0 * i / rot_dim);
+    double slow = 0.0;
+    if (factor > 1.0) slow = std::min(1.0, std::max(0.0, (i - low) / std::max(high - low, 1e-3)));
+    inv_freq[i] = f / factor * slow + f * (1.0 - slow);
+  }
+  if (mscale) *mscale = factor > 1.0 ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return DSA_OK;
+}
+
+dsa_status_t dsa_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, void* out, int64_t out_stride_t,
+                      int64_t out_stride_h, const int32_t* positions, int pos0, const double* inv_freq, int T, int H,
+                      int D, int rot_off, int rot_dim, int interleaved, float mscale, int dtype, void* stream) {
+  return run_rope(x, x_stride_t, x_stride_h, out, out_stride_t, out_stride_h, positions, pos0, inv_freq, T, H, D,
+                  rot_off, rot_dim, interleaved, mscale, dtype, false, stream);
+}
+
+dsa_status_t dsa_rope_backward(const void* dout, int64_t dout_stride_t, int64_t dout_stride_h, void* dx,
+                               int64_t dx_stride_t, int64_t dx_stride_h, const int32_t* positions, int pos0,
+                               const double* inv_freq, int T, int H, int D, int rot_off, int rot_dim, int interleaved,
+                               float mscale, int dtype, void* stream) {
+  return run_rope(dout, dout_stride_t, dout_stride_h, dx, dx_stride_t, dx_stride_h, positions, pos0, inv_freq, T, H, D,
+                  rot_off, rot_dim, interleaved, mscale, dtype, true, stream);
 }
 
 }  // extern "C"

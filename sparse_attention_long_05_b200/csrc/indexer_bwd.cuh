@@ -1,0 +1,421 @@
+// Backward pass of the lightning-indexer scores (indexer.cuh) at the selected entries.
+//
+// I[t,i] = sum_j w_j relu(q_j . k_s), s = idx[t][i], q_j = qs_t q_idx[t][j] and k_s = ks_s k_idx[s] the dequantised
+// operands.  With the gradient e = dsel[t][i], x = q_idx[t][j] . k_idx[s] and the live pairs 1[x > 0]:
+//   dw_j = qs sum_i e ks relu(x)       dq_j = sum_i (e w_j 1[x > 0] ks) k_idx[s]       dk_s = sum_(t,i) qs sum_j G q_idx[j]
+// with G = e w_j 1[x > 0]: three products of 2 x 64 heads x 128 dims per entry.  dq and dk are gradients of the
+// dequantised values (what a straight-through quantiser passes on).
+//
+// One CTA per token, keys are the M dimension.  e4m3 rows are gathered with plain 16-byte loads and written as bf16
+// (exact) in the swizzled form the tensor core reads, so the one copy serves x (K-major), dq (transposed, MN-major)
+// and, for q, dk; kind::f16 needs both operands bf16 and G is.  x is exact: products of e4m3 are, and their sum is
+// held in fp32.  G and G ks are rounded to bf16 once (2^-9).  dw is summed from the fp32 x.  Per token: 16 tiles of
+// 128 keys, each x -> G -> (dk, dq); x of the next tile is issued before G of this one is waited for.
+// HBM sees each entry's contribution to dk twice (written here, summed by scatter.cuh).
+// The small indexer (4 heads, 64 dims) runs in the same layout, its missing heads and dims zero.
+#pragma once
+#include "common.cuh"
+#include "sparse_mla_bwd.cuh"
+
+namespace dsa {
+
+struct IndexerBwdParams {
+  const uint8_t* q_idx;        // [T, HI, DI] e4m3
+  const float* q_scale;        // [T] or null
+  const uint8_t* k_idx;        // [S, DI] e4m3
+  const float* k_scale;        // [S] or null
+  const float* w;              // [T, HI]
+  const int* idx;              // [T, k]
+  const float* dsel;           // [T, k]
+  const int* n_end;            // [T]
+  uint16_t* dq;                // [T, HI, DI] bf16
+  float* dw;                   // [T, HI]
+  int T, k, kp;
+  long long S;
+};
+
+namespace ixb {
+constexpr int THREADS = 576, PRODUCERS = 8;      // w0 index rows, w1 MMA, w2 w3 w8..13 keys, w4..7 G, w14..17 results
+constexpr int NK = 128, HP = 64;
+constexpr int KCH = 128 * 128, QCH = 64 * 128;   // 128 keys (64 heads) x 64 dims bf16
+constexpr int K_BYTES = 2 * KCH, Q_BYTES = 2 * QCH, G_BYTES = 128 * 128;
+constexpr int B_IDX_FULL = 0, B_IDX_EMPTY = 2, B_Q_FULL = 4, B_Q_EMPTY = 6, B_K_FULL = 8, B_K_EMPTY = 10;
+constexpr int B_X_FULL = 12, B_X_EMPTY = 14, B_G_FULL = 16, B_G_EMPTY = 18, B_DK_FULL = 20, B_DK_EMPTY = 22;
+constexpr int B_DQ_FULL = 24, B_DQ_EMPTY = 26;
+constexpr int OFF_W = 1024, OFF_DW = OFF_W + 512;            // w of the token (2 buffers), dw of the four warps
+constexpr int OFF_IDX = 4096, OFF_Q = OFF_IDX + 2 * mla::KMAX * 4, OFF_K = OFF_Q + 2 * Q_BYTES;
+constexpr int OFF_G = OFF_K + 2 * K_BYTES;                   // 2 x (G, G ks)
+constexpr int OFF_OUT = OFF_G + 4 * G_BYTES;
+constexpr int SMEM = OFF_OUT + 2 * KCH + 1024;
+constexpr uint32_t TX = 0, TDK = 128, TDQ = 384;             // x 2 x 64, dk 2 x 128, dq 2 x 64 columns
+static_assert(SMEM <= 232448 && OFF_DW + 1024 <= OFF_IDX, "shared memory");
+}  // namespace ixb
+
+// two e4m3 -> two bf16 (exact)
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
+  float lo, hi;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi) : "r"(h));
+  return pack_bf16(lo, hi);
+}
+// 16 e4m3 (dims 16 u .. 16 u + 15 of a row) into a swizzled bf16 tile of 64-dim chunks `chunk` bytes apart
+__device__ __forceinline__ void put_e4m3_row16(uint8_t* tile, int chunk, int row, int u, uint4 v) {
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+  uint32_t y[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[2 * i] = e4m3x2_to_bf16x2(x[i] & 0xffff);
+    y[2 * i + 1] = e4m3x2_to_bf16x2(x[i] >> 16);
+  }
+  uint8_t* line = tile + (u >> 2) * chunk + row * 128;
+  const int unit = 2 * (u & 3);
+  *reinterpret_cast<uint4*>(line + ((unit ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+  *reinterpret_cast<uint4*>(line + (((unit + 1) ^ (row & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+}
+
+template <int HI, int DI>
+__global__ void __launch_bounds__(ixb::THREADS, 1)
+indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdParams p) {
+  using namespace ixb;
+  extern __shared__ uint8_t smem_raw[];
+  BwdCta cta = bwd_base(smem_raw);
+  const uint32_t sbase = cta.sbase;
+  volatile int* abort_flag = cta.abort_flag;
+  const int warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(cta.bar(B_IDX_FULL + i), 1);
+      mbar_init(cta.bar(B_IDX_EMPTY + i), PRODUCERS);
+      mbar_init(cta.bar(B_Q_FULL + i), PRODUCERS);
+      mbar_init(cta.bar(B_Q_EMPTY + i), 1);
+      mbar_init(cta.bar(B_K_FULL + i), PRODUCERS);
+      mbar_init(cta.bar(B_K_EMPTY + i), 1);
+      mbar_init(cta.bar(B_X_FULL + i), 1);
+      mbar_init(cta.bar(B_X_EMPTY + i), 4);
+      mbar_init(cta.bar(B_G_FULL + i), 4);
+      mbar_init(cta.bar(B_G_EMPTY + i), 1);
+      mbar_init(cta.bar(B_DK_FULL + i), 1);
+      mbar_init(cta.bar(B_DK_EMPTY + i), 4);
+      mbar_init(cta.bar(B_DQ_FULL + i), 1);
+      mbar_init(cta.bar(B_DQ_EMPTY + i), 4);
+    }
+  }
+  if constexpr (HI < HP || DI < 128) {
+    // the heads and dims that are never written stay zero
+    for (int i = threadIdx.x; i < (2 * Q_BYTES + 2 * K_BYTES + 4 * G_BYTES) / 16; i += THREADS)
+      reinterpret_cast<uint4*>(cta.smem + OFF_Q)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  bwd_begin(cta);
+  const uint32_t tmem = cta.tmem;
+  bool ok = true;
+  int n = 0;                             // tokens with entries, walked so far
+  auto tiles_of = [&](int t) { return (p.n_end[t] + NK - 1) / NK; };
+
+  if (warp == 0) {
+    // ===================================================================== index rows
+    if (lane == 0) {
+      for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+        if (tiles_of(t) <= 0) continue;
+        const int ib = n & 1;
+        if (!(ok = mbar_wait(cta.bar(B_IDX_EMPTY + ib), ((n >> 1) & 1) ^ 1, abort_flag))) break;
+        mbar_arrive_expect_tx(cta.bar(B_IDX_FULL + ib), p.k * 4);
+        bulk_load(sbase + OFF_IDX + ib * mla::KMAX * 4, p.idx + static_cast<long long>(t) * p.k, p.k * 4,
+                  cta.bar(B_IDX_FULL + ib));
+        ++n;
+      }
+      if (*abort_flag)
+        for (int i = max(0, n - 2); i < n; ++i) mbar_wait_drain(cta.bar(B_IDX_FULL + (i & 1)), (i >> 1) & 1);
+    }
+  } else if (warp == 2 || warp == 3 || (warp >= 8 && warp < 14)) {
+    // ===================================================================== keys and queries to bf16 tiles
+    const int pw = (warp < 8) ? warp - 2 : warp - 6;
+    constexpr int U = DI / 16;                    // 16-byte units of a row
+    constexpr int ROWS = 32 / U;                  // rows a warp reads at once
+    constexpr int STEPS = NK / PRODUCERS / ROWS;  // 4 (DI = 128), 2 (64)
+    const int sub = lane / U, u = lane % U;
+    int g = 0;
+    for (int t = blockIdx.x; t < p.T && ok; t += gridDim.x) {
+      const int tiles = tiles_of(t);
+      if (tiles <= 0) continue;
+      const int ib = n & 1;
+      if (!(ok = warp_wait(cta.bar(B_IDX_FULL + ib), (n >> 1) & 1, abort_flag))) break;
+      const int* ids = reinterpret_cast<const int*>(cta.smem + OFF_IDX + ib * mla::KMAX * 4);
+      // the rows of the next tile are read while this one waits for its buffer; an empty slot's row is zero
+      auto load = [&](int j, uint4 (&v)[STEPS]) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+          const int slot = j * NK + pw * (NK / PRODUCERS) + s * ROWS + sub;
+          const int e = slot < p.k ? ids[slot] : -1;
+          v[s] = make_uint4(0, 0, 0, 0);
+          if (e >= 0 && e < p.S) v[s] = __ldg(reinterpret_cast<const uint4*>(p.k_idx + static_cast<long long>(e) * DI) + u);
+        }
+      };
+      uint4 v[STEPS];
+      load(0, v);
+      if (!(ok = warp_wait(cta.bar(B_Q_EMPTY + ib), ((n >> 1) & 1) ^ 1, abort_flag))) break;
+      const uint4* qrow = reinterpret_cast<const uint4*>(p.q_idx + static_cast<long long>(t) * HI * DI);
+      for (int i = pw * 32 + lane; i < HI * U; i += PRODUCERS * 32)
+        put_e4m3_row16(cta.smem + OFF_Q + ib * Q_BYTES, QCH, i / U, i % U, __ldg(qrow + i));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(cta.bar(B_Q_FULL + ib));
+      for (int j = 0; j < tiles; ++j, ++g) {
+        const int kb = g & 1;
+        uint4 next[STEPS];
+        if (j + 1 < tiles) load(j + 1, next);
+        if (!(ok = warp_wait(cta.bar(B_K_EMPTY + kb), ((g >> 1) & 1) ^ 1, abort_flag))) break;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+          put_e4m3_row16(cta.smem + OFF_K + kb * K_BYTES, KCH, pw * (NK / PRODUCERS) + s * ROWS + sub, u, v[s]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(cta.bar(B_K_FULL + kb));
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) v[s] = next[s];
+      }
+      if (lane == 0) mbar_arrive(cta.bar(B_IDX_EMPTY + ib));
+      ++n;
+    }
+  } else if (warp == 1) {
+    // ===================================================================== MMA issue
+    struct Cursor { int t, j, tiles, n, g; } a{static_cast<int>(blockIdx.x), 0, 0, 0, 0}, b;
+    auto seek = [&](Cursor& c) {          // first token at or after c.t with entries
+      while (c.t < p.T && (c.tiles = tiles_of(c.t)) <= 0) c.t += gridDim.x;
+    };
+    auto step = [&](Cursor& c) {
+      ++c.g;
+      if (++c.j == c.tiles) { c.j = 0; ++c.n; c.t += gridDim.x; seek(c); }
+    };
+    seek(a);
+    b = a;
+    constexpr uint32_t ix = idesc_bf16(128, HP, false), idk = idesc_bf16(128, DI, true);
+    constexpr uint32_t idq = idesc_bf16_major(128, HP, true, true);
+    auto scores = [&]() -> bool {         // x of cursor a's tile
+      const int s = a.g & 1, qb = a.n & 1;
+      if (a.j == 0 && !warp_wait(cta.bar(B_Q_FULL + qb), (a.n >> 1) & 1, abort_flag)) return false;
+      if (!warp_wait(cta.bar(B_K_FULL + s), (a.g >> 1) & 1, abort_flag)) return false;
+      if (!warp_wait(cta.bar(B_X_EMPTY + s), ((a.g >> 1) & 1) ^ 1, abort_flag)) return false;
+      tc_fence_after();
+      const uint64_t kd = smem_desc(sbase + OFF_K + s * K_BYTES, 16, 1024, kLayoutSW128);
+      const uint64_t qd = smem_desc(sbase + OFF_Q + qb * Q_BYTES, 16, 1024, kLayoutSW128);
+      if (elect_one()) {
+#pragma unroll
+        for (int i = 0; i < DI / 16; ++i)
+          mma_bf16_ss(tmem + TX + 64 * s, kd + (((i >> 2) * KCH) >> 4) + 2 * (i & 3),
+                      qd + (((i >> 2) * QCH) >> 4) + 2 * (i & 3), ix, i ? 1u : 0u);
+        mma_commit(cta.bar(B_X_FULL + s));
+      }
+      __syncwarp();
+      step(a);
+      return true;
+    };
+    if (a.t < p.T) ok = scores();
+    while (ok && b.t < p.T) {
+      if (a.t < p.T && !(ok = scores())) break;
+      const int s = b.g & 1, qb = b.n & 1;
+      if (b.j == 0 && !(ok = warp_wait(cta.bar(B_DQ_EMPTY + qb), ((b.n >> 1) & 1) ^ 1, abort_flag))) break;
+      if (!(ok = warp_wait(cta.bar(B_DK_EMPTY + s), ((b.g >> 1) & 1) ^ 1, abort_flag))) break;
+      if (!(ok = warp_wait(cta.bar(B_G_FULL + s), (b.g >> 1) & 1, abort_flag))) break;
+      tc_fence_after();
+      const uint32_t gb = sbase + OFF_G + 2 * s * G_BYTES;
+      const uint64_t gd = smem_desc(gb, 16, 1024, kLayoutSW128);                             // keys x heads, K = heads
+      const uint64_t qd = smem_desc(sbase + OFF_Q + qb * Q_BYTES, QCH, 1024, kLayoutSW128);  // heads x dims, N = dims
+      const uint64_t kd = smem_desc(sbase + OFF_K + s * K_BYTES, KCH, 1024, kLayoutSW128);   // keys x dims, M = dims
+      const uint64_t hd = smem_desc(gb + G_BYTES, 8192, 1024, kLayoutSW128);                 // keys x heads, N = heads
+      const bool last = b.j == b.tiles - 1;
+      if (elect_one()) {
+#pragma unroll
+        for (int i = 0; i < HP / 16; ++i)
+          mma_bf16_ss(tmem + TDK + 128 * s, gd + 2 * i, qd + ((i * 2048) >> 4), idk, i ? 1u : 0u);
+        mma_commit(cta.bar(B_DK_FULL + s));
+#pragma unroll
+        for (int i = 0; i < NK / 16; ++i)
+          mma_bf16_ss(tmem + TDQ + 64 * qb, kd + ((i * 2048) >> 4), hd + ((i * 2048) >> 4), idq, (b.j | i) ? 1u : 0u);
+        mma_commit(cta.bar(B_K_EMPTY + s));
+        mma_commit(cta.bar(B_G_EMPTY + s));
+        if (last) {
+          mma_commit(cta.bar(B_Q_EMPTY + qb));
+          mma_commit(cta.bar(B_DQ_FULL + qb));
+        }
+      }
+      __syncwarp();
+      step(b);
+    }
+  } else if (warp < 8) {
+    // ===================================================================== G, G ks and dw (one key a thread)
+    const int quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+    float* dw_s = reinterpret_cast<float*>(cta.smem + OFF_DW);
+    int g = 0;
+    for (int t = blockIdx.x; t < p.T && ok; t += gridDim.x) {
+      const int tiles = tiles_of(t);
+      if (tiles <= 0) {
+        if (row < HI) p.dw[static_cast<long long>(t) * HI + row] = 0.f;
+        continue;
+      }
+      float* ws = reinterpret_cast<float*>(cta.smem + OFF_W) + 64 * (n & 1);
+      if (row < 64) ws[row] = row < HI ? p.w[static_cast<long long>(t) * HI + row] : 0.f;
+      if (!(ok = named_bar_all(1, 128, ok))) break;
+      float dw[2] = {0.f, 0.f};
+      for (int j = 0; j < tiles; ++j, ++g) {
+        const int s = g & 1, slot = j * NK + row;
+        float e = 0.f, ks = 0.f;
+        if (slot < p.k) {
+          const long long at = static_cast<long long>(t) * p.k + slot;
+          const int id = p.idx[at];
+          if (id >= 0 && id < p.S) {
+            e = p.dsel[at];
+            ks = p.k_scale ? p.k_scale[id] : 1.f;
+          }
+        }
+        ok = warp_wait(cta.bar(B_X_FULL + s), (g >> 1) & 1, abort_flag);
+        ok = ok && warp_wait(cta.bar(B_G_EMPTY + s), ((g >> 1) & 1) ^ 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        uint8_t* gl = cta.smem + OFF_G + 2 * s * G_BYTES + row * 128;
+        const float eks = e * ks;
+#pragma unroll
+        for (int c = 0; c < (HI + 31) / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(lane_addr + tmem + TX + 64 * s + 32 * c, v);
+          tmem_wait_ld();
+          if (c == (HI + 31) / 32 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(cta.bar(B_X_EMPTY + s));
+          }
+          float x[32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t a[4], b[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float lo[2], hi[2];
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const int h = 8 * i + 2 * q + r;
+                const float xv = __uint_as_float(v[h]);
+                const bool live = xv > 0.f;
+                const float gv = live ? e * ws[32 * c + h] : 0.f;
+                lo[r] = gv;
+                hi[r] = gv * ks;
+                x[h] = live ? eks * xv : 0.f;
+              }
+              a[q] = pack_bf16(lo[0], lo[1]);
+              b[q] = pack_bf16(hi[0], hi[1]);
+            }
+            const int unit = ((4 * c + i) ^ (row & 7)) << 4;
+            *reinterpret_cast<uint4*>(gl + unit) = make_uint4(a[0], a[1], a[2], a[3]);
+            *reinterpret_cast<uint4*>(gl + G_BYTES + unit) = make_uint4(b[0], b[1], b[2], b[3]);
+          }
+          // sums over the warp's 32 keys: five halving steps, lane l ends with head 32 c + l
+#define DSA_IXB_HALVE(O)                                                                \
+  {                                                                                     \
+    const bool up = (lane & (O)) != 0;                                                  \
+    _Pragma("unroll") for (int i = 0; i < (O); ++i) {                                   \
+      const float keep = up ? x[(O) + i] : x[i];                                        \
+      const float send = up ? x[i] : x[(O) + i];                                        \
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, (O));                            \
+    }                                                                                   \
+  }
+          DSA_IXB_HALVE(16)
+          DSA_IXB_HALVE(8)
+          DSA_IXB_HALVE(4)
+          DSA_IXB_HALVE(2)
+          DSA_IXB_HALVE(1)
+#undef DSA_IXB_HALVE
+          dw[c] += x[0];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(cta.bar(B_G_FULL + s));
+      }
+      dw_s[quad * 64 + lane] = dw[0];
+      dw_s[quad * 64 + 32 + lane] = dw[1];
+      if (!(ok = named_bar_all(1, 128, ok))) break;
+      if (row < HI) {
+        const float qs = p.q_scale ? p.q_scale[t] : 1.f;
+        p.dw[static_cast<long long>(t) * HI + row] =
+            ((dw_s[row] + dw_s[64 + row]) + (dw_s[128 + row] + dw_s[192 + row])) * qs;
+      }
+      // the next token's first barrier comes before anyone writes dw_s again
+      ++n;
+    }
+  } else {
+    // ===================================================================== contributions to dk, and dq (w14..17)
+    const int quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+    const bool leader = warp == 16 && lane == 0;
+    int g = 0;
+    for (int t = blockIdx.x; t < p.T && ok; t += gridDim.x) {
+      const int tiles = tiles_of(t);
+      uint16_t* dq = p.dq + static_cast<long long>(t) * HI * DI;
+      if (tiles <= 0) {
+        for (int i = row; i < HI * DI / 8; i += 128) reinterpret_cast<uint4*>(dq)[i] = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      const float qs = p.q_scale ? p.q_scale[t] : 1.f;
+      for (int j = 0; j < tiles; ++j, ++g) {
+        const int s = g & 1;
+        if (leader) bulk_wait_read();
+        ok = warp_wait(cta.bar(B_DK_FULL + s), (g >> 1) & 1, abort_flag);
+        if (!(ok = named_bar_all(2, 128, ok))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < DI / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(lane_addr + tmem + TDK + 128 * s + 32 * c, v);
+          tmem_wait_ld();
+          if (c == DI / 32 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(cta.bar(B_DK_EMPTY + s));
+          }
+          uint8_t* line = cta.smem + OFF_OUT + (c >> 1) * KCH + row * 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            auto pk = [&](int q) {
+              return pack_bf16(__uint_as_float(v[8 * i + 2 * q]) * qs, __uint_as_float(v[8 * i + 2 * q + 1]) * qs);
+            };
+            *reinterpret_cast<uint4*>(line + (((4 * (c & 1) + i) ^ (row & 7)) << 4)) =
+                make_uint4(pk(0), pk(1), pk(2), pk(3));
+          }
+        }
+        fence_proxy_async_smem();
+        named_bar_sync(2, 128);
+        if (leader) {
+          for (int c = 0; c < DI / 64; ++c) tma_store_2d(&tm_out, sbase + OFF_OUT + c * KCH, 64 * c, t * p.kp + j * NK);
+          bulk_commit();
+        }
+      }
+      if (!ok) break;
+      // dq^T: lane = dim, column = head
+      const int qb = n & 1;
+      if (!(ok = warp_wait(cta.bar(B_DQ_FULL + qb), (n >> 1) & 1, abort_flag))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < (HI + 31) / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld32(lane_addr + tmem + TDQ + 64 * qb + 32 * c, v);
+        tmem_wait_ld();
+        if (row < DI) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * c + i < HI)
+              dq[(32 * c + i) * DI + row] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[i])));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(cta.bar(B_DQ_EMPTY + qb));
+      ++n;
+    }
+    if (leader) bulk_wait_all();
+  }
+  bwd_end(cta);
+}
+
+}  // namespace dsa
