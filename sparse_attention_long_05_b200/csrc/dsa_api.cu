@@ -669,16 +669,15 @@ int round_up(int n, int m) { return (n + m - 1) / m * m; }
 // Scatter of a chunk's contributions: the table and what goes with it.
 struct ScatterWs {
   int *n_end, *fill;
-  uint16_t *table, *mult, *contrib;
+  uint16_t *table, *contrib;
   float* acc;
   int ld;
 };
-ScatterWs carve_scatter(Carve& w, int Tc, int64_t S, int k, int kp, int width, bool many) {
+ScatterWs carve_scatter(Carve& w, int Tc, int64_t S, int kp, int width, bool many) {
   ScatterWs s{};
   s.ld = round_up(Tc, 8);
   s.n_end = w.take<int>(Tc);
   s.fill = w.take<int>(Tc);
-  s.mult = w.take<uint16_t>(size_t(Tc) * k);
   s.table = w.take<uint16_t>(size_t(S) * s.ld);
   s.contrib = w.take<uint16_t>(size_t(Tc) * kp * width);
   s.acc = many ? w.take<float>(size_t(S) * width) : nullptr;
@@ -694,15 +693,15 @@ dsa_status_t scatter_begin(const ScatterWs& w, const int* idx, int T, int64_t S,
   dsa_status_t e = last_launch_status();
   if (e != DSA_OK) return e;
   if (launch_pdl(scatter_build_kernel, dim3(T), dim3(256), 0, st, idx, k, static_cast<long long>(S), w.n_end, w.fill,
-                 w.table, w.ld, w.mult) != cudaSuccess)
+                 w.table, w.ld) != cudaSuccess)
     return DSA_ERR_CUDA;
   return last_launch_status();
 }
 
 template <int W>
-dsa_status_t scatter_end(const ScatterWs& w, int T, int64_t S, int k, int kp, bool first, bool last, uint16_t* out,
+dsa_status_t scatter_end(const ScatterWs& w, const int* idx, int T, int64_t S, int k, int kp, bool first, bool last, uint16_t* out,
                          cudaStream_t st) {
-  const ScatterParams p{w.contrib, w.table, w.mult, T, w.ld, k, kp, w.acc, first ? 1 : 0, last ? 1 : 0, out};
+  const ScatterParams p{w.contrib, w.table, idx, T, w.ld, k, kp, w.acc, first ? 1 : 0, last ? 1 : 0, out};
   if (launch_pdl(scatter_sum_kernel<W>, dim3(static_cast<unsigned>(S)), dim3(ScatterCfg<W>::THREADS), 0, st, p) !=
       cudaSuccess)
     return DSA_ERR_CUDA;
@@ -738,7 +737,7 @@ AttnBwdWs attn_bwd_ws(void* ws, int T, int64_t S, int H, int k) {
   a.kp = round_up(k, 128);
   a.Tc = bwd_chunk(T, S, a.kp, mbw::D * 2 + 4 * size_t(a.HP));
   Carve w{static_cast<char*>(ws)};
-  a.sc = carve_scatter(w, a.Tc, S, k, a.kp, mbw::D, a.Tc < T);
+  a.sc = carve_scatter(w, a.Tc, S, a.kp, mbw::D, a.Tc < T);
   a.delta = w.take<float>(size_t(a.Tc) * H);
   a.pds = w.take<uint16_t>(size_t(a.Tc) * a.kp * 2 * a.HP);
   a.bytes = w.at;
@@ -798,7 +797,7 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
                    p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
-    e = scatter_end<mbw::D>(w.sc, n, S, k, w.kp, t0 == 0, t0 + n >= T, dc, st);
+    e = scatter_end<mbw::D>(w.sc, p.idx, n, S, k, w.kp, t0 == 0, t0 + n >= T, dc, st);
     if (e != DSA_OK) return e;
   }
   return DSA_OK;
@@ -831,7 +830,7 @@ dsa_status_t run_kl_bwd(const uint16_t* q, const uint16_t* c, int S, const int32
   p.dkl = dkl;
   p.dsel = dsel;
   if (launch_pdl(scatter_build_kernel, dim3(T), dim3(256), 0, st, idx, k, static_cast<long long>(S), n_end, fill,
-                 nullptr, 0, nullptr) != cudaSuccess)
+                 nullptr, 0) != cudaSuccess)
     return DSA_ERR_CUDA;
   const dsa_status_t e = last_launch_status();
   if (e != DSA_OK) return e;
@@ -853,7 +852,7 @@ IndexBwdWs index_bwd_ws(void* ws, int T, int64_t S, int d_I, int k) {
   a.kp = round_up(k, 128);
   a.Tc = bwd_chunk(T, S, a.kp, size_t(d_I) * 2);
   Carve w{static_cast<char*>(ws)};
-  a.sc = carve_scatter(w, a.Tc, S, k, a.kp, d_I, a.Tc < T);
+  a.sc = carve_scatter(w, a.Tc, S, a.kp, d_I, a.Tc < T);
   a.bytes = w.at;
   return a;
 }
@@ -882,7 +881,7 @@ dsa_status_t run_index_bwd(IndexerBwdParams p, int T, uint16_t* dk, const IndexB
                    p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
-    e = scatter_end<DI>(w.sc, p.T, p.S, p.k, w.kp, t0 == 0, t0 + p.T >= T, dk, st);
+    e = scatter_end<DI>(w.sc, p.idx, p.T, p.S, p.k, w.kp, t0 == 0, t0 + p.T >= T, dk, st);
     if (e != DSA_OK) return e;
   }
   return DSA_OK;

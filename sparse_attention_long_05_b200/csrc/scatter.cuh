@@ -5,7 +5,7 @@
 // slot[s][t] = the slot in which token t selected row s (16 bits, empty: 0xffff), turns the scatter into a gather:
 // one CTA per row s lists the row's entries in token order and adds them up.  Every sum has one order whatever the
 // kernels' timing, so results repeat bit for bit; with atomics they would not.  Bound by HBM: each contribution is
-// read once (2 W bytes), the table once (2 bytes per row and token, 64 rows' worth per selected entry at 128K rows).
+// read once (2 W bytes), the table once (2 bytes per row and token).
 #pragma once
 #include "common.cuh"
 
@@ -15,7 +15,7 @@ namespace sct {
 constexpr int MAX_T = 2048;               // tokens of a chunk at most (a row's list sits in shared memory)
 constexpr int MAX_K = 2048;               // slots of a token at most: 11 bits of a table entry
 constexpr uint16_t EMPTY = 0xffff;
-constexpr uint16_t TWICE = 0x0800;        // the token selected the row more than once: see mult
+constexpr uint16_t TWICE = 0x0800;        // the token selected the row again in later slots
 }  // namespace sct
 
 __global__ void __launch_bounds__(256) scatter_clear_kernel(uint4* table, long long n) {
@@ -27,72 +27,81 @@ __global__ void __launch_bounds__(256) scatter_clear_kernel(uint4* table, long l
 }
 
 // One CTA per token: n_end (slots up to the last valid entry), fill (the row of the first valid one, 0 without any),
-// and with a table its entries.  A row selected twice by a token is entered once, with its lowest slot, and the
-// number of times in mult: the entries' contributions are equal.  An entry outside [-1, S) counts as empty and is
-// recorded as DSA_ERR_BAD_INDEX.
+// and with a table its entries.  A row selected more than once by a token is entered with its lowest slot and
+// flagged.  An entry outside [-1, S) counts as empty and is recorded as DSA_ERR_BAD_INDEX.
 __global__ void __launch_bounds__(256) scatter_build_kernel(const int* idx, int k, long long S, int* n_end, int* fill,
-                                                            uint16_t* table, int ld, uint16_t* mult) {
+                                                            uint16_t* table, int ld) {
   __shared__ int last, first;
-  __shared__ int times[sct::MAX_K];
   const int t = blockIdx.x;
   if (threadIdx.x == 0) { last = 0; first = sct::MAX_K; }
-  for (int i = threadIdx.x; i < k; i += blockDim.x) times[i] = 1;
   __syncthreads();
   pdl_allow_next();
   pdl_wait();
   const int* row = idx + static_cast<long long>(t) * k;
   auto valid = [&](int e) { return e >= 0 && e < S; };
   auto cell = [&](int e) { return table + static_cast<long long>(e) * ld + t; };
+  constexpr int PER = sct::MAX_K / 256;
+  int e[PER];
   int my_last = 0, my_first = sct::MAX_K;
-  for (int i = threadIdx.x; i < k; i += blockDim.x) {
-    const int e = row[i];
-    if (valid(e)) {
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    const int i = u * 256 + threadIdx.x;
+    e[u] = i < k ? row[i] : -1;
+    if (valid(e[u])) {
       my_last = i + 1;
       my_first = min(my_first, i);
-      if (table) *cell(e) = static_cast<uint16_t>(i);
-    } else if (e != -1) {
+      if (table) *cell(e[u]) = static_cast<uint16_t>(i);
+    } else if (e[u] != -1) {
       raise_status(DSA_ERR_BAD_INDEX);
+      e[u] = -1;
     }
   }
-  atomicMax(&last, my_last);
-  atomicMin(&first, my_first);
+  my_last = __reduce_max_sync(0xffffffffu, my_last);
+  my_first = __reduce_min_sync(0xffffffffu, my_first);
+  if (lane_id() == 0) {
+    atomicMax(&last, my_last);
+    atomicMin(&first, my_first);
+  }
   __syncthreads();
   if (threadIdx.x == 0) {
     n_end[t] = last;
     fill[t] = first < k ? row[first] : 0;
   }
   if (!table) return;
-  // the lowest slot wins: repeated until no slot is below the one entered
+  // the lowest slot wins: repeated until no slot is below the one entered (one round where no row repeats)
+  bool again = false;
   while (true) {
     bool moved = false;
-    for (int i = threadIdx.x; i < k; i += blockDim.x) {
-      const int e = row[i];
-      if (valid(e) && __ldcg(cell(e)) > i) {
-        *cell(e) = static_cast<uint16_t>(i);
-        moved = true;
+    again = false;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int i = u * 256 + threadIdx.x;
+      if (e[u] >= 0) {
+        const int won = __ldcg(cell(e[u]));
+        if (won > i) {
+          *cell(e[u]) = static_cast<uint16_t>(i);
+          moved = true;
+        }
+        again |= won != i;
       }
     }
     if (!__syncthreads_or(moved)) break;
   }
-  bool again = false;
-  for (int i = threadIdx.x; i < k; i += blockDim.x) {
-    const int e = row[i];
-    if (!valid(e)) continue;
-    const int won = __ldcg(cell(e));
-    if (won != i) { atomicAdd(&times[won], 1); again = true; }
-  }
-  if (!__syncthreads_or(again)) return;
-  for (int i = threadIdx.x; i < k; i += blockDim.x)
-    if (times[i] > 1) {
-      *cell(row[i]) = static_cast<uint16_t>(i) | sct::TWICE;
-      mult[static_cast<long long>(t) * k + i] = static_cast<uint16_t>(times[i]);
+  // the last round's reads saw the final slots: whoever is not the winner flags the row
+  if (again) {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      if (e[u] < 0) continue;
+      const int won = __ldcg(cell(e[u])) & (sct::TWICE - 1);
+      if (won != u * 256 + static_cast<int>(threadIdx.x)) *cell(e[u]) = static_cast<uint16_t>(won | sct::TWICE);
     }
+  }
 }
 
 struct ScatterParams {
   const uint16_t* contrib;    // [T * kp, W] bf16
   const uint16_t* table;      // [S, ld]
-  const uint16_t* mult;       // [T, k]
+  const int* idx;             // [T, k]
   int T, ld, k, kp;
   float* acc;                 // [S, W] sums of the chunks so far, or null (one chunk)
   int first, last;            // first / last chunk
@@ -100,84 +109,121 @@ struct ScatterParams {
 };
 
 // One CTA per row: W / 8 threads hold the row's W values (16-byte loads), as many groups of them as fit the CTA take
-// equal runs of the row's list, four rows in flight each.
+// equal runs of the row's list, eight rows in flight each.
 template <int W>
 struct ScatterCfg {
   static constexpr int PER_ROW = W / 8;
-  static constexpr int GROUPS = 288 / PER_ROW;        // 4 (W = 576), 18 (128), 36 (64)
-  static constexpr int THREADS = GROUPS * PER_ROW;    // 288
+  static constexpr int GROUPS = W == 576 ? 2 : 160 / PER_ROW;   // 2 (W = 576), 10 (128), 20 (64)
+  static constexpr int THREADS = GROUPS * PER_ROW;              // 144, 160, 160
+  static constexpr int WARPS = (THREADS + 31) / 32;
+  static constexpr int SCAN = (sct::MAX_T / 8 + THREADS - 1) / THREADS;   // 16-byte table reads of a thread
 };
 
 template <int W>
-__global__ void __launch_bounds__(ScatterCfg<W>::THREADS) scatter_sum_kernel(const ScatterParams p) {
+__global__ void __launch_bounds__(ScatterCfg<W>::THREADS, 6) scatter_sum_kernel(const ScatterParams p) {
   using C = ScatterCfg<W>;
-  static_assert(C::THREADS % 32 == 0, "whole warps");
   __shared__ uint32_t list[sct::MAX_T];
-  __shared__ int warp_n[C::THREADS / 32];
-  __shared__ float part[C::GROUPS][W];
+  __shared__ int warp_n[C::WARPS];
+  __shared__ alignas(16) float part[C::GROUPS][W];
   pdl_allow_next();
   pdl_wait();
   const long long s = blockIdx.x;
-  const uint16_t* row = p.table + s * p.ld;
+  const uint4* row = reinterpret_cast<const uint4*>(p.table + s * p.ld);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int n = 0;
-  for (int t0 = 0; t0 < p.T; t0 += C::THREADS) {
-    const int t = t0 + threadIdx.x;
-    const uint16_t v = t < p.T ? row[t] : sct::EMPTY;
-    const uint32_t have = __ballot_sync(0xffffffffu, v != sct::EMPTY);
-    if (lane == 0) warp_n[warp] = __popc(have);
-    __syncthreads();
-    int at = n;
-    for (int w = 0; w < C::THREADS / 32; ++w) {
-      if (w < warp) at += warp_n[w];
-      n += warp_n[w];
+#pragma unroll
+  for (int it = 0; it < C::SCAN; ++it) {
+    // eight tokens a thread; the last warp may be half full, so every thread of it takes part in the exchange
+    const int at = it * C::THREADS + threadIdx.x;
+    if (it * C::THREADS * 8 >= p.ld) break;
+    const uint4 q = at < p.ld / 8 ? row[at] : make_uint4(~0u, ~0u, ~0u, ~0u);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    int mine = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) mine += ((w[u >> 1] >> (16 * (u & 1))) & 0xffffu) != sct::EMPTY;
+    const uint32_t in_warp = __activemask();
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(in_warp, upto, d);
+      if (lane >= d) upto += v;
     }
-    // token and slot; the flag goes to the top bit
-    if (v != sct::EMPTY)
-      list[at + __popc(have & ((1u << lane) - 1))] =
-          (static_cast<uint32_t>(t) << 11) | (v & (sct::TWICE - 1)) | ((v & sct::TWICE) ? 0x80000000u : 0u);
+    if (lane == 31 || threadIdx.x == C::THREADS - 1) warp_n[warp] = upto;
+    __syncthreads();
+    int to = n + upto - mine;
+#pragma unroll
+    for (int v = 0; v < C::WARPS; ++v) {
+      if (v < warp) to += warp_n[v];
+      n += warp_n[v];
+    }
+    // token, slot, and the flag in the top bit
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t v = (w[u >> 1] >> (16 * (u & 1))) & 0xffffu;
+      if (v != sct::EMPTY)
+        list[to++] = (static_cast<uint32_t>(8 * at + u) << 11) | (v & (sct::TWICE - 1)) | ((v & sct::TWICE) << 20);
+    }
     __syncthreads();
   }
   const int group = threadIdx.x / C::PER_ROW, col = threadIdx.x % C::PER_ROW;
   float sum[8] = {};
-  const int each = (n + C::GROUPS - 1) / C::GROUPS, end = min(n, (group + 1) * each);
-  for (int i = group * each; i < end; i += 4) {
-    uint4 v[4];
-    float m[4];
+  auto read = [&](uint32_t t, int slot) {
+    return __ldcs(reinterpret_cast<const uint4*>(p.contrib + (static_cast<long long>(t) * p.kp + slot) * W) + col);
+  };
+  auto add = [&](uint4 v) {
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      m[u] = 0.f;
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (i + u < end) {
-        const uint32_t e = list[i + u];
-        const long long t = (e >> 11) & 0xfffff;
-        const int slot = e & (sct::TWICE - 1);
-        v[u] = reinterpret_cast<const uint4*>(p.contrib + (t * p.kp + slot) * W)[col];
-        m[u] = (e >> 31) ? static_cast<float>(p.mult[t * p.k + slot]) : 1.f;
-      }
+    for (int q = 0; q < 4; ++q) {
+      sum[2 * q] += __uint_as_float(x[q] << 16);
+      sum[2 * q + 1] += __uint_as_float(x[q] & 0xffff0000u);
+    }
+  };
+  const int each = (n + C::GROUPS - 1) / C::GROUPS, end = min(n, (group + 1) * each);
+  for (int i = group * each; i < end; i += 8) {
+    uint4 v[8];
+    uint32_t any = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t e = i + u < end ? list[i + u] : 0;
+      any |= e;
+      v[u] = i + u < end ? read((e >> 11) & 0xfffff, e & (sct::TWICE - 1)) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-      if (i + u < end) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          sum[2 * q] = fmaf(m[u], __uint_as_float(x[q] << 16), sum[2 * q]);
-          sum[2 * q + 1] = fmaf(m[u], __uint_as_float(x[q] & 0xffff0000u), sum[2 * q + 1]);
-        }
+    for (int u = 0; u < 8; ++u) add(v[u]);
+    if (any >> 31) {                     // the row's later slots of a token that selected it more than once
+#pragma unroll 1
+      for (int u = i; u < min(end, i + 8); ++u) {
+        const uint32_t e = list[u], t = (e >> 11) & 0xfffff;
+        if (!(e >> 31)) continue;
+        const int* ids = p.idx + static_cast<long long>(t) * p.k;
+#pragma unroll 1
+        for (int j = (e & (sct::TWICE - 1)) + 1; j < p.k; ++j)
+          if (ids[j] == s) add(read(t, j));
       }
     }
   }
 #pragma unroll
   for (int q = 0; q < 8; ++q) part[group][8 * col + q] = sum[q];
   __syncthreads();
-  for (int d = threadIdx.x; d < W; d += C::THREADS) {
-    float total = 0.f;
-    for (int g = 0; g < C::GROUPS; ++g) total += part[g][d];
+  for (int d = 4 * threadIdx.x; d < W; d += 4 * C::THREADS) {
+    float4 total = *reinterpret_cast<const float4*>(&part[0][d]);
+#pragma unroll
+    for (int g = 1; g < C::GROUPS; ++g) {
+      const float4 v = *reinterpret_cast<const float4*>(&part[g][d]);
+      total.x += v.x; total.y += v.y; total.z += v.z; total.w += v.w;
+    }
     const long long at = s * W + d;
-    if (p.acc && !p.first) total += p.acc[at];
-    if (p.last) p.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(total));
-    else p.acc[at] = total;
+    if (p.acc && !p.first) {
+      const float4 v = *reinterpret_cast<const float4*>(p.acc + at);
+      total.x += v.x; total.y += v.y; total.z += v.z; total.w += v.w;
+    }
+    if (p.last) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(total.x, total.y), hi = __floats2bfloat162_rn(total.z, total.w);
+      *reinterpret_cast<uint2*>(p.out + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    } else {
+      *reinterpret_cast<float4*>(p.acc + at) = total;
+    }
   }
 }
 

@@ -1,0 +1,464 @@
+"""The training-side operators on the GPU against plain fp64 implementations: rotary positions, the sparse attention's
+backward pass, the gradient of the indexer's objective, the backward pass of the index scores, and a run of them
+together.
+
+Tolerances.  u = 2^-9 bounds bf16's rounding of a value on average over its mantissas and 2^-8 in the worst case
+(half a step).  A bf16 gradient is a sum of products whose factors were rounded at most twice (an operand of the
+product and the entry's contribution) plus its own rounding: each element is within 3 x 2^-8 of the sum of the
+products' sizes, taken here as a bound on the elements, and the relative L2 error of independent roundings stays below
+2^-8 (three of them of rms 2^-8 / sqrt(12) x sqrt(2) make 0.0033 at most; 2^-8 is 0.0039).  fp32 results that are sums
+of n fp32 terms with logits off by 2^-20 stay within 1e-5 in relative L2."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+D, DV = 576, 512
+SCALE = D ** -0.5
+L2_BF16 = 2.0 ** -8
+L2_FP32 = 1e-5
+
+
+@pytest.fixture(scope="module")
+def dsa():
+    import sparse_attention_long_05_b200 as m
+    return m
+
+
+def _rel(got, want):
+    got, want = got.double().cpu(), want.double().cpu()
+    assert torch.isfinite(got).all()
+    return float((got - want).norm() / want.norm().clamp(min=1e-300))
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _selection(T, S, k, g, kind):
+    """[T, k] int32 on the CPU.  causal: the last T positions of S, ascending; holes: unsorted, with -1 between;
+    twice: rows named several times; blank: every second token empty."""
+    idx = torch.full((T, k), -1, dtype=torch.int32)
+    for t in range(T):
+        n = min(k, S - T + t + 1)
+        if kind == "causal":
+            idx[t, :n] = torch.randperm(S - T + t + 1, generator=g)[:n].sort().values.int()
+        elif kind == "holes":
+            m = int(torch.randint(1, min(k, S) + 1, (1,), generator=g))
+            at = torch.randperm(k, generator=g)[:m]
+            idx[t, at] = torch.randperm(S, generator=g)[:m].int()
+        elif kind == "twice":
+            idx[t] = torch.randint(0, min(S, 40 + 5 * t), (k,), generator=g).int()
+            if t == 1:
+                idx[t] = 3
+        elif kind == "blank" and t % 2:
+            idx[t, :n] = torch.randperm(S - T + t + 1, generator=g)[:n].int()
+        elif kind == "one":
+            idx[t, k - 1] = (7 * t) % S
+    return idx
+
+
+def _attention(q, c, idx):
+    """fp64 out and lse of the forward, differentiable."""
+    on = idx >= 0
+    rows = c[idx.clamp(min=0).long()]
+    x = torch.einsum("thd,tkd->thk", q, rows) * SCALE
+    x = x.masked_fill(~on[:, None], -math.inf)
+    lse = torch.logsumexp(x, 2)
+    p = torch.where(on[:, None], (x - torch.where(lse.isinf(), 0.0, lse)[..., None]).exp(), 0.0)
+    return torch.einsum("thk,tkd->thd", p, rows[..., :DV]), lse, p, rows
+
+
+def _attention_case(T, S, H, k, kind, seed):
+    g = _gen(seed)
+    q = torch.randn(T, H, D, generator=g).bfloat16()
+    c = torch.randn(S, D, generator=g).bfloat16()
+    dout = torch.randn(T, H, DV, generator=g).bfloat16()
+    return q, c, _selection(T, S, k, g, kind), dout
+
+
+def _formula(q, c, idx, out, lse, dout):
+    """dq, dc from the definition, with the given out and lse (fp64)."""
+    q, c, out, lse, dout = (t.double() for t in (q, c, out, lse, dout))
+    on = (idx >= 0)[:, None]
+    rows = c[idx.clamp(min=0).long()]
+    p = torch.where(on, (torch.einsum("thd,tkd->thk", q, rows) * SCALE - lse[..., None]).exp(), 0.0)
+    dp = torch.einsum("thd,tkd->thk", dout, rows[..., :DV])
+    ds = SCALE * p * (dp - (dout * out).sum(-1, keepdim=True))
+    each = torch.einsum("thk,thd->tkd", ds, q)
+    each[..., :DV] += torch.einsum("thk,thd->tkd", p, dout)
+    dc = torch.zeros_like(c).index_add_(0, idx.clamp(min=0).long().flatten(), each.flatten(0, 1))
+    return torch.einsum("thk,tkd->thd", ds, rows), dc
+
+
+def _run_attention(dsa, q, c, idx, dout, **kw):
+    qd, cd, idxd, dd = (t.cuda() for t in (q, c, idx, dout))
+    out, lse = dsa.dsa_sparse_mla_attn(qd, cd, idxd, SCALE)
+    dq, dc = dsa.dsa_sparse_mla_attn_backward(qd, cd, idxd, out, lse, dd, SCALE, **kw)
+    assert dsa.dsa_get_device_status() == 0
+    return out, lse, dq, dc
+
+
+CASES = [(1, 1, 1, 128, "causal"), (1, 300, 128, 128, "causal"), (3, 130, 8, 192, "causal"), (5, 700, 64, 320, "holes"),
+         (9, 200, 65, 128, "twice"), (8, 150, 37, 128, "blank"), (4, 50, 128, 256, "one"), (17, 2300, 128, 2048, "causal"),
+         (160, 161, 16, 128, "causal"), (6, 900, 128, 576, "holes")]
+
+
+@pytest.mark.parametrize("T,S,H,k,kind", CASES)
+def test_attention_backward(dsa, T, S, H, k, kind):
+    q, c, idx, dout = _attention_case(T, S, H, k, kind, 11 * T + S)
+    out, lse, dq, dc = _run_attention(dsa, q, c, idx, dout)
+    want_q, want_c = _formula(q, c, idx, out.cpu(), lse.cpu(), dout)
+    # a single selected key has P = 1 and dP = delta up to the rounding of out: dS is rounding alone, bounded absolutely
+    if S == 1 or kind == "one":
+        size = SCALE * (dout.double().norm(dim=2).max() * c.double().norm(dim=1).max()) * 2.0 ** -7
+        assert (dq.double().cpu() - want_q).abs().max() <= size * c.double().abs().max()
+    else:
+        assert _rel(dq, want_q) <= L2_BF16
+    assert _rel(dc, want_c) <= L2_BF16
+    unused = torch.ones(S, dtype=torch.bool)
+    unused[idx[idx >= 0].long()] = False
+    assert (dc.cpu()[unused] == 0).all()
+    assert (dq.cpu()[(idx < 0).all(1)] == 0).all()
+
+
+def test_attention_backward_matches_autograd(dsa):
+    # the formula itself, against automatic differentiation of the forward in fp64
+    q, c, idx, dout = _attention_case(5, 260, 24, 192, "holes", 3)
+    qd, cd = q.double().requires_grad_(), c.double().requires_grad_()
+    out = _attention(qd, cd, idx)[0]
+    out.backward(dout.double())
+    _, _, dq, dc = _run_attention(dsa, q, c, idx, dout)
+    # the forward's out is rounded to bf16 before delta is formed: one rounding more than _formula has
+    assert _rel(dq, qd.grad) <= 2 * L2_BF16 and _rel(dc, cd.grad) <= 2 * L2_BF16
+
+
+def test_attention_backward_is_the_slope(dsa):
+    # against differences of the fp64 forward along random directions
+    q, c, idx, dout = _attention_case(3, 150, 16, 128, "causal", 5)
+    _, _, dq, dc = _run_attention(dsa, q, c, idx, dout)
+    g = _gen(6)
+    h = 1e-4
+    for name, x, dx in (("q", q, dq), ("c", c, dc)):
+        v = torch.randn(x.shape, generator=g).double()
+        a = {"q": q.double(), "c": c.double()}
+        lo, hi = dict(a), dict(a)
+        lo[name], hi[name] = a[name] - h * v, a[name] + h * v
+        slope = ((_attention(hi["q"], hi["c"], idx)[0] - _attention(lo["q"], lo["c"], idx)[0]) * dout.double()).sum() / (2 * h)
+        got = (dx.double().cpu() * v).sum()
+        # the error of the projection: the gradient's relative L2 error times its norm (v is unit normal), five sigma
+        assert abs(got - slope) <= 5 * 2 * L2_BF16 * dx.double().norm().cpu()
+
+
+def test_attention_backward_in_chunks_and_repeated(dsa):
+    # more tokens than one chunk holds, over many rows; repeated calls agree bit for bit and reuse a workspace
+    T, S, H, k = 300, 70001, 16, 2048
+    g = _gen(8)
+    q = torch.randn(T, H, D, generator=g).bfloat16().cuda()
+    c = torch.randn(S, D, generator=g).bfloat16().cuda()
+    dout = torch.randn(T, H, DV, generator=g).bfloat16().cuda()
+    idx = torch.randint(0, S, (T, k), generator=g).int().cuda()
+    idx[:, 0] = 5                                        # one row that every token selects
+    out, lse = dsa.dsa_sparse_mla_attn(q, c, idx, SCALE)
+    need = dsa.dsa_sparse_mla_attn_backward_workspace_size(T, S, H, k)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    dq, dc = dsa.dsa_sparse_mla_attn_backward(q, c, idx, out, lse, dout, SCALE, ws=ws)
+    ws.fill_(0xab)
+    dq2, dc2 = dsa.dsa_sparse_mla_attn_backward(q, c, idx, out, lse, dout, SCALE, ws=ws)
+    assert torch.equal(dq, dq2) and torch.equal(dc, dc2)
+    assert dsa.dsa_get_device_status() == 0
+    want_q, want_c = torch.empty(T, H, D, dtype=torch.float64), torch.zeros(S, D, dtype=torch.float64, device="cuda")
+    for a in range(0, T, 50):
+        b = slice(a, a + 50)
+        x, y = _formula(q[b], c, idx[b], out[b], lse[b], dout[b])
+        want_q[b] = x.cpu()
+        want_c += y
+    assert _rel(dq, want_q) <= L2_BF16 and _rel(dc, want_c) <= L2_BF16
+
+
+def test_attention_backward_nan_rows_nobody_selects(dsa):
+    q, c, idx, dout = _attention_case(6, 400, 20, 192, "holes", 9)
+    used = torch.zeros(400, dtype=torch.bool)
+    used[idx[idx >= 0].long()] = True
+    idx[2] = -1                                          # an empty token with NaN queries
+    clean = _run_attention(dsa, q, c, idx, dout)
+    c2, q2 = c.clone(), q.clone()
+    used = torch.zeros(400, dtype=torch.bool)
+    used[idx[idx >= 0].long()] = True
+    c2[~used] = math.nan
+    q2[2] = math.nan
+    out, lse = (t.cuda() for t in (clean[0].cpu(), clean[1].cpu()))
+    dq, dc = dsa.dsa_sparse_mla_attn_backward(q2.cuda(), c2.cuda(), idx.cuda(), out, lse, dout.cuda(), SCALE)
+    assert torch.equal(dq, clean[2]) and torch.equal(dc, clean[3])
+
+
+def test_bad_indices_are_recorded_and_skipped(dsa):
+    q, c, idx, dout = _attention_case(4, 300, 16, 128, "causal", 12)
+    _, _, dq, dc = _run_attention(dsa, q, c, idx, dout)
+    out, lse = dsa.dsa_sparse_mla_attn(q.cuda(), c.cuda(), idx.cuda(), SCALE)
+    bad = torch.cat([idx, torch.full((4, 64), -1, dtype=torch.int32)], 1)
+    bad[0, 130], bad[2, 140], bad[3, 150] = 300, -2, 2 ** 31 - 1
+    dq2, dc2 = dsa.dsa_sparse_mla_attn_backward(q.cuda(), c.cuda(), bad.cuda(), out, lse, dout.cuda(), SCALE)
+    assert dsa.dsa_get_device_status() == 6             # DSA_ERR_BAD_INDEX
+    assert torch.equal(dq, dq2) and torch.equal(dc, dc2)
+
+
+# ------------------------------------------------------------------------------------------------ indexer objective
+@pytest.mark.parametrize("T,S,H,k,kind", [c for c in CASES if c[4] != "one" and c[1] > 1] + [(4, 50, 128, 256, "one")])
+def test_objective_backward(dsa, T, S, H, k, kind):
+    q, c, idx, _ = _attention_case(T, S, H, k, kind, 5 * T + S)
+    g = _gen(T)
+    sel, dkl = 3 * torch.randn(T, k, generator=g), torch.randn(T, generator=g)
+    qd, cd, idxd = q.cuda(), c.cuda(), idx.cuda()
+    _, lse = dsa.dsa_sparse_mla_attn(qd, cd, idxd, SCALE)
+    got = dsa.dsa_indexer_kl_backward(qd, cd, idxd, sel.cuda(), lse, dkl.cuda(), SCALE)
+    assert dsa.dsa_get_device_status() == 0
+    _, _, p, _ = _attention(q.double(), c.double(), idx)
+    target = p.sum(1)
+    target = target / target.sum(1, keepdim=True).clamp(min=1e-300)
+    x = sel.double().requires_grad_()
+    on = idx >= 0
+    logq = torch.log_softmax(x.masked_fill(~on, -1e300), 1)
+    kl = torch.where(on & (target > 0), target * (target.clamp(min=1e-300).log() - logq), 0.0).sum(1)
+    kl.backward(dkl.double())
+    want = torch.where(on, x.grad, 0.0)
+    if kind == "one":
+        assert (got.double().cpu() - want).abs().max() <= 1e-6 * float(dkl.abs().max())
+    else:
+        assert _rel(got, want) <= L2_FP32
+    assert (got.cpu()[~on] == 0).all()
+    # without a gradient of the divergences every token counts once
+    ones = dsa.dsa_indexer_kl_backward(qd, cd, idxd, sel.cuda(), lse, None, SCALE)
+    assert torch.equal(ones, dsa.dsa_indexer_kl_backward(qd, cd, idxd, sel.cuda(), lse, torch.ones(T, device="cuda"), SCALE))
+
+
+# ------------------------------------------------------------------------------------------------ index scores
+def _indexer_case(T, S, heads, dim, k, kind, scaled, seed):
+    g = _gen(seed)
+    if scaled:
+        q, kk = torch.randn(T, heads, dim, generator=g), torch.randn(S, dim, generator=g)
+        qs, ks = q.abs().amax((1, 2)) / 448, kk.abs().amax(1) / 448
+        q, kk = (q / qs[:, None, None]).clamp(-448, 448), (kk / ks[:, None]).clamp(-448, 448)
+        w = torch.randn(T, heads, generator=g) * heads ** -0.5
+    else:
+        q = torch.randint(-7, 8, (T, heads, dim), generator=g).float()
+        kk = torch.randint(-7, 8, (S, dim), generator=g).float()
+        qs = ks = None
+        w = torch.randint(-3, 4, (T, heads), generator=g).float()
+    idx = _selection(T, S, k, g, kind)
+    return q.to(torch.float8_e4m3fn), qs, kk.to(torch.float8_e4m3fn), ks, w, idx, torch.randn(T, k, generator=g) / k
+
+
+def _indexer_scores(q, k, w, idx):
+    x = torch.einsum("thd,tkd->thk", q, k[idx.clamp(min=0).long()]).relu()
+    return torch.einsum("th,thk->tk", w, x)
+
+
+@pytest.mark.parametrize("heads,dim", [(64, 128), (4, 64)])
+@pytest.mark.parametrize("T,S,k,kind,scaled", [(1, 1, 128, "causal", False), (3, 130, 192, "causal", True),
+                                               (5, 700, 320, "holes", True), (9, 200, 128, "twice", True),
+                                               (8, 150, 128, "blank", False), (4, 50, 256, "one", True),
+                                               (17, 2300, 2048, "causal", True), (160, 161, 128, "causal", False)])
+def test_index_scores_backward(dsa, heads, dim, T, S, k, kind, scaled):
+    q, qs, kk, ks, w, idx, dsel = _indexer_case(T, S, heads, dim, k, kind, scaled, 7 * T + S)
+    dev = [None if t is None else t.cuda() for t in (q, qs, kk, ks, w, idx, dsel)]
+    dq, dk, dw = dsa.dsa_indexer_scores_backward(*dev)
+    assert dsa.dsa_get_device_status() == 0
+    qf, kf = q.float().double(), kk.float().double()
+    if scaled:
+        qf, kf = qf * qs.double()[:, None, None], kf * ks.double()[:, None]
+    qf, kf, wf = qf.requires_grad_(), kf.requires_grad_(), w.double().requires_grad_()
+    on = idx >= 0
+    (_indexer_scores(qf, kf, wf, idx) * torch.where(on, dsel.double(), 0.0)).sum().backward()
+    assert _rel(dq, qf.grad) <= L2_BF16
+    assert _rel(dk, kf.grad) <= L2_BF16
+    assert _rel(dw, wf.grad) <= L2_FP32
+    unused = torch.ones(S, dtype=torch.bool)
+    unused[idx[on].long()] = False
+    assert (dk.cpu()[unused] == 0).all()
+    again = dsa.dsa_indexer_scores_backward(*dev)
+    assert all(torch.equal(a, b) for a, b in zip((dq, dk, dw), again))
+
+
+def test_index_scores_backward_is_the_slope_of_the_forward(dsa):
+    # dw against the forward kernel itself: the scores are linear in w
+    q, qs, kk, ks, w, idx, dsel = _indexer_case(6, 500, 64, 128, 192, "causal", True, 4)
+    dev = [t.cuda() for t in (q, qs, kk, ks, w, idx, dsel)]
+    _, _, dw = dsa.dsa_indexer_scores_backward(*dev)
+    v = torch.randn(w.shape, generator=_gen(5)).cuda()
+    scores = dsa.dsa_indexer_scores(dev[0], dev[1], dev[2], dev[3], v, pos0=500)
+    up = torch.where(dev[5] >= 0, scores.gather(1, dev[5].clamp(min=0).long()) * dev[6], 0.0).double().sum()
+    size = (scores.abs().max() * dev[6].abs().sum()).item()
+    assert abs(float((dw.double() * v.double()).sum() - up)) <= 1e-6 * size
+
+
+# ------------------------------------------------------------------------------------------------ rotary positions
+def _rope_reference(x, f, pos, off, inter, m, backward):
+    y = x.double().clone()
+    R = 2 * len(f)
+    theta = pos.double()[:, None] * f.double()[None]
+    cos, sin = m * theta.cos()[:, None], m * theta.sin()[:, None] * (-1 if backward else 1)
+    a, b = (slice(off, off + R, 2), slice(off + 1, off + R, 2)) if inter else (slice(off, off + R // 2), slice(off + R // 2, off + R))
+    y[..., a], y[..., b] = x.double()[..., a] * cos - x.double()[..., b] * sin, x.double()[..., a] * sin + x.double()[..., b] * cos
+    return y
+
+
+def _rope_close(got, want, x, m):
+    # half a step of the type, plus the angle's fp32 sine (2^-20 for bf16, 2^-22 for fp32) times the pair's size
+    eps = torch.finfo(got.dtype).eps / 2
+    slack = (2.0 ** -20 if got.dtype == torch.bfloat16 else 2.0 ** -21) * 2 * m * float(x.abs().max())
+    err = (got.double().cpu() - want).abs()
+    assert bool((err <= want.abs() * eps * (1 + 2.0 ** -6) + slack).all()), float(err.max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inter", [True, False])
+@pytest.mark.parametrize("T,H,D,R,off", [(1, 1, 64, 64, 0), (3, 128, 576, 64, 512), (7, 5, 128, 64, 0), (130, 1, 72, 16, 8),
+                                         (2, 3, 11, 6, 3), (33, 64, 128, 128, 0), (5, 2, 96, 24, 40)])
+def test_rope(dsa, dtype, inter, T, H, D, R, off):
+    g = _gen(T + D)
+    x = torch.randn(T, H, D, generator=g).to(dtype)
+    pos = torch.randint(0, 1_000_000, (T,), generator=g, dtype=torch.int32)
+    f, m = dsa.dsa_rope_frequencies(R, 10000.0, factor=8.0, orig_len=4096)
+    fd, xd, pd = f.cuda(), x.cuda(), pos.cuda()
+    y = dsa.dsa_rope(xd, fd, pd, rot_off=off, interleaved=inter, mscale=m)
+    assert torch.equal(xd.cpu(), x)
+    want = _rope_reference(x, f, pos, off, inter, m, False)
+    _rope_close(y, want, x, m)
+    keep = [d for d in range(D) if not off <= d < off + R]
+    assert torch.equal(y.cpu()[..., keep], x[..., keep])
+    # in place, and the gradient: the transpose
+    inpl = xd.clone()
+    assert dsa.dsa_rope(inpl, fd, pd, rot_off=off, interleaved=inter, mscale=m, out=inpl) is inpl
+    assert torch.equal(inpl, y)
+    back = dsa.dsa_rope_backward(xd, fd, pd, rot_off=off, interleaved=inter, mscale=m)
+    _rope_close(back, _rope_reference(x, f, pos, off, inter, m, True), x, m)
+
+
+def test_rope_strides_offsets_and_positions(dsa):
+    g = _gen(1)
+    f = dsa.dsa_rope_frequencies(64)[0].cuda()
+    wide = torch.randn(20, 8, 576, generator=g).bfloat16().cuda()
+    q = wide[:, :, 512:]                                                     # the position dims of wider rows
+    want = _rope_reference(q.cpu(), f.cpu(), torch.arange(20) + 90, 0, True, 1.0, False)
+    _rope_close(dsa.dsa_rope(q, f, pos0=90), want, q.cpu(), 1.0)
+    flipped = wide.transpose(0, 1)[:, :, 512:]                               # heads outermost
+    pos = torch.arange(8, dtype=torch.int32, device="cuda") * 1000
+    got = dsa.dsa_rope(flipped, f, pos)
+    _rope_close(got, _rope_reference(flipped.cpu(), f.cpu(), pos.cpu(), 0, True, 1.0, False), wide.cpu(), 1.0)
+    odd = torch.randn(9, 3, 67, generator=g).bfloat16().cuda()[:, :, 1:65]   # rows that no 16-byte piece fits
+    _rope_close(dsa.dsa_rope(odd, f, pos0=5, interleaved=False),
+                _rope_reference(odd.cpu(), f.cpu(), torch.arange(9) + 5, 0, False, 1.0, False), odd.cpu(), 1.0)
+    # in place on a view: the rest of the rows stays
+    before = wide.clone()
+    dsa.dsa_rope(q, f, pos0=90, out=q)
+    assert torch.equal(wide[..., :512], before[..., :512])
+    _rope_close(q, want, before.cpu(), 1.0)
+    # into the gaps of the same buffer
+    both = torch.randn(6, 1, 128, generator=g).cuda()
+    x, out = both[..., :64], both[..., 64:]
+    keep = x.clone()
+    dsa.dsa_rope(x, f, pos0=3, out=out)
+    assert torch.equal(x, keep)
+    _rope_close(out, _rope_reference(keep.cpu(), f.cpu(), torch.arange(6) + 3, 0, True, 1.0, False), keep.cpu(), 1.0)
+    # one input row for every token
+    row = torch.randn(1, 4, 64, generator=g).cuda().expand(5, 4, 64)
+    _rope_close(dsa.dsa_rope(row, f), _rope_reference(row.cpu(), f.cpu(), torch.arange(5), 0, True, 1.0, False), row.cpu(), 1.0)
+    assert dsa.dsa_rope(both[:0], f).shape == (0, 1, 128)
+
+
+# ------------------------------------------------------------------------------------------------ together
+def _training_step(dsa, s, stream=None):
+    """One step of a layer: positions, attention, its backward pass, the objective's gradient, the indexer's."""
+    qr = dsa.dsa_rope(s["q"], s["f"], rot_off=512, pos0=s["pos0"], stream=stream)
+    cr = dsa.dsa_rope(s["c"].unsqueeze(1), s["f"], rot_off=512, stream=stream).squeeze(1)
+    out, lse = dsa.dsa_sparse_mla_attn(qr, cr, s["idx"], SCALE, stream=stream)
+    dq, dc = dsa.dsa_sparse_mla_attn_backward(qr, cr, s["idx"], out, lse, s["dout"], SCALE, stream=stream)
+    dq = dsa.dsa_rope_backward(dq, s["f"], rot_off=512, pos0=s["pos0"], dx=dq, stream=stream)
+    dc = dsa.dsa_rope_backward(dc.unsqueeze(1), s["f"], rot_off=512, stream=stream).squeeze(1)
+    dsel = dsa.dsa_indexer_kl_backward(qr, cr, s["idx"], s["sel"], lse, None, SCALE, stream=stream)
+    return (dq, dc) + dsa.dsa_indexer_scores_backward(s["q_idx"], s["qs"], s["k_idx"], s["ks"], s["w"], s["idx"], dsel, stream=stream)
+
+
+def _step_inputs(dsa, seed, T=24, S=400, H=32, k=192):
+    q, c, idx, dout = _attention_case(T, S, H, k, "causal", seed)
+    qi, qs, ki, ks, w, _, _ = _indexer_case(T, S, 64, 128, k, "causal", True, seed)
+    s = dict(q=q, c=c, idx=idx, dout=dout, q_idx=qi, qs=qs, k_idx=ki, ks=ks, w=w, sel=torch.randn(T, k, generator=_gen(seed)))
+    s = {n: t.cuda() for n, t in s.items()}
+    return dict(s, f=dsa.dsa_rope_frequencies(64)[0].cuda(), pos0=S - T)
+
+
+def test_training_step(dsa):
+    s = _step_inputs(dsa, 21)
+    got = _training_step(dsa, s)
+    h = {n: t.cpu() for n, t in s.items() if isinstance(t, torch.Tensor)}
+    T, S = h["q"].shape[0], h["c"].shape[0]
+    q, c = h["q"].double().requires_grad_(), h["c"].double().requires_grad_()
+
+    def turn(x, pos):
+        theta = pos.double()[:, None] * h["f"][None]
+        cos, sin = theta.cos(), theta.sin()
+        a, b = x[..., 512::2], x[..., 513::2]
+        if x.dim() == 3:
+            cos, sin = cos[:, None], sin[:, None]
+        return torch.cat([x[..., :512], torch.stack([a * cos - b * sin, a * sin + b * cos], -1).flatten(-2)], -1)
+
+    qr, cr = turn(q, torch.arange(T) + S - T), turn(c, torch.arange(S))
+    out, _, p, _ = _attention(qr, cr, h["idx"])
+    out.backward(h["dout"].double())
+    # the rotated dims are rounded to bf16 before and after the products: two roundings more
+    assert _rel(got[0], q.grad) <= 4 * L2_BF16 and _rel(got[1], c.grad) <= 4 * L2_BF16
+    on = h["idx"] >= 0
+    target = p.detach().sum(1) / p.shape[1]
+    dsel = torch.where(on, torch.softmax(h["sel"].double().masked_fill(~on, -1e300), 1) - target, 0.0)
+    qf = (h["q_idx"].float().double() * h["qs"].double()[:, None, None]).requires_grad_()
+    kf = (h["k_idx"].float().double() * h["ks"].double()[:, None]).requires_grad_()
+    wf = h["w"].double().requires_grad_()
+    (_indexer_scores(qf, kf, wf, h["idx"]) * dsel).sum().backward()
+    for a, b in zip(got[2:], (qf.grad, kf.grad, wf.grad)):
+        assert _rel(a, b) <= 2 * L2_BF16
+
+
+def test_training_step_on_streams_and_in_graphs(dsa):
+    a, b = _step_inputs(dsa, 31), _step_inputs(dsa, 32)
+    want_a, want_b = _training_step(dsa, a), _training_step(dsa, b)
+    torch.cuda.synchronize()
+    # two calls at once on streams of their own
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    ga, gb = _training_step(dsa, a, sa), _training_step(dsa, b, sb)
+    torch.cuda.synchronize()
+    for x, y in zip(ga + gb, want_a + want_b):
+        assert torch.equal(x, y)
+    # captured, replayed on new contents of the same buffers, two graphs in turn
+    graphs, outs = [], []
+    for s in (a, b):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(_training_step(dsa, s))
+        graphs.append(graph)
+    for n, t in a.items():
+        if isinstance(t, torch.Tensor) and n != "f":
+            t.copy_(b[n])
+    for _ in range(2):
+        graphs[0].replay()
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    for x, y in zip(outs[0] + outs[1], want_b + want_b):
+        assert torch.equal(x, y)
+    assert dsa.dsa_get_device_status() == 0
+
+
+def test_empty_work(dsa):
+    c = torch.randn(30, D).bfloat16().cuda()
+    e = lambda *shape, dt=torch.bfloat16: torch.empty(*shape, dtype=dt, device="cuda")
+    dq, dc = dsa.dsa_sparse_mla_attn_backward(e(0, 8, D), c, e(0, 128, dt=torch.int32), e(0, 8, DV),
+                                              e(0, 8, dt=torch.float32), e(0, 8, DV), SCALE, dc=torch.ones_like(c))
+    assert dq.shape == (0, 8, D) and (dc == 0).all()
+    k = torch.zeros(30, 128, device="cuda").to(torch.float8_e4m3fn)
+    _, dk, dw = dsa.dsa_indexer_scores_backward(e(0, 64, 128, dt=torch.float8_e4m3fn), None, k, None,
+                                                e(0, 64, dt=torch.float32), e(0, 128, dt=torch.int32),
+                                                e(0, 128, dt=torch.float32), dk=torch.ones(30, 128, device="cuda").bfloat16())
+    assert (dk == 0).all() and dw.shape == (0, 64)
