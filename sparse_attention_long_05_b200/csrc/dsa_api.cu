@@ -751,7 +751,7 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
   const size_t rows = size_t(w.Tc) * w.kp;
   if (!make_heads_map(&tq, q, T, H, mbw::D) || !make_heads_map(&tdo, dout, T, H, mbw::DV) ||
       !make_rows_map(&tc, c, S, mbw::D, 1) || !make_rows_map(&tp128, w.pds, rows, 2 * w.HP, 128) ||
-      !make_rows_map(&tp64, w.pds, rows, 2 * w.HP, 64) || !make_rows_map(&tout, w.sc.contrib, rows, mbw::D, 128))
+      !make_rows_map(&tp64, w.pds, rows, 2 * w.HP, 64) || !make_rows_map(&tout, w.sc.contrib, rows, mbw::D, 32))
     return DSA_ERR_CUDA;
   if (set_smem(mla_bwd_p_kernel<false>, mbw::p::Map<false>::SMEM) != cudaSuccess ||
       set_smem(mla_bwd_dc_kernel, mbw::dc::SMEM) != cudaSuccess ||
@@ -785,7 +785,7 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
                    dout + o * H * mbw::DV, out + o * H * mbw::DV, dr, w.delta) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
-    if (launch_pdl(mla_bwd_p_kernel<false>, dim3(std::min(sms, n * (w.HP / 64))), dim3(mbw::p::THREADS),
+    if (launch_pdl(mla_bwd_p_kernel<false>, dim3(2 * std::min(sms / 2, n)), dim3(mbw::p::THREADS),
                    mbw::p::Map<false>::SMEM, st, tq, tdo, tc, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
@@ -835,7 +835,7 @@ dsa_status_t run_kl_bwd(const uint16_t* q, const uint16_t* c, int S, const int32
   const dsa_status_t e = last_launch_status();
   if (e != DSA_OK) return e;
   if (set_smem(mla_bwd_p_kernel<true>, mbw::p::Map<true>::SMEM) != cudaSuccess) return DSA_ERR_CUDA;
-  if (launch_pdl(mla_bwd_p_kernel<true>, dim3(std::min(num_sms(), T)), dim3(mbw::p::THREADS),
+  if (launch_pdl(mla_bwd_p_kernel<true>, dim3(2 * std::min(num_sms() / 2, T)), dim3(mbw::p::THREADS),
                  mbw::p::Map<true>::SMEM, st, tq, tq, tc, p) != cudaSuccess)
     return DSA_ERR_CUDA;
   return last_launch_status();
@@ -860,7 +860,7 @@ IndexBwdWs index_bwd_ws(void* ws, int T, int64_t S, int d_I, int k) {
 template <int HI, int DI>
 dsa_status_t run_index_bwd(IndexerBwdParams p, int T, uint16_t* dk, const IndexBwdWs& w, cudaStream_t st) {
   CUtensorMap tout;
-  if (!make_rows_map(&tout, w.sc.contrib, static_cast<long long>(w.Tc) * w.kp, DI, 128)) return DSA_ERR_CUDA;
+  if (!make_rows_map(&tout, w.sc.contrib, static_cast<long long>(w.Tc) * w.kp, DI, 32)) return DSA_ERR_CUDA;
   if (set_smem(indexer_bwd_kernel<HI, DI>, ixb::SMEM) != cudaSuccess) return DSA_ERR_CUDA;
   p.n_end = w.sc.n_end;
   p.kp = w.kp;

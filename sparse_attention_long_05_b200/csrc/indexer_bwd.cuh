@@ -348,7 +348,6 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
     // ===================================================================== contributions to dk, and dq (w14..17)
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
-    const bool leader = warp == 16 && lane == 0;
     int g = 0;
     for (int t = blockIdx.x; t < p.T && ok; t += gridDim.x) {
       const int tiles = tiles_of(t);
@@ -360,35 +359,36 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
       const float qs = p.q_scale ? p.q_scale[t] : 1.f;
       for (int j = 0; j < tiles; ++j, ++g) {
         const int s = g & 1;
-        if (leader) bulk_wait_read();
-        ok = warp_wait(cta.bar(B_DK_FULL + s), (g >> 1) & 1, abort_flag);
-        if (!(ok = named_bar_all(2, 128, ok))) break;
+        if (!(ok = warp_wait(cta.bar(B_DK_FULL + s), (g >> 1) & 1, abort_flag))) break;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < DI / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld32(lane_addr + tmem + TDK + 128 * s + 32 * c, v);
+        for (int c = 0; c < DI / 64; ++c) {
+          // each warp stages and stores its own 32 rows, 64 dims at a time
+          uint32_t v[64];
+          uint32_t (&v0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
+          uint32_t (&v1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32]);
+          tmem_ld32(lane_addr + tmem + TDK + 128 * s + 64 * c, v0);
+          tmem_ld32(lane_addr + tmem + TDK + 128 * s + 64 * c + 32, v1);
+          if (lane == 0) bulk_wait_read<DI / 64 - 1>();
+          __syncwarp();
           tmem_wait_ld();
-          if (c == DI / 32 - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(cta.bar(B_DK_EMPTY + s));
-          }
-          uint8_t* line = cta.smem + OFF_OUT + (c >> 1) * KCH + row * 128;
+          if (c == DI / 64 - 1) tc_fence_before();
+          __syncwarp();
+          if (c == DI / 64 - 1 && lane == 0) mbar_arrive(cta.bar(B_DK_EMPTY + s));
+          uint8_t* line = cta.smem + OFF_OUT + c * KCH + row * 128;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 8; ++i) {
             auto pk = [&](int q) {
               return pack_bf16(__uint_as_float(v[8 * i + 2 * q]) * qs, __uint_as_float(v[8 * i + 2 * q + 1]) * qs);
             };
-            *reinterpret_cast<uint4*>(line + (((4 * (c & 1) + i) ^ (row & 7)) << 4)) =
-                make_uint4(pk(0), pk(1), pk(2), pk(3));
+            *reinterpret_cast<uint4*>(line + ((i ^ (row & 7)) << 4)) = make_uint4(pk(0), pk(1), pk(2), pk(3));
           }
-        }
-        fence_proxy_async_smem();
-        named_bar_sync(2, 128);
-        if (leader) {
-          for (int c = 0; c < DI / 64; ++c) tma_store_2d(&tm_out, sbase + OFF_OUT + c * KCH, 64 * c, t * p.kp + j * NK);
-          bulk_commit();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tm_out, sbase + OFF_OUT + c * KCH + quad * 32 * 128, 64 * c, t * p.kp + j * NK + quad * 32);
+            bulk_commit();
+          }
         }
       }
       if (!ok) break;
@@ -413,7 +413,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
       if (lane == 0) mbar_arrive(cta.bar(B_DQ_EMPTY + qb));
       ++n;
     }
-    if (leader) bulk_wait_all();
+    if (lane == 0) bulk_wait_all();
   }
   bwd_end(cta);
 }

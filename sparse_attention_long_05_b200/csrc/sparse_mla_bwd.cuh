@@ -57,8 +57,9 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
                :: "l"(map), "r"(src), "r"(x), "r"(y) : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// the committed stores have read their shared memory / have been written
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// all but the last N committed stores have read their shared memory / all have been written
+template <int N = 0>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" :: "n"(N) : "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -77,6 +78,37 @@ __device__ __forceinline__ bool named_bar_all(int id, int nthreads, bool v) {
   return r != 0;
 }
 
+// ---- CTA pairs (tcgen05 cta_group::2): the even CTA of the cluster issues MMAs whose A rows and whose halves of B lie
+// in both CTAs' shared memory (same offsets), and whose D rows lie in both tensor memories.
+__device__ __forceinline__ void mma2_bf16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// arrives on the barrier at this offset in both CTAs when every MMA issued so far has completed
+__device__ __forceinline__ void mma2_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               :: "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+// loads into this CTA's shared memory that complete on a barrier of either CTA of the pair (a cluster address)
+__device__ __forceinline__ void tma2_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4, %5}], [%2];"
+      :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void tma2_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                             int r0, int r1, int r2, int r3) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
+      :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
+}
+
 namespace mbw {
 constexpr int NK = 128;                 // keys per tile (the M dimension of P and dC)
 constexpr int D = 576, DV = 512;
@@ -90,27 +122,25 @@ constexpr int OFF_TMEM = 512, OFF_ABORT = 516;
 // ---- mla_bwd_p_kernel
 namespace p {
 constexpr int THREADS = 448, GATHER_WARPS = 8;
-constexpr int NS = 4;                   // ring stages of one gathered chunk (16 KB)
-constexpr int NACC = 4;                 // accumulators of 128 columns
-constexpr int B_IDX_FULL = 0, B_IDX_EMPTY = 2, B_RES_FULL = 4, B_RES_EMPTY = B_RES_FULL + DCH;
-constexpr int B_RING_FULL = B_RES_EMPTY + DCH, B_RING_EMPTY = B_RING_FULL + NS;
-constexpr int B_ACC_FULL = B_RING_EMPTY + NS, B_ACC_EMPTY = B_ACC_FULL + NACC;
-constexpr int B_COUNT = B_ACC_EMPTY + NACC;
+constexpr int NS_MAX = 9;
+constexpr int B_RES_FULL = 0, B_RES_EMPTY = B_RES_FULL + DCH, B_RING_FULL = B_RES_EMPTY + DCH;
+constexpr int B_RING_EMPTY = B_RING_FULL + NS_MAX, B_ACC_FULL = B_RING_EMPTY + NS_MAX, B_ACC_EMPTY = B_ACC_FULL + 4;
+constexpr int B_SUMS = B_ACC_EMPTY + 4;                       // objective: the other CTA's sums of a token (2 buffers)
+constexpr int B_COUNT = B_SUMS + 2;
 static_assert(B_COUNT * 8 <= OFF_TMEM, "barrier area");
-constexpr int OFF_HEADS = BAR_BYTES;                          // lse and delta of the item's heads, 2 buffers x 1 KB
-constexpr int OFF_IDX = OFF_HEADS + 2048;                     // 2 x 8 KB index rows
-constexpr int OFF_RED = OFF_IDX;                              // (objective: see IDXB)
-constexpr int RES_BYTES = DCH * CHUNK;                        // objective: 128 heads x 576; backward uses 8.5 chunks
+constexpr int OFF_SUMS = 528;                                 // objective: [2 buffers] of 16 bytes from the other CTA
+constexpr int OFF_HEADS = BAR_BYTES;                          // lse and delta of the token's heads, 2 buffers x 1 KB
+constexpr int OFF_RES = OFF_HEADS + 2048;
 template <bool KL> struct Map {
-  // the objective's gradient keeps all 128 heads of q (144 KB) and has room for one index row
-  static constexpr int IDXB = KL ? 1 : 2;
-  static constexpr int RES = KL ? DCH * CHUNK : 8 * CHUNK + HCHUNK;
-  static constexpr int OFF_RES = (OFF_IDX + IDXB * mla::KMAX * 4 + 1023) / 1024 * 1024;
+  static constexpr int RES_CHUNK = KL ? HCHUNK : CHUNK;       // a 64-dim chunk of the resident rows (the last: 64 rows)
+  static constexpr int RES = 8 * RES_CHUNK + HCHUNK;          // 72 KB, 136 KB
+  static constexpr int NS = KL ? 9 : 5;                       // ring stages of one gathered chunk (16 KB)
+  static constexpr int NACC = KL ? 4 : 2;                     // accumulators of 128, 256 columns
   static constexpr int OFF_RING = OFF_RES + RES;
   static constexpr int SMEM = OFF_RING + NS * CHUNK + 1024;
 };
 static_assert(Map<false>::SMEM <= 232448 && Map<true>::SMEM <= 232448, "shared memory per CTA");
-static_assert(Map<false>::OFF_RING % 1024 == 0 && Map<true>::OFF_RING % 1024 == 0, "1 KB aligned tiles");
+static_assert(OFF_RES % 1024 == 0 && OFF_SUMS + 32 <= BAR_BYTES && Map<true>::NS <= NS_MAX, "layout");
 }  // namespace p
 
 // ---- mla_bwd_dc_kernel
@@ -159,214 +189,222 @@ __device__ __forceinline__ BwdCta bwd_base(uint8_t* raw) {
   c.tmem = 0;
   return c;
 }
-// after the barriers are initialised by thread 0: tensor memory by warp 1, then the predecessor's results
+// after the barriers are initialised by thread 0: tensor memory by warp 1 (of both CTAs of a pair), then the
+// predecessor's results
+template <bool PAIR = false>
 __device__ __forceinline__ void bwd_begin(BwdCta& c) {
   if (threadIdx.x == 0) {
     *c.abort_flag = 0;
     fence_mbar_init();
   }
   if (warp_id() == 1) {
-    tmem_alloc(c.sbase + mbw::OFF_TMEM, mbw::TMEM_COLS);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                   :: "r"(c.sbase + mbw::OFF_TMEM), "r"(mbw::TMEM_COLS) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      tmem_alloc(c.sbase + mbw::OFF_TMEM, mbw::TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();      // the barriers of both CTAs are initialised
   tc_fence_after();
   c.tmem = *reinterpret_cast<volatile uint32_t*>(c.smem + mbw::OFF_TMEM);
   pdl_allow_next();
   pdl_wait();
 }
+template <bool PAIR = false>
 __device__ __forceinline__ void bwd_end(BwdCta& c) {
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) {
+    if (*c.abort_flag) {                   // loads that complete on the other CTA's barriers land meanwhile
+      const long long t0 = clock64();
+      while (clock64() - t0 < (g_wait_limit >> 8)) {
+      }
+    }
+    cluster_sync();                        // no CTA leaves while its peer may still touch its shared memory
+  }
   if (warp_id() == 1) {
     tc_fence_after();
-    tmem_dealloc(c.tmem, mbw::TMEM_COLS);
+    if constexpr (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(c.tmem), "r"(mbw::TMEM_COLS) : "memory");
+    else
+      tmem_dealloc(c.tmem, mbw::TMEM_COLS);
   }
 }
 
 // Row of c read for slot `slot` of a token: its entry, or the token's fill row for an empty or invalid one (its dS
 // and P are zero; a row of the token's own cannot bring in a NaN that the token does not already see).
-__device__ __forceinline__ int bwd_row(const MlaBwdParams& p, const int* ids, int slot, int fill) {
-  const int e = slot < p.k ? ids[slot] : -1;
+__device__ __forceinline__ int bwd_row(const MlaBwdParams& p, int e, int fill) {
   return (e >= 0 && e < p.S) ? e : fill;
 }
 
-// P and dS of one (token, 64 heads) per item, or (KL) the gradient of the objective of one token per item.
+// P and dS of one token per CTA pair, or (KL) the gradient of the objective of one token per pair.
 //
-// M = 128 keys, N = 128: columns 0..63 are S^T and 64..127 dP^T of the 64 heads (KL: S^T of all heads, N = HP).  The
-// resident operand is released chunk by chunk during the last tile, so the next item's loads overlap it.
+// M = 256 keys (128 in each CTA, which gathers only its own), N = 2 HP: CTA 0 holds q's rows and CTA 1 dout's, so that
+// one MMA gives S^T (columns 0 .. HP - 1) and dP^T (HP .. 2 HP - 1) of all heads; the position dims, which dout lacks,
+// are an N = HP product with half of q's rows in each CTA.  KL: N = HP, half of q's rows in each CTA.  With both CTAs of
+// a token sharing their halves, each key is gathered once per token: gathers land after 1.5 to 2 us under load, and
+// the bytes in flight (80 KB a CTA, KL 144 KB) set the rate.  The resident rows are released chunk by chunk during the
+// token's last tile, so the next token's loads overlap it.
 template <bool KL>
-__global__ void __launch_bounds__(mbw::p::THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mbw::p::THREADS, 1)
 mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                  const __grid_constant__ CUtensorMap tm_c, const MlaBwdParams p) {
   using namespace mbw;
   using namespace mbw::p;
   using M = Map<KL>;
+  constexpr int NS = M::NS, NACC = M::NACC;
   extern __shared__ uint8_t smem_raw[];
   BwdCta cta = bwd_base(smem_raw);
   const uint32_t sbase = cta.sbase;
   volatile int* abort_flag = cta.abort_flag;
   const int warp = warp_id(), lane = lane_id();
+  const int rank = static_cast<int>(cluster_rank());
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(cta.bar(B_IDX_FULL + i), 1);
-      mbar_init(cta.bar(B_IDX_EMPTY + i), GATHER_WARPS + 4);
-    }
-    for (int i = 0; i < DCH; ++i) { mbar_init(cta.bar(B_RES_FULL + i), 1); mbar_init(cta.bar(B_RES_EMPTY + i), 1); }
-    for (int i = 0; i < NS; ++i) { mbar_init(cta.bar(B_RING_FULL + i), 2); mbar_init(cta.bar(B_RING_EMPTY + i), 1); }
-    for (int i = 0; i < NACC; ++i) { mbar_init(cta.bar(B_ACC_FULL + i), 1); mbar_init(cta.bar(B_ACC_EMPTY + i), 4); }
+    for (int i = 0; i < DCH; ++i) { mbar_init(cta.bar(B_RES_FULL + i), 2); mbar_init(cta.bar(B_RES_EMPTY + i), 1); }
+    for (int i = 0; i < NS; ++i) { mbar_init(cta.bar(B_RING_FULL + i), 4); mbar_init(cta.bar(B_RING_EMPTY + i), 1); }
+    for (int i = 0; i < NACC; ++i) { mbar_init(cta.bar(B_ACC_FULL + i), 1); mbar_init(cta.bar(B_ACC_EMPTY + i), 8); }
+    for (int i = 0; i < 2; ++i) mbar_init(cta.bar(B_SUMS + i), 1);
   }
-  bwd_begin(cta);
+  bwd_begin<true>(cta);
   const uint32_t tmem = cta.tmem;
-  const uint32_t res = sbase + M::OFF_RES, ring = sbase + M::OFF_RING;
-  const int halves = KL ? 1 : p.HP / 64;
-  const int items = p.T * halves;
+  const uint32_t res = sbase + OFF_RES, ring = sbase + M::OFF_RING;
+  const uint32_t lead = map_cluster(sbase, 0);     // CTA 0's barriers, where every load of the pair completes
+  const int first = static_cast<int>(blockIdx.x >> 1), stride = static_cast<int>(gridDim.x >> 1);
+  auto tiles_of = [&](int t) { return (p.n_end[t] + 2 * NK - 1) / (2 * NK); };
   bool ok = true;
-  int n = 0;                              // items with at least one tile, walked so far
+  int n = 0;                              // tokens with entries, walked so far
 
   if (warp == 0) {
-    // ===================================================================== loader: index rows, q and dout rows
+    // ===================================================================== resident rows of q (and dout)
     if (lane == 0) {
-      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        const int t = item / halves, hf = item % halves;
+      for (int t = first; t < p.T && ok; t += stride) {
         if (p.n_end[t] <= 0) continue;
-        const int ib = n % M::IDXB;
-        if (!(ok = mbar_wait(cta.bar(B_IDX_EMPTY + ib), ((n / M::IDXB) & 1) ^ 1, abort_flag))) break;
-        mbar_arrive_expect_tx(cta.bar(B_IDX_FULL + ib), p.k * 4);
-        bulk_load(sbase + OFF_IDX + ib * mla::KMAX * 4, p.idx + static_cast<long long>(t) * p.k, p.k * 4,
-                  cta.bar(B_IDX_FULL + ib));
         for (int c = 0; c < DCH; ++c) {
           if (!(ok = mbar_wait(cta.bar(B_RES_EMPTY + c), (n & 1) ^ 1, abort_flag))) break;
-          const uint32_t dst = res + c * CHUNK, full = cta.bar(B_RES_FULL + c);
-          if constexpr (KL) {
-            mbar_arrive_expect_tx(full, (p.HP / 64) * HCHUNK);
-            for (int i = 0; i < p.HP / 64; ++i) tma_load_3d(dst + i * HCHUNK, &tm_q, full, 64 * c, 64 * i, p.t0 + t);
+          const uint32_t dst = res + c * M::RES_CHUNK, full = lead + 8 * (B_RES_FULL + c);
+          if (KL || c == 8) {
+            mbar_arrive_expect_tx_remote(full, HCHUNK);
+            tma2_load_3d(dst, &tm_q, full, 64 * c, rank * (p.HP / 2), p.t0 + t);
           } else {
-            mbar_arrive_expect_tx(full, c < 8 ? CHUNK : HCHUNK);
-            tma_load_3d(dst, &tm_q, full, 64 * c, 64 * hf, p.t0 + t);
-            if (c < 8) tma_load_3d(dst + HCHUNK, &tm_do, full, 64 * c, 64 * hf, p.t0 + t);
+            mbar_arrive_expect_tx_remote(full, (p.HP / 64) * HCHUNK);
+            for (int i = 0; i < p.HP / 64; ++i)
+              tma2_load_3d(dst + i * HCHUNK, rank ? &tm_do : &tm_q, full, 64 * c, 64 * i, p.t0 + t);
           }
         }
         ++n;
       }
-      if (*abort_flag && n > 0) {          // leave no load in flight into this CTA's shared memory
-        for (int i = 0; i < M::IDXB; ++i) mbar_wait_drain(cta.bar(B_IDX_FULL + i), ((n - 1) / M::IDXB) & 1);
-        for (int c = 0; c < DCH; ++c) mbar_wait_drain(cta.bar(B_RES_FULL + c), (n - 1) & 1);
-      }
     }
   } else if (warp == 2 || warp == 3 || warp >= 8) {
     // ===================================================================== gathers
-    // Two warps share a ring stage (64 rows each, one gather4 of four rows per lane): with a stage of its own, a
-    // warp meets the stage's barriers once per 64 KB of the CTA's traffic.
+    // Chunks of 128 keys x 64 dims go round four pairs of warps, each warp fetching half of the keys (a gather4 of four
+    // rows per lane), so that a warp meets a stage's barriers once per 64 KB of the CTA's traffic.  The entries of the
+    // next tile are read while this one is gathered.
     const int gw = (warp < 8) ? warp - 2 : warp - 6;
-    const int st = gw >> 1, rg = (gw & 1) * 16 + lane;
-    int m = 0;                             // chunks gathered by the CTA before this tile
-    uint32_t uses = 0;                     // chunks this warp has gathered
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const int t = item / halves, tiles = (p.n_end[t] + NK - 1) / NK;
+    const int turn = gw >> 1, rg = (gw & 1) * 16 + (lane & 15);
+    int m = 0;                             // chunks of the tiles before this one
+    for (int t = first; t < p.T && ok; t += stride) {
+      const int tiles = tiles_of(t), fill = p.fill[t];
       if (tiles <= 0) continue;
-      const int ib = n % M::IDXB, fill = p.fill[t];
-      if (!(ok = warp_wait(cta.bar(B_IDX_FULL + ib), (n / M::IDXB) & 1, abort_flag))) break;
-      const int* ids = reinterpret_cast<const int*>(cta.smem + OFF_IDX + ib * mla::KMAX * 4);
+      const int* ids = p.idx + static_cast<long long>(t) * p.k;
+      auto entries = [&](int j) {          // k is a multiple of 64, a lane's four slots lie on one side of it
+        const int slot = (2 * j + rank) * NK + 4 * rg;
+        return slot < p.k ? __ldg(reinterpret_cast<const int4*>(ids + slot)) : make_int4(-1, -1, -1, -1);
+      };
+      int4 e = entries(0);
       for (int j = 0; j < tiles && ok; ++j, m += DCH) {
-        int r[4] = {0, 0, 0, 0};
-        if (lane < 16) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) r[u] = bwd_row(p, ids, j * NK + 4 * rg + u, fill);
-        }
-        for (int c = (st - m % NS + NS) % NS; c < DCH; c += NS) {
+        const int r0 = bwd_row(p, e.x, fill), r1 = bwd_row(p, e.y, fill), r2 = bwd_row(p, e.z, fill),
+                  r3 = bwd_row(p, e.w, fill);
+        if (j + 1 < tiles) e = entries(j + 1);
+        for (int c = (turn - m % 4 + 4) % 4; c < DCH; c += 4) {
+          const int st = (m + c) % NS;
+          const uint32_t full = lead + 8 * (B_RING_FULL + st);
           bool got = true;
           if (lane == 0) {
-            got = mbar_wait(cta.bar(B_RING_EMPTY + st), (uses & 1) ^ 1, abort_flag);
-            if (got) mbar_arrive_expect_tx(cta.bar(B_RING_FULL + st), 64 * 128);
+            got = mbar_wait(cta.bar(B_RING_EMPTY + st), (((m + c) / NS) & 1) ^ 1, abort_flag);
+            if (got) mbar_arrive_expect_tx_remote(full, 64 * 128);
           }
           if (!(ok = __shfl_sync(0xffffffffu, got, 0))) break;
-          if (lane < 16)
-            tma_gather4(ring + st * CHUNK + rg * 512, &tm_c, cta.bar(B_RING_FULL + st), 64 * c, r[0], r[1], r[2], r[3]);
-          ++uses;
+          if (lane < 16) tma2_gather4(ring + st * CHUNK + rg * 512, &tm_c, full, 64 * c, r0, r1, r2, r3);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(cta.bar(B_IDX_EMPTY + ib));
-      ++n;
     }
-    if (lane == 0 && *abort_flag && uses > 0) mbar_wait_drain(cta.bar(B_RING_FULL + st), (uses - 1) & 1);
   } else if (warp == 1) {
-    // ===================================================================== MMA issue
-    Pipe<NS> rp;
-    int g = 0;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const int t = item / halves, tiles = (p.n_end[t] + NK - 1) / NK;
-      if (tiles <= 0) continue;
-      for (int j = 0; j < tiles && ok; ++j, ++g) {
-        const int ab = g % NACC;
-        if (!(ok = warp_wait(cta.bar(B_ACC_EMPTY + ab), ((g / NACC) & 1) ^ 1, abort_flag))) break;
-        tc_fence_after();
-        for (int c = 0; c < DCH; ++c, rp.advance()) {
-          if (j == 0 && !(ok = warp_wait(cta.bar(B_RES_FULL + c), n & 1, abort_flag))) break;
-          if (!(ok = warp_wait(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
+    // ===================================================================== MMA issue (CTA 0 for the pair)
+    if (rank == 0) {
+      Pipe<NS> rp;
+      int g = 0;
+      const uint32_t wide = idesc_bf16(256, KL ? p.HP : 2 * p.HP, false), narrow = idesc_bf16(256, p.HP, false);
+      for (int t = first; t < p.T && ok; t += stride) {
+        const int tiles = tiles_of(t);
+        if (tiles <= 0) continue;
+        for (int j = 0; j < tiles && ok; ++j, ++g) {
+          const int ab = g % NACC;
+          if (!(ok = warp_wait<true>(cta.bar(B_ACC_EMPTY + ab), ((g / NACC) & 1) ^ 1, abort_flag))) break;
           tc_fence_after();
-          const uint64_t ad = smem_desc(ring + rp.stage * CHUNK, 16, 1024, kLayoutSW128);
-          const uint64_t bd = smem_desc(res + c * CHUNK, 16, 1024, kLayoutSW128);
-          const uint32_t idesc = KL ? idesc_bf16(128, p.HP, false) : idesc_bf16(128, c < 8 ? 128 : 64, false);
-          if (elect_one()) {
+          for (int c = 0; c < DCH; ++c, rp.advance()) {
+            if (j == 0 && !(ok = warp_wait<true>(cta.bar(B_RES_FULL + c), n & 1, abort_flag))) break;
+            if (!(ok = warp_wait<true>(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
+            tc_fence_after();
+            const uint64_t ad = smem_desc(ring + rp.stage * CHUNK, 16, 1024, kLayoutSW128);
+            const uint64_t bd = smem_desc(res + c * M::RES_CHUNK, 16, 1024, kLayoutSW128);
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_bf16_ss(tmem + 128 * ab, ad + 2 * k, bd + 2 * k, idesc, (c | k) ? 1u : 0u);
-            mma_commit(cta.bar(B_RING_EMPTY + rp.stage));
-            if (j == tiles - 1) mma_commit(cta.bar(B_RES_EMPTY + c));
+              for (int k = 0; k < 4; ++k)
+                mma2_bf16_ss(tmem + (512 / NACC) * ab, ad + 2 * k, bd + 2 * k, c < 8 ? wide : narrow,
+                             (c | k) ? 1u : 0u);
+              mma2_commit(cta.bar(B_RING_EMPTY + rp.stage));
+              if (j == tiles - 1) mma2_commit(cta.bar(B_RES_EMPTY + c));
+            }
+            __syncwarp();
           }
+          if (!ok) break;
+          if (elect_one()) mma2_commit(cta.bar(B_ACC_FULL + ab));
           __syncwarp();
         }
-        if (!ok) break;
-        if (elect_one()) mma_commit(cta.bar(B_ACC_FULL + ab));
-        __syncwarp();
+        ++n;
       }
-      ++n;
     }
   } else {
     // ===================================================================== probabilities (warps 4..7, one key a thread)
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     constexpr float kLog2e = 1.4426950408889634f;
-    int g = 0, heads_at = 0;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const int t = item / halves, hf = item % halves, tiles = (p.n_end[t] + NK - 1) / NK;
+    int g = 0;
+    for (int t = first; t < p.T && ok; t += stride) {
+      const int tiles = tiles_of(t);
+      const long long base = static_cast<long long>(t) * p.k;
       if constexpr (KL) {
-        for (int i = tiles * NK + row; i < p.k; i += NK) p.dsel[static_cast<long long>(t) * p.k + i] = 0.f;
+        for (int i = tiles * 2 * NK + rank * NK + row; i < p.k; i += 2 * NK) p.dsel[base + i] = 0.f;
       }
       if (tiles <= 0) continue;
-      const int ib = n % M::IDXB;
-      // the item's lse (in log2 units) and delta, or KL: the lse of all heads.  A head without any probability mass
-      // (lse = -inf) and the heads that only fill up the tile get +inf: P = 0.
-      float* hs = reinterpret_cast<float*>(cta.smem + OFF_HEADS) + heads_at * 256;
-      heads_at ^= 1;
+      // the token's lse (in log2 units) and delta.  A head without any probability mass (lse = -inf) and the heads that
+      // only fill up the tile get +inf: P = 0.
+      float* hs = reinterpret_cast<float*>(cta.smem + OFF_HEADS) + (n & 1) * 256;
       {
-        const int h = KL ? row : 64 * hf + (row & 63);
-        float v = KL || row < 64 ? INFINITY : 0.f;
-        if (h < p.H) {
-          const long long at = static_cast<long long>(t) * p.H + h;
-          if (KL || row < 64) {
-            const float l = p.lse[at];
-            v = l == -INFINITY ? INFINITY : l * kLog2e;
-          } else {
-            v = p.delta[at];
-          }
-        }
-        hs[row] = v;
+        const long long at = static_cast<long long>(t) * p.H + row;
+        const float l = row < p.H ? p.lse[at] : -INFINITY;
+        hs[row] = l == -INFINITY ? INFINITY : l * kLog2e;
+        if (!KL) hs[128 + row] = row < p.H ? p.delta[at] : 0.f;
       }
-      ok = warp_wait(cta.bar(B_IDX_FULL + ib), (n / M::IDXB) & 1, abort_flag);
       if (!(ok = named_bar_all(1, 128, ok))) break;
-      const int* ids = reinterpret_cast<const int*>(cta.smem + OFF_IDX + ib * mla::KMAX * 4);
       [[maybe_unused]] float m_i = -INFINITY, z_i = 0.f, s_a = 0.f;
       for (int j = 0; j < tiles; ++j, ++g) {
-        const int ab = g % NACC, slot = j * NK + row;
-        const int e = slot < p.k ? ids[slot] : -1;
+        const int ab = g % NACC, slot = (2 * j + rank) * NK + row;
+        const int e = slot < p.k ? __ldg(p.idx + base + slot) : -1;
         const bool valid = e >= 0 && e < p.S;
         if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), (g / NACC) & 1, abort_flag))) break;
         tc_fence_after();
-        const uint32_t acc = lane_addr + tmem + 128 * ab;
+        const uint32_t acc = lane_addr + tmem + (512 / NACC) * ab;
+        auto release = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(lead + 8 * (B_ACC_EMPTY + ab));
+        };
         if constexpr (KL) {
           float a0 = 0.f, a1 = 0.f;
           for (int c = 0; c < p.HP / 32; ++c) {
@@ -379,15 +417,12 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               a1 += ex2_approx(fmaf(__uint_as_float(v[i + 1]), p.scale_log2, -hs[32 * c + i + 1]));
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(cta.bar(B_ACC_EMPTY + ab));
+          release();
           if (slot < p.k) {
-            const long long at = static_cast<long long>(t) * p.k + slot;
             const float a = valid ? a0 + a1 : 0.f;
-            p.dsel[at] = a;                // the same thread reads it back below
+            p.dsel[base + slot] = a;       // the same thread reads it back below
             if (valid) {
-              const float x = p.sel[at];
+              const float x = p.sel[base + slot];
               s_a += a;
               if (x > m_i) {
                 z_i = z_i * ex2_approx((m_i - x) * kLog2e) + 1.f;
@@ -398,42 +433,40 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
           }
         } else {
-          uint16_t* out = p.pds + (static_cast<long long>(t) * p.kp + slot) * (2 * p.HP) + 64 * hf;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          uint16_t* out = p.pds + (static_cast<long long>(t) * p.kp + slot) * (2 * p.HP);
+          const int blocks = p.HP / 32;
+#pragma unroll 2
+          for (int c = 0; c < blocks; ++c) {
             uint32_t s[32], d[32];
             tmem_ld32(acc + 32 * c, s);
-            tmem_ld32(acc + 64 + 32 * c, d);
+            tmem_ld32(acc + p.HP + 32 * c, d);
             tmem_wait_ld();
-            if (c == 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(cta.bar(B_ACC_EMPTY + ab));
-            }
+            if (c == blocks - 1) release();
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float pr = ex2_approx(fmaf(__uint_as_float(s[i]), p.scale_log2, -hs[32 * c + i]));
-              const float ds = pr * (__uint_as_float(d[i]) - hs[64 + 32 * c + i]) * p.scale;
+              const float ds = pr * (__uint_as_float(d[i]) - hs[128 + 32 * c + i]) * p.scale;
               s[i] = __float_as_uint(valid ? pr : 0.f);
               d[i] = __float_as_uint(valid ? ds : 0.f);
             }
-            uint4* ds4 = reinterpret_cast<uint4*>(out + 32 * c);
-            uint4* p4 = reinterpret_cast<uint4*>(out + p.HP + 32 * c);
+            if (slot < p.kp) {
+              uint4* ds4 = reinterpret_cast<uint4*>(out + 32 * c);
+              uint4* p4 = reinterpret_cast<uint4*>(out + p.HP + 32 * c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              auto pk = [&](const uint32_t (&v)[32], int q) {
-                return pack_bf16(__uint_as_float(v[8 * i + 2 * q]), __uint_as_float(v[8 * i + 2 * q + 1]));
-              };
-              ds4[i] = make_uint4(pk(d, 0), pk(d, 1), pk(d, 2), pk(d, 3));
-              p4[i] = make_uint4(pk(s, 0), pk(s, 1), pk(s, 2), pk(s, 3));
+              for (int i = 0; i < 4; ++i) {
+                auto pk = [&](const uint32_t (&v)[32], int q) {
+                  return pack_bf16(__uint_as_float(v[8 * i + 2 * q]), __uint_as_float(v[8 * i + 2 * q + 1]));
+                };
+                ds4[i] = make_uint4(pk(d, 0), pk(d, 1), pk(d, 2), pk(d, 3));
+                p4[i] = make_uint4(pk(s, 0), pk(s, 1), pk(s, 2), pk(s, 3));
+              }
             }
           }
         }
       }
       if (!(ok = named_bar_all(1, 128, ok))) break;
-      if (lane == 0) mbar_arrive(cta.bar(B_IDX_EMPTY + ib));
       if constexpr (KL) {
-        // the token's sums over its 128 threads, then g (softmax(I) - p) for each slot
+        // the token's sums over the pair's 256 threads, then g (softmax(I) - p) for each slot
         float mm = m_i;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
@@ -446,28 +479,53 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         if (lane == 0) { rs[3 * quad] = mm; rs[3 * quad + 1] = z; rs[3 * quad + 2] = s_a; }
         named_bar_sync(1, 128);
-        const float m_all = fmaxf(fmaxf(rs[0], rs[3]), fmaxf(rs[6], rs[9]));
-        float z_all = 0.f, a_all = 0.f;
+        auto join = [&](float& ma, float& za, float mb, float zb) {
+          const float mx = fmaxf(ma, mb);
+          const float fa = ma > -INFINITY ? ex2_approx((ma - mx) * kLog2e) : 0.f;
+          const float fb = mb > -INFINITY ? ex2_approx((mb - mx) * kLog2e) : 0.f;
+          za = za * fa + zb * fb;
+          ma = mx;
+        };
+        float m_all = rs[0], z_all = rs[1], a_all = rs[2];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          if (rs[3 * w] > -INFINITY) z_all += rs[3 * w + 1] * ex2_approx((rs[3 * w] - m_all) * kLog2e);
+        for (int w = 1; w < 4; ++w) {
+          join(m_all, z_all, rs[3 * w], rs[3 * w + 1]);
           a_all += rs[3 * w + 2];
+        }
+        // the other CTA's sums (buffer n & 1: it cannot be two tokens ahead, as it needs this CTA's sums of each)
+        const int sb = n & 1;
+        if (row == 0) {
+          mbar_arrive_expect_tx(cta.bar(B_SUMS + sb), 16);
+          st_async_v4(map_cluster(sbase + OFF_SUMS + 16 * sb, rank ^ 1),
+                      make_uint4(__float_as_uint(m_all), __float_as_uint(z_all), __float_as_uint(a_all), 0),
+                      map_cluster(cta.bar(B_SUMS + sb), rank ^ 1));
+        }
+        ok = warp_wait<true>(cta.bar(B_SUMS + sb), (n >> 1) & 1, abort_flag);
+        if (!(ok = named_bar_all(1, 128, ok))) break;
+        const float4 other = *reinterpret_cast<const float4*>(cta.smem + OFF_SUMS + 16 * sb);
+        if (rank == 0) {                   // both CTAs join the two halves in the same order
+          join(m_all, z_all, other.x, other.y);
+          a_all = a_all + other.z;
+        } else {
+          float mo = other.x, zo = other.y;
+          join(mo, zo, m_all, z_all);
+          m_all = mo;
+          z_all = zo;
+          a_all = other.z + a_all;
         }
         const float up = p.dkl ? p.dkl[t] : 1.f;
         const float iz = z_all > 0.f ? 1.f / z_all : 0.f, ia = a_all > 0.f ? 1.f / a_all : 0.f;
-        for (int i = row; i < min(tiles * NK, p.k); i += NK) {
-          const long long at = static_cast<long long>(t) * p.k + i;
-          // reading the entry again decides validity as above (its index row may have been replaced by now)
-          const int e = p.idx[at];
-          const float x = p.sel[at];
+        for (int i = rank * NK + row; i < min(tiles * 2 * NK, p.k); i += 2 * NK) {
+          const int e = __ldg(p.idx + base + i);
+          const float x = p.sel[base + i];
           const float soft = x > -INFINITY ? ex2_approx((x - m_all) * kLog2e) * iz : 0.f;
-          p.dsel[at] = (e >= 0 && e < p.S) ? up * (soft - p.dsel[at] * ia) : 0.f;
+          p.dsel[base + i] = (e >= 0 && e < p.S) ? up * (soft - p.dsel[base + i] * ia) : 0.f;
         }
       }
       ++n;
     }
   }
-  bwd_end(cta);
+  bwd_end<true>(cta);
 }
 
 // Contributions to dc: out[t kp + slot][d] = sum_h dS q[t][h][d] + P dout[t][h][d] for 192 dims d per item.
@@ -576,40 +634,41 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
       const int t = item / 3, d3 = item % 3, tiles = (p.n_end[t] + NK - 1) / NK;
       for (int j = 0; j < tiles; ++j, ++g) {
         const int ab = g & 1;
-        // the previous tile's stores have read the staging area
-        if (warp == 4 && lane == 0) bulk_wait_read();
-        ok = warp_wait(cta.bar(B_ACC_FULL + ab), (g >> 1) & 1, abort_flag);
-        if (!(ok = named_bar_all(1, 128, ok))) break;
+        if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), (g >> 1) & 1, abort_flag))) break;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 6; ++c) {
-          uint32_t v[32];
-          tmem_ld32(lane_addr + tmem + 256 * ab + 32 * c, v);
+        for (int c = 0; c < 3; ++c) {
+          // each warp stages and stores its own 32 rows, 64 dims at a time: the store of this piece one tile ago has
+          // read its staging area once at most the two later ones are pending
+          uint32_t v[64];
+          uint32_t (&v0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
+          uint32_t (&v1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32]);
+          tmem_ld32(lane_addr + tmem + 256 * ab + 64 * c, v0);
+          tmem_ld32(lane_addr + tmem + 256 * ab + 64 * c + 32, v1);
+          if (lane == 0) bulk_wait_read<2>();
+          __syncwarp();
           tmem_wait_ld();
-          if (c == 5) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(cta.bar(B_ACC_EMPTY + ab));
-          }
+          if (c == 2) tc_fence_before();
+          __syncwarp();
+          if (c == 2 && lane == 0) mbar_arrive(cta.bar(B_ACC_EMPTY + ab));
           // 128-byte swizzled rows of 64 dims: 16-byte unit u of row r at unit u ^ (r % 8)
-          uint8_t* line = cta.smem + OFF_OUT + (c >> 1) * CHUNK + row * 128;
+          uint8_t* line = cta.smem + OFF_OUT + c * CHUNK + row * 128;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 8; ++i) {
             auto pk = [&](int q) { return pack_bf16(__uint_as_float(v[8 * i + 2 * q]), __uint_as_float(v[8 * i + 2 * q + 1])); };
-            *reinterpret_cast<uint4*>(line + (((4 * (c & 1) + i) ^ (row & 7)) << 4)) =
-                make_uint4(pk(0), pk(1), pk(2), pk(3));
+            *reinterpret_cast<uint4*>(line + ((i ^ (row & 7)) << 4)) = make_uint4(pk(0), pk(1), pk(2), pk(3));
           }
-        }
-        fence_proxy_async_smem();
-        named_bar_sync(1, 128);
-        if (warp == 4 && lane == 0) {
-          for (int c = 0; c < 3; ++c)
-            tma_store_2d(&tm_out, sbase + OFF_OUT + c * CHUNK, 192 * d3 + 64 * c, t * p.kp + j * NK);
-          bulk_commit();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tm_out, sbase + OFF_OUT + c * CHUNK + quad * 32 * 128, 192 * d3 + 64 * c,
+                         t * p.kp + j * NK + quad * 32);
+            bulk_commit();
+          }
         }
       }
     }
-    if (warp == 4 && lane == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_all();
   }
   bwd_end(cta);
 }
@@ -690,7 +749,10 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const __grid_consta
         int r[4] = {0, 0, 0, 0};
         if (active) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) r[u] = bwd_row(p, ids, j * KT + 4 * rg + u, fill);
+          for (int u = 0; u < 4; ++u) {
+            const int slot = j * KT + 4 * rg + u;
+            r[u] = bwd_row(p, slot < p.k ? ids[slot] : -1, fill);
+          }
         }
         bool got = true;
         if (lane == 0) {
