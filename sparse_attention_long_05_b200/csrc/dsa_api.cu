@@ -668,7 +668,7 @@ int round_up(int n, int m) { return (n + m - 1) / m * m; }
 
 // Scatter of a chunk's contributions: the table and what goes with it.
 struct ScatterWs {
-  int *n_end, *fill;
+  int* n_end;
   uint16_t *table, *contrib;
   float* acc;
   int ld;
@@ -677,7 +677,6 @@ ScatterWs carve_scatter(Carve& w, int Tc, int64_t S, int kp, int width, bool man
   ScatterWs s{};
   s.ld = round_up(Tc, 8);
   s.n_end = w.take<int>(Tc);
-  s.fill = w.take<int>(Tc);
   s.table = w.take<uint16_t>(size_t(S) * s.ld);
   s.contrib = w.take<uint16_t>(size_t(Tc) * kp * width);
   s.acc = many ? w.take<float>(size_t(S) * width) : nullptr;
@@ -692,7 +691,7 @@ dsa_status_t scatter_begin(const ScatterWs& w, const int* idx, int T, int64_t S,
     return DSA_ERR_CUDA;
   dsa_status_t e = last_launch_status();
   if (e != DSA_OK) return e;
-  if (launch_pdl(scatter_build_kernel, dim3(T), dim3(256), 0, st, idx, k, static_cast<long long>(S), w.n_end, w.fill,
+  if (launch_pdl(scatter_build_kernel, dim3(T), dim3(256), 0, st, idx, k, static_cast<long long>(S), w.n_end,
                  w.table, w.ld) != cudaSuccess)
     return DSA_ERR_CUDA;
   return last_launch_status();
@@ -764,7 +763,7 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
     MlaBwdParams p{};
     p.idx = idx + o * k;
     p.n_end = w.sc.n_end;
-    p.fill = w.sc.fill;
+    p.c = c;
     p.lse = lse + o * H;
     p.delta = w.delta;
     p.pds = w.pds;
@@ -793,7 +792,7 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
                    tq, tdo, tout, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
-    if (launch_pdl(mla_bwd_dq_kernel, dim3(std::min(sms, 3 * n)), dim3(mbw::dq::THREADS), mbw::dq::SMEM, st, tp64, tc,
+    if (launch_pdl(mla_bwd_dq_kernel, dim3(std::min(sms, 3 * n)), dim3(mbw::dq::THREADS), mbw::dq::SMEM, st, tp64,
                    p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
@@ -803,7 +802,7 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
   return DSA_OK;
 }
 
-size_t kl_bwd_ws_bytes(int T) { return 2 * align_up(size_t(T) * 4, 256); }
+size_t kl_bwd_ws_bytes(int T) { return align_up(size_t(T) * 4, 256); }
 
 dsa_status_t run_kl_bwd(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx, const float* sel,
                         const float* lse, const float* dkl, int T, int H, int k, float scale, float* dsel, void* ws,
@@ -813,10 +812,9 @@ dsa_status_t run_kl_bwd(const uint16_t* q, const uint16_t* c, int S, const int32
   Carve w{static_cast<char*>(ws)};
   MlaBwdParams p{};
   int* n_end = w.take<int>(T);
-  int* fill = w.take<int>(T);
   p.idx = idx;
   p.n_end = n_end;
-  p.fill = fill;
+  p.c = c;
   p.lse = lse;
   p.T = T;
   p.H = H;
@@ -829,7 +827,7 @@ dsa_status_t run_kl_bwd(const uint16_t* q, const uint16_t* c, int S, const int32
   p.sel = sel;
   p.dkl = dkl;
   p.dsel = dsel;
-  if (launch_pdl(scatter_build_kernel, dim3(T), dim3(256), 0, st, idx, k, static_cast<long long>(S), n_end, fill,
+  if (launch_pdl(scatter_build_kernel, dim3(T), dim3(256), 0, st, idx, k, static_cast<long long>(S), n_end,
                  nullptr, 0) != cudaSuccess)
     return DSA_ERR_CUDA;
   const dsa_status_t e = last_launch_status();

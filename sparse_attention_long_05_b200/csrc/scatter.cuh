@@ -26,14 +26,13 @@ __global__ void __launch_bounds__(256) scatter_clear_kernel(uint4* table, long l
     table[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
 }
 
-// One CTA per token: n_end (slots up to the last valid entry), fill (the row of the first valid one, 0 without any),
-// and with a table its entries.  A row selected more than once by a token is entered with its lowest slot and
+// One CTA per token: n_end (slots up to the last valid entry), and with a table its entries.  A row selected more than once by a token is entered with its lowest slot and
 // flagged.  An entry outside [-1, S) counts as empty and is recorded as DSA_ERR_BAD_INDEX.
-__global__ void __launch_bounds__(256) scatter_build_kernel(const int* idx, int k, long long S, int* n_end, int* fill,
+__global__ void __launch_bounds__(256) scatter_build_kernel(const int* idx, int k, long long S, int* n_end,
                                                             uint16_t* table, int ld) {
-  __shared__ int last, first;
+  __shared__ int last;
   const int t = blockIdx.x;
-  if (threadIdx.x == 0) { last = 0; first = sct::MAX_K; }
+  if (threadIdx.x == 0) last = 0;
   __syncthreads();
   pdl_allow_next();
   pdl_wait();
@@ -42,14 +41,13 @@ __global__ void __launch_bounds__(256) scatter_build_kernel(const int* idx, int 
   auto cell = [&](int e) { return table + static_cast<long long>(e) * ld + t; };
   constexpr int PER = sct::MAX_K / 256;
   int e[PER];
-  int my_last = 0, my_first = sct::MAX_K;
+  int my_last = 0;
 #pragma unroll
   for (int u = 0; u < PER; ++u) {
     const int i = u * 256 + threadIdx.x;
     e[u] = i < k ? row[i] : -1;
     if (valid(e[u])) {
       my_last = i + 1;
-      my_first = min(my_first, i);
       if (table) *cell(e[u]) = static_cast<uint16_t>(i);
     } else if (e[u] != -1) {
       raise_status(DSA_ERR_BAD_INDEX);
@@ -57,16 +55,9 @@ __global__ void __launch_bounds__(256) scatter_build_kernel(const int* idx, int 
     }
   }
   my_last = __reduce_max_sync(0xffffffffu, my_last);
-  my_first = __reduce_min_sync(0xffffffffu, my_first);
-  if (lane_id() == 0) {
-    atomicMax(&last, my_last);
-    atomicMin(&first, my_first);
-  }
+  if (lane_id() == 0) atomicMax(&last, my_last);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    n_end[t] = last;
-    fill[t] = first < k ? row[first] : 0;
-  }
+  if (threadIdx.x == 0) n_end[t] = last;
   if (!table) return;
   // the lowest slot wins: repeated until no slot is below the one entered (one round where no row repeats)
   bool again = false;

@@ -32,7 +32,7 @@ namespace dsa {
 struct MlaBwdParams {
   const int* idx;              // [T, k] selections of the chunk's tokens
   const int* n_end;            // [T] slots up to the token's last valid entry
-  const int* fill;             // [T] a row of c that the token selects (what its invalid slots read)
+  const uint16_t* c;           // [S, 576]
   const float* lse;            // [T, H]
   const float* delta;          // [T, H]
   uint16_t* pds;               // [T * kp, 2 HP] bf16: dS of HP heads, then P of HP heads, for every slot
@@ -109,6 +109,13 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
 }
 
+// one 32-byte store (32-byte aligned)
+__device__ __forceinline__ void st_global_32(void* at, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 namespace mbw {
 constexpr int NK = 128;                 // keys per tile (the M dimension of P and dC)
 constexpr int D = 576, DV = 512;
@@ -121,8 +128,8 @@ constexpr int OFF_TMEM = 512, OFF_ABORT = 516;
 
 // ---- mla_bwd_p_kernel
 namespace p {
-constexpr int THREADS = 448, GATHER_WARPS = 8;
-constexpr int NS_MAX = 9;
+constexpr int THREADS = 448;            // w0 resident rows, w1 MMA, w2 w3 w8..13 gathers, w4..7 probabilities
+constexpr int NS_MAX = 5;
 constexpr int B_RES_FULL = 0, B_RES_EMPTY = B_RES_FULL + DCH, B_RING_FULL = B_RES_EMPTY + DCH;
 constexpr int B_RING_EMPTY = B_RING_FULL + NS_MAX, B_ACC_FULL = B_RING_EMPTY + NS_MAX, B_ACC_EMPTY = B_ACC_FULL + 4;
 constexpr int B_SUMS = B_ACC_EMPTY + 4;                       // objective: the other CTA's sums of a token (2 buffers)
@@ -134,10 +141,13 @@ constexpr int OFF_RES = OFF_HEADS + 2048;
 template <bool KL> struct Map {
   static constexpr int RES_CHUNK = KL ? HCHUNK : CHUNK;       // a 64-dim chunk of the resident rows (the last: 64 rows)
   static constexpr int RES = 8 * RES_CHUNK + HCHUNK;          // 72 KB, 136 KB
-  static constexpr int NS = KL ? 9 : 5;                       // ring stages of one gathered chunk (16 KB)
+  static constexpr int SC = KL ? 3 : 1;                       // gathered chunks (16 KB) of a ring stage
+  static constexpr int NS = KL ? 3 : 5;                       // ring stages
+  static constexpr int WPS = KL ? 8 : 2;                      // warps that fill a stage
   static constexpr int NACC = KL ? 4 : 2;                     // accumulators of 128, 256 columns
   static constexpr int OFF_RING = OFF_RES + RES;
-  static constexpr int SMEM = OFF_RING + NS * CHUNK + 1024;
+  static constexpr int SMEM = OFF_RING + NS * SC * CHUNK + 1024;
+  static_assert(DCH % SC == 0 && SC * 32 % WPS == 0 && SC * 32 / WPS <= 32, "stage split");
 };
 static_assert(Map<false>::SMEM <= 232448 && Map<true>::SMEM <= 232448, "shared memory per CTA");
 static_assert(OFF_RES % 1024 == 0 && OFF_SUMS + 32 <= BAR_BYTES && Map<true>::NS <= NS_MAX, "layout");
@@ -159,17 +169,16 @@ static_assert(SMEM <= 232448, "shared memory per CTA");
 
 // ---- mla_bwd_dq_kernel
 namespace dq {
-constexpr int THREADS = 448, GATHER_WARPS = 8;
+constexpr int THREADS = 448;
 constexpr int KT = 64;                  // keys per stage
 constexpr int A_BYTES = 2 * HCHUNK, STAGE = A_BYTES + 3 * HCHUNK;   // dS: 64 keys x 128 heads; keys: 64 x 192 dims
-constexpr int NS = 4;
-constexpr int G4 = 3 * KT / 4;          // gather4 instructions per stage
-constexpr int B_IDX_FULL = 0, B_IDX_EMPTY = 2, B_RING_FULL = 4, B_RING_EMPTY = B_RING_FULL + NS;
+constexpr int NS = 5;
+constexpr int B_RING_FULL = 0, B_RING_EMPTY = B_RING_FULL + NS;
 constexpr int B_ACC_FULL = B_RING_EMPTY + NS, B_ACC_EMPTY = B_ACC_FULL + 2;
 static_assert((B_ACC_EMPTY + 2) * 8 <= OFF_TMEM, "barrier area");
-constexpr int OFF_IDX = BAR_BYTES, OFF_RING = (OFF_IDX + 2 * mla::KMAX * 4 + 1023) / 1024 * 1024;
+constexpr int OFF_RING = BAR_BYTES;
 constexpr int SMEM = OFF_RING + NS * STAGE + 1024;
-static_assert(SMEM <= 232448 && G4 % GATHER_WARPS == 0 && STAGE % 1024 == 0, "stage split");
+static_assert(SMEM <= 232448 && STAGE % 1024 == 0 && KT == 64, "stages");
 }  // namespace dq
 }  // namespace mbw
 
@@ -236,11 +245,15 @@ __device__ __forceinline__ void bwd_end(BwdCta& c) {
   }
 }
 
-// Row of c read for slot `slot` of a token: its entry, or the token's fill row for an empty or invalid one (its dS
-// and P are zero; a row of the token's own cannot bring in a NaN that the token does not already see).
-__device__ __forceinline__ int bwd_row(const MlaBwdParams& p, int e, int fill) {
-  return (e >= 0 && e < p.S) ? e : fill;
+// 16 bytes into shared memory, or zeros where nothing is to be read
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
+// one arrival on `bar` (of those it was initialised to expect) when this thread's copies so far have landed
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // P and dS of one token per CTA pair, or (KL) the gradient of the objective of one token per pair.
 //
@@ -248,7 +261,7 @@ __device__ __forceinline__ int bwd_row(const MlaBwdParams& p, int e, int fill) {
 // one MMA gives S^T (columns 0 .. HP - 1) and dP^T (HP .. 2 HP - 1) of all heads; the position dims, which dout lacks,
 // are an N = HP product with half of q's rows in each CTA.  KL: N = HP, half of q's rows in each CTA.  With both CTAs of
 // a token sharing their halves, each key is gathered once per token: gathers land after 1.5 to 2 us under load, and
-// the bytes in flight (80 KB a CTA, KL 144 KB) set the rate.  The resident rows are released chunk by chunk during the
+// (80 KB are in flight a CTA, KL 144 KB).  The resident rows are released chunk by chunk during the
 // token's last tile, so the next token's loads overlap it.
 template <bool KL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mbw::p::THREADS, 1)
@@ -257,7 +270,7 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   using namespace mbw;
   using namespace mbw::p;
   using M = Map<KL>;
-  constexpr int NS = M::NS, NACC = M::NACC;
+  constexpr int NS = M::NS, NACC = M::NACC, SC = M::SC, SPT = DCH / SC;   // stages of a tile
   extern __shared__ uint8_t smem_raw[];
   BwdCta cta = bwd_base(smem_raw);
   const uint32_t sbase = cta.sbase;
@@ -266,7 +279,7 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const int rank = static_cast<int>(cluster_rank());
   if (threadIdx.x == 0) {
     for (int i = 0; i < DCH; ++i) { mbar_init(cta.bar(B_RES_FULL + i), 2); mbar_init(cta.bar(B_RES_EMPTY + i), 1); }
-    for (int i = 0; i < NS; ++i) { mbar_init(cta.bar(B_RING_FULL + i), 4); mbar_init(cta.bar(B_RING_EMPTY + i), 1); }
+    for (int i = 0; i < NS; ++i) { mbar_init(cta.bar(B_RING_FULL + i), 2 * M::WPS); mbar_init(cta.bar(B_RING_EMPTY + i), 1); }
     for (int i = 0; i < NACC; ++i) { mbar_init(cta.bar(B_ACC_FULL + i), 1); mbar_init(cta.bar(B_ACC_EMPTY + i), 8); }
     for (int i = 0; i < 2; ++i) mbar_init(cta.bar(B_SUMS + i), 1);
   }
@@ -300,15 +313,17 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
     }
   } else if (warp == 2 || warp == 3 || warp >= 8) {
-    // ===================================================================== gathers
-    // Chunks of 128 keys x 64 dims go round four pairs of warps, each warp fetching half of the keys (a gather4 of four
-    // rows per lane), so that a warp meets a stage's barriers once per 64 KB of the CTA's traffic.  The entries of the
-    // next tile are read while this one is gathered.
+    // ===================================================================== gathers (gather4: four rows x 64 dims)
+    // One lane issues one gather4 of a stage; the warps that fill a stage share its 32 SC of them, and stages go round
+    // the groups of such warps.  The entries of the next tile are read while this one is gathered.
+    // An empty or invalid slot reads row `slot` (any row would do: its P and dS are set to zero).
+    constexpr int PER = SC * 32 / M::WPS, GROUPS = 8 / M::WPS;
     const int gw = (warp < 8) ? warp - 2 : warp - 6;
-    const int turn = gw >> 1, rg = (gw & 1) * 16 + (lane & 15);
-    int m = 0;                             // chunks of the tiles before this one
+    const int grp = gw / M::WPS, gi = (gw % M::WPS) * PER + lane, cc = gi / 32, rg = gi % 32;
+    const bool active = lane < PER;
+    int m = 0;                             // stages of the tiles before this one
     for (int t = first; t < p.T && ok; t += stride) {
-      const int tiles = tiles_of(t), fill = p.fill[t];
+      const int tiles = tiles_of(t);
       if (tiles <= 0) continue;
       const int* ids = p.idx + static_cast<long long>(t) * p.k;
       auto entries = [&](int j) {          // k is a multiple of 64, a lane's four slots lie on one side of it
@@ -316,20 +331,24 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         return slot < p.k ? __ldg(reinterpret_cast<const int4*>(ids + slot)) : make_int4(-1, -1, -1, -1);
       };
       int4 e = entries(0);
-      for (int j = 0; j < tiles && ok; ++j, m += DCH) {
-        const int r0 = bwd_row(p, e.x, fill), r1 = bwd_row(p, e.y, fill), r2 = bwd_row(p, e.z, fill),
-                  r3 = bwd_row(p, e.w, fill);
+      for (int j = 0; j < tiles && ok; ++j, m += SPT) {
+        const int slot = (2 * j + rank) * NK + 4 * rg;
+        auto row = [&](int x, int i) {
+          return (x >= 0 && x < p.S) ? x : static_cast<int>(slot + i < p.S ? slot + i : 0);
+        };
+        const int r0 = row(e.x, 0), r1 = row(e.y, 1), r2 = row(e.z, 2), r3 = row(e.w, 3);
         if (j + 1 < tiles) e = entries(j + 1);
-        for (int c = (turn - m % 4 + 4) % 4; c < DCH; c += 4) {
-          const int st = (m + c) % NS;
+        for (int s = (grp + (GROUPS - 1) * m) % GROUPS; s < SPT; s += GROUPS) {   // (m + s) % GROUPS == grp
+          const int st = (m + s) % NS;
           const uint32_t full = lead + 8 * (B_RING_FULL + st);
           bool got = true;
           if (lane == 0) {
-            got = mbar_wait(cta.bar(B_RING_EMPTY + st), (((m + c) / NS) & 1) ^ 1, abort_flag);
-            if (got) mbar_arrive_expect_tx_remote(full, 64 * 128);
+            got = mbar_wait(cta.bar(B_RING_EMPTY + st), (((m + s) / NS) & 1) ^ 1, abort_flag);
+            if (got) mbar_arrive_expect_tx_remote(full, PER * 512);
           }
           if (!(ok = __shfl_sync(0xffffffffu, got, 0))) break;
-          if (lane < 16) tma2_gather4(ring + st * CHUNK + rg * 512, &tm_c, full, 64 * c, r0, r1, r2, r3);
+          if (active)
+            tma2_gather4(ring + (st * SC + cc) * CHUNK + rg * 512, &tm_c, full, 64 * (s * SC + cc), r0, r1, r2, r3);
         }
       }
     }
@@ -346,19 +365,25 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           const int ab = g % NACC;
           if (!(ok = warp_wait<true>(cta.bar(B_ACC_EMPTY + ab), ((g / NACC) & 1) ^ 1, abort_flag))) break;
           tc_fence_after();
-          for (int c = 0; c < DCH; ++c, rp.advance()) {
-            if (j == 0 && !(ok = warp_wait<true>(cta.bar(B_RES_FULL + c), n & 1, abort_flag))) break;
-            if (!(ok = warp_wait<true>(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
+          for (int sg = 0; sg < SPT; ++sg, rp.advance()) {
+            if (j == 0)
+              for (int c = sg * SC; c < (sg + 1) * SC && ok; ++c)
+                ok = warp_wait<true>(cta.bar(B_RES_FULL + c), n & 1, abort_flag);
+            if (!(ok = ok && warp_wait<true>(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
             tc_fence_after();
-            const uint64_t ad = smem_desc(ring + rp.stage * CHUNK, 16, 1024, kLayoutSW128);
-            const uint64_t bd = smem_desc(res + c * M::RES_CHUNK, 16, 1024, kLayoutSW128);
             if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma2_bf16_ss(tmem + (512 / NACC) * ab, ad + 2 * k, bd + 2 * k, c < 8 ? wide : narrow,
-                             (c | k) ? 1u : 0u);
+              for (int cc = 0; cc < SC; ++cc) {
+                const int c = sg * SC + cc;
+                const uint64_t ad = smem_desc(ring + (rp.stage * SC + cc) * CHUNK, 16, 1024, kLayoutSW128);
+                const uint64_t bd = smem_desc(res + c * M::RES_CHUNK, 16, 1024, kLayoutSW128);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma2_bf16_ss(tmem + (512 / NACC) * ab, ad + 2 * k, bd + 2 * k, c < 8 ? wide : narrow,
+                               (c | k) ? 1u : 0u);
+                if (j == tiles - 1) mma2_commit(cta.bar(B_RES_EMPTY + c));
+              }
               mma2_commit(cta.bar(B_RING_EMPTY + rp.stage));
-              if (j == tiles - 1) mma2_commit(cta.bar(B_RES_EMPTY + c));
             }
             __syncwarp();
           }
@@ -450,15 +475,18 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               d[i] = __float_as_uint(valid ? ds : 0.f);
             }
             if (slot < p.kp) {
-              uint4* ds4 = reinterpret_cast<uint4*>(out + 32 * c);
-              uint4* p4 = reinterpret_cast<uint4*>(out + p.HP + 32 * c);
+              // 32 bytes a store: whole sectors (with 16-byte stores the pass took 1466 us instead of XXX)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                auto pk = [&](const uint32_t (&v)[32], int q) {
-                  return pack_bf16(__uint_as_float(v[8 * i + 2 * q]), __uint_as_float(v[8 * i + 2 * q + 1]));
+              for (int i = 0; i < 2; ++i) {
+                auto put = [&](uint16_t* at, const uint32_t (&v)[32]) {
+                  uint32_t w[8];
+#pragma unroll
+                  for (int q = 0; q < 8; ++q)
+                    w[q] = pack_bf16(__uint_as_float(v[16 * i + 2 * q]), __uint_as_float(v[16 * i + 2 * q + 1]));
+                  st_global_32(at + 16 * i, w);
                 };
-                ds4[i] = make_uint4(pk(d, 0), pk(d, 1), pk(d, 2), pk(d, 3));
-                p4[i] = make_uint4(pk(s, 0), pk(s, 1), pk(s, 2), pk(s, 3));
+                put(out + 32 * c, d);
+                put(out + p.HP + 32 * c, s);
               }
             }
           }
@@ -675,8 +703,7 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
 
 // dq[t][:, 192 dims] = dS^T . C per item, accumulated over the token's keys in tensor memory (lane = head).
 __global__ void __launch_bounds__(mbw::dq::THREADS, 1)
-mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const __grid_constant__ CUtensorMap tm_c,
-                  const MlaBwdParams p) {
+mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams p) {
   using namespace mbw;
   using namespace mbw::dq;
   extern __shared__ uint8_t smem_raw[];
@@ -686,13 +713,11 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const __grid_consta
   const int warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(cta.bar(B_IDX_FULL + i), 1);
-      mbar_init(cta.bar(B_IDX_EMPTY + i), GATHER_WARPS);
       mbar_init(cta.bar(B_ACC_FULL + i), 1);
       mbar_init(cta.bar(B_ACC_EMPTY + i), 4);
     }
     for (int i = 0; i < NS; ++i) {
-      mbar_init(cta.bar(B_RING_FULL + i), GATHER_WARPS + 1);
+      mbar_init(cta.bar(B_RING_FULL + i), 128 + 1);
       mbar_init(cta.bar(B_RING_EMPTY + i), 1);
     }
   }
@@ -704,19 +729,12 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const __grid_consta
   int n = 0;
 
   if (warp == 0) {
-    // ===================================================================== index rows and dS tiles
+    // ===================================================================== dS tiles
     if (lane == 0) {
       Pipe<NS> rp;
       int issued = 0;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         const int t = item / 3, tiles = (p.n_end[t] + KT - 1) / KT;
-        if (tiles <= 0) continue;
-        const int ib = n & 1;
-        if (!(ok = mbar_wait(cta.bar(B_IDX_EMPTY + ib), ((n >> 1) & 1) ^ 1, abort_flag))) break;
-        mbar_arrive_expect_tx(cta.bar(B_IDX_FULL + ib), p.k * 4);
-        bulk_load(sbase + OFF_IDX + ib * mla::KMAX * 4, p.idx + static_cast<long long>(t) * p.k, p.k * 4,
-                  cta.bar(B_IDX_FULL + ib));
-        ++n;
         for (int j = 0; j < tiles; ++j, rp.advance(), ++issued) {
           if (!(ok = mbar_wait(cta.bar(B_RING_EMPTY + rp.stage), rp.phase ^ 1, abort_flag))) break;
           const uint32_t full = cta.bar(B_RING_FULL + rp.stage), dst = ring + rp.stage * STAGE;
@@ -725,52 +743,46 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const __grid_consta
             tma_load_2d(dst + i * HCHUNK, &tm_ds, full, 64 * i, t * p.kp + j * KT);
         }
       }
-      if (*abort_flag) {
-        if (n > 0) mbar_wait_drain(cta.bar(B_IDX_FULL + ((n - 1) & 1)), ((n - 1) >> 1) & 1);
+      if (*abort_flag)
         for (int i = max(0, issued - NS); i < issued; ++i)
           mbar_wait_drain(cta.bar(B_RING_FULL + i % NS), (i / NS) & 1);
-      }
     }
   } else if (warp == 2 || warp == 3 || warp >= 8) {
-    // ===================================================================== gathers
+    // ===================================================================== gathers (cp.async)
+    // Stages of 64 keys x 192 dims go round two groups of four warps, 16 keys a warp; eight lanes copy 128 bytes of a
+    // row.  (TMA's gather4, whose warp issues one of four rows about every 50 ns: 1006 us against 860 for 2048 tokens.)
+    // An empty slot's row is filled with zeros: a NaN in a row that no token selects must not meet its dS = 0.
     const int gw = (warp < 8) ? warp - 2 : warp - 6;
-    constexpr int kPer = G4 / GATHER_WARPS;                  // 6 gather4 a warp and stage
-    const int gi = gw * kPer + lane, cc = gi / (KT / 4), rg = gi % (KT / 4);
-    const bool active = lane < kPer;
-    Pipe<NS> rp;
-    int issued = 0;
+    const int grp = gw >> 2, rows = (gw & 3) * 16, sub = lane >> 3, unit = lane & 7;
+    int m = 0;                             // stages of the items before this one
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const int t = item / 3, d3 = item % 3, tiles = (p.n_end[t] + KT - 1) / KT;
-      if (tiles <= 0) continue;
-      const int ib = n & 1, fill = p.fill[t];
-      if (!(ok = warp_wait(cta.bar(B_IDX_FULL + ib), (n >> 1) & 1, abort_flag))) break;
-      const int* ids = reinterpret_cast<const int*>(cta.smem + OFF_IDX + ib * mla::KMAX * 4);
-      for (int j = 0; j < tiles; ++j, rp.advance(), ++issued) {
-        int r[4] = {0, 0, 0, 0};
-        if (active) {
+      const int* ids = p.idx + static_cast<long long>(t) * p.k;
+      // k is a multiple of the tile: every slot of a tile is below k
+      auto entry = [&](int j) { return j < tiles ? __ldg(ids + j * KT + rows + (lane & 15)) : -1; };
+      const int j0 = (grp + m) & 1;
+      int mine = entry(j0);
+      for (int j = j0; j < tiles; j += 2) {
+        const int st = (m + j) % NS;
+        const int next = entry(j + 2);
+        if (!(ok = warp_wait(cta.bar(B_RING_EMPTY + st), (((m + j) / NS) & 1) ^ 1, abort_flag))) break;
+        const uint32_t dst = ring + st * STAGE + A_BYTES + (rows + sub) * 128;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int slot = j * KT + 4 * rg + u;
-            r[u] = bwd_row(p, slot < p.k ? ids[slot] : -1, fill);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int e = __shfl_sync(0xffffffffu, mine, 4 * i + sub);
+          const bool valid = e >= 0 && e < p.S;
+          const char* src = reinterpret_cast<const char*>(p.c) + (valid ? static_cast<long long>(e) * (D * 2) : 0) +
+                            384 * d3 + 16 * unit;
+          const uint32_t at = dst + i * 512 + ((unit ^ ((4 * i + sub) & 7)) << 4);
+#pragma unroll
+          for (int c = 0; c < 3; ++c) cp_async16(at + c * HCHUNK, src + 128 * c, valid);
         }
-        bool got = true;
-        if (lane == 0) {
-          got = mbar_wait(cta.bar(B_RING_EMPTY + rp.stage), rp.phase ^ 1, abort_flag);
-          if (got) mbar_arrive_expect_tx(cta.bar(B_RING_FULL + rp.stage), kPer * 512);
-        }
-        if (!(ok = __shfl_sync(0xffffffffu, got, 0))) break;
-        if (active)
-          tma_gather4(ring + rp.stage * STAGE + A_BYTES + cc * HCHUNK + rg * 512, &tm_c,
-                      cta.bar(B_RING_FULL + rp.stage), 192 * d3 + 64 * cc, r[0], r[1], r[2], r[3]);
+        cp_async_arrive(cta.bar(B_RING_FULL + st));
+        mine = next;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(cta.bar(B_IDX_EMPTY + ib));
-      ++n;
+      m += tiles;
     }
-    if (lane == 0 && *abort_flag)
-      for (int i = max(0, issued - NS); i < issued; ++i)
-        mbar_wait_drain(cta.bar(B_RING_FULL + i % NS), (i / NS) & 1);
+    cp_async_wait_all();
   } else if (warp == 1) {
     // ===================================================================== MMA issue
     Pipe<NS> rp;
@@ -783,6 +795,7 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const __grid_consta
       tc_fence_after();
       for (int j = 0; j < tiles; ++j, rp.advance()) {
         if (!(ok = warp_wait(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
+        fence_proxy_async_smem();            // the gathered keys were written through the generic proxy
         tc_fence_after();
         const uint32_t at = ring + rp.stage * STAGE;
         const uint64_t ad = smem_desc(at, HCHUNK, 1024, kLayoutSW128);
