@@ -746,11 +746,11 @@ AttnBwdWs attn_bwd_ws(void* ws, int T, int64_t S, int H, int k) {
 dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx, const uint16_t* out,
                           const float* lse, const uint16_t* dout, int T, int H, int k, float scale, uint16_t* dq,
                           uint16_t* dc, const AttnBwdWs& w, cudaStream_t st) {
-  CUtensorMap tq, tdo, tc, tp128, tp64, tout;
+  CUtensorMap tq, tdo, tc, tp128, tp64;
   const size_t rows = size_t(w.Tc) * w.kp;
   if (!make_heads_map(&tq, q, T, H, mbw::D) || !make_heads_map(&tdo, dout, T, H, mbw::DV) ||
       !make_rows_map(&tc, c, S, mbw::D, 1) || !make_rows_map(&tp128, w.pds, rows, 2 * w.HP, 128) ||
-      !make_rows_map(&tp64, w.pds, rows, 2 * w.HP, 64) || !make_rows_map(&tout, w.sc.contrib, rows, mbw::D, 32))
+      !make_rows_map(&tp64, w.pds, rows, 2 * w.HP, 64))
     return DSA_ERR_CUDA;
   if (set_smem(mla_bwd_p_kernel<false>, mbw::p::Map<false>::SMEM) != cudaSuccess ||
       set_smem(mla_bwd_dc_kernel, mbw::dc::SMEM) != cudaSuccess ||
@@ -767,6 +767,7 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
     p.lse = lse + o * H;
     p.delta = w.delta;
     p.pds = w.pds;
+    p.contrib = w.sc.contrib;
     p.dq = dq + o * H * mbw::D;
     p.T = n;
     p.t0 = t0;
@@ -789,7 +790,7 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
     if (launch_pdl(mla_bwd_dc_kernel, dim3(std::min(sms, 3 * n)), dim3(mbw::dc::THREADS), mbw::dc::SMEM, st, tp128,
-                   tq, tdo, tout, p) != cudaSuccess)
+                   tq, tdo, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
     if (launch_pdl(mla_bwd_dq_kernel, dim3(std::min(sms, 3 * n)), dim3(mbw::dq::THREADS), mbw::dq::SMEM, st, tp64,

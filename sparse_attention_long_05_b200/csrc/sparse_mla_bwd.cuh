@@ -36,6 +36,7 @@ struct MlaBwdParams {
   const float* lse;            // [T, H]
   const float* delta;          // [T, H]
   uint16_t* pds;               // [T * kp, 2 HP] bf16: dS of HP heads, then P of HP heads, for every slot
+  uint16_t* contrib;           // [T * kp, 576] bf16: each entry's contribution to dc
   uint16_t* dq;                // [T, H, 576]
   int T, t0;                   // tokens of the chunk; the first one's index in q and dout
   int H, HP;                   // heads; heads rounded up to 64
@@ -109,11 +110,22 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
 }
 
-// one 32-byte store (32-byte aligned)
-__device__ __forceinline__ void st_global_32(void* at, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-               :: "l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
+// 32 rows of 8 N bf16 of a warp, one row a lane (packed in v), to rows `stride` bytes apart.  Turned in the warp's own
+// 512 N bytes of shared memory, so that N adjacent lanes write a row's piece (N = 8: whole 128-byte lines).
+template <int N>
+__device__ __forceinline__ void store_rows(uint8_t* buf, const uint32_t (&v)[4 * N], void* dst, long long stride) {
+  const int lane = lane_id();
+  // unit i of row r at unit i ^ x(r): eight lanes on end meet all 32 banks in both directions
+  auto at = [&](int r, int i) { return reinterpret_cast<uint4*>(buf + r * (16 * N) + ((i ^ (N == 8 ? r & 7 : (r >> 1) & 3)) << 4)); };
+#pragma unroll
+  for (int i = 0; i < N; ++i) *at(lane, i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  __syncwarp();
+  const int sub = lane / N, unit = lane % N;
+  char* to = static_cast<char*>(dst) + sub * stride + 16 * unit;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    *reinterpret_cast<uint4*>(to + (32 / N) * i * stride) = *at((32 / N) * i + sub, unit);
+  __syncwarp();
 }
 
 namespace mbw {
@@ -128,8 +140,8 @@ constexpr int OFF_TMEM = 512, OFF_ABORT = 516;
 
 // ---- mla_bwd_p_kernel
 namespace p {
-constexpr int THREADS = 448;            // w0 resident rows, w1 MMA, w2 w3 w8..13 gathers, w4..7 probabilities
-constexpr int NS_MAX = 5;
+constexpr int THREADS = 576;            // w0 resident rows, w1 MMA, w2 w3 w8..13 gathers, w4..7 w14..17 probabilities
+constexpr int NS_MAX = 4;
 constexpr int B_RES_FULL = 0, B_RES_EMPTY = B_RES_FULL + DCH, B_RING_FULL = B_RES_EMPTY + DCH;
 constexpr int B_RING_EMPTY = B_RING_FULL + NS_MAX, B_ACC_FULL = B_RING_EMPTY + NS_MAX, B_ACC_EMPTY = B_ACC_FULL + 4;
 constexpr int B_SUMS = B_ACC_EMPTY + 4;                       // objective: the other CTA's sums of a token (2 buffers)
@@ -142,11 +154,12 @@ template <bool KL> struct Map {
   static constexpr int RES_CHUNK = KL ? HCHUNK : CHUNK;       // a 64-dim chunk of the resident rows (the last: 64 rows)
   static constexpr int RES = 8 * RES_CHUNK + HCHUNK;          // 72 KB, 136 KB
   static constexpr int SC = KL ? 3 : 1;                       // gathered chunks (16 KB) of a ring stage
-  static constexpr int NS = KL ? 3 : 5;                       // ring stages
+  static constexpr int NS = KL ? 3 : 4;                       // ring stages
   static constexpr int WPS = KL ? 8 : 2;                      // warps that fill a stage
   static constexpr int NACC = KL ? 4 : 2;                     // accumulators of 128, 256 columns
   static constexpr int OFF_RING = OFF_RES + RES;
-  static constexpr int SMEM = OFF_RING + NS * SC * CHUNK + 1024;
+  static constexpr int OFF_TURN = OFF_RING + NS * SC * CHUNK;  // store_rows: 2 KB of each of eight warps
+  static constexpr int SMEM = OFF_TURN + (KL ? 0 : 8 * 2048) + 1024;
   static_assert(DCH % SC == 0 && SC * 32 % WPS == 0 && SC * 32 / WPS <= 32, "stage split");
 };
 static_assert(Map<false>::SMEM <= 232448 && Map<true>::SMEM <= 232448, "shared memory per CTA");
@@ -155,15 +168,15 @@ static_assert(OFF_RES % 1024 == 0 && OFF_SUMS + 32 <= BAR_BYTES && Map<true>::NS
 
 // ---- mla_bwd_dc_kernel
 namespace dc {
-constexpr int THREADS = 256;
-constexpr int NS = 5;                   // ring stages of [dS | P]: 128 keys x 64 heads (16 KB)
+constexpr int THREADS = 384;            // w0 resident rows, w1 MMA, w2 dS and P, w4..7 w8..11 contributions
+constexpr int NS = 3;                   // ring stages: dS or P of 128 keys x all heads (two 64-head blocks, 32 KB)
 constexpr int UNIT = 3 * HCHUNK;        // resident operand of 64 heads: 64 heads x 192 dims (24 KB)
 constexpr int NU = 4;                   // units: q of heads 0..63, 64..127, dout of the same
 constexpr int B_RES_FULL = 0, B_RES_EMPTY = B_RES_FULL + NU, B_RING_FULL = B_RES_EMPTY + NU;
 constexpr int B_RING_EMPTY = B_RING_FULL + NS, B_ACC_FULL = B_RING_EMPTY + NS, B_ACC_EMPTY = B_ACC_FULL + 2;
 static_assert((B_ACC_EMPTY + 2) * 8 <= OFF_TMEM, "barrier area");
-constexpr int OFF_RES = BAR_BYTES, OFF_RING = OFF_RES + NU * UNIT, OFF_OUT = OFF_RING + NS * CHUNK;
-constexpr int SMEM = OFF_OUT + 3 * CHUNK + 1024;
+constexpr int OFF_RES = BAR_BYTES, OFF_RING = OFF_RES + NU * UNIT, OFF_TURN = OFF_RING + NS * 2 * CHUNK;
+constexpr int SMEM = OFF_TURN + 8 * 4096 + 1024;
 static_assert(SMEM <= 232448, "shared memory per CTA");
 }  // namespace dc
 
@@ -312,7 +325,7 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         ++n;
       }
     }
-  } else if (warp == 2 || warp == 3 || warp >= 8) {
+  } else if (warp == 2 || warp == 3 || (warp >= 8 && warp < 14)) {
     // ===================================================================== gathers (gather4: four rows x 64 dims)
     // One lane issues one gather4 of a stage; the warps that fill a stage share its 32 SC of them, and stages go round
     // the groups of such warps.  The entries of the next tile are read while this one is gathered.
@@ -395,7 +408,10 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
     }
   } else {
-    // ===================================================================== probabilities (warps 4..7, one key a thread)
+    // ===================================================================== probabilities (one key a thread)
+    // Two groups of four warps take tiles in turn: the work on a tile is a chain of tensor-memory loads, exponentials and
+    // stores, and one group alone needed twice the tile's MMA time (1300 us for 2048 tokens, against XXX).
+    const int grp = warp >= 14 ? 1 : 0;
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     constexpr float kLog2e = 1.4426950408889634f;
@@ -404,25 +420,41 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const int tiles = tiles_of(t);
       const long long base = static_cast<long long>(t) * p.k;
       if constexpr (KL) {
-        for (int i = tiles * 2 * NK + rank * NK + row; i < p.k; i += 2 * NK) p.dsel[base + i] = 0.f;
+        for (int i = (2 * (tiles + grp) + rank) * NK + row; i < p.k; i += 4 * NK) p.dsel[base + i] = 0.f;
       }
       if (tiles <= 0) continue;
-      // the token's lse (in log2 units) and delta.  A head without any probability mass (lse = -inf) and the heads that
-      // only fill up the tile get +inf: P = 0.
+      // the token's -lse (in log2 units) and -scale delta.  A head without any probability mass (lse = -inf) and the heads
+      // that only fill up the tile get -inf: P = 0.
       float* hs = reinterpret_cast<float*>(cta.smem + OFF_HEADS) + (n & 1) * 256;
-      {
+      if (grp == 0) {
         const long long at = static_cast<long long>(t) * p.H + row;
         const float l = row < p.H ? p.lse[at] : -INFINITY;
-        hs[row] = l == -INFINITY ? INFINITY : l * kLog2e;
-        if (!KL) hs[128 + row] = row < p.H ? p.delta[at] : 0.f;
+        hs[row] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        if (!KL) hs[128 + row] = row < p.H ? -p.delta[at] * p.scale : 0.f;
       }
-      if (!(ok = named_bar_all(1, 128, ok))) break;
+      if (!(ok = named_bar_all(1, 256, ok))) break;
       [[maybe_unused]] float m_i = -INFINITY, z_i = 0.f, s_a = 0.f;
-      for (int j = 0; j < tiles; ++j, ++g) {
-        const int ab = g % NACC, slot = (2 * j + rank) * NK + row;
-        const int e = slot < p.k ? __ldg(p.idx + base + slot) : -1;
-        const bool valid = e >= 0 && e < p.S;
-        if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), (g / NACC) & 1, abort_flag))) break;
+      // the entry (KL: and its index score) of the next tile is read while this one is worked on
+      auto entry = [&](int j) {
+        const int slot = (2 * j + rank) * NK + row;
+        return slot < p.k ? __ldg(p.idx + base + slot) : -1;
+      };
+      auto score = [&](int j) {
+        const int slot = (2 * j + rank) * NK + row;
+        return KL && slot < p.k ? __ldg(p.sel + base + slot) : 0.f;
+      };
+      const int j0 = (g ^ grp) & 1;          // this group's first tile: (g + j) % 2 == grp
+      int e_next = j0 < tiles ? entry(j0) : -1;
+      [[maybe_unused]] float x_next = j0 < tiles ? score(j0) : 0.f;
+      for (int j = j0; j < tiles; j += 2) {
+        const int ab = (g + j) % NACC, slot = (2 * j + rank) * NK + row;
+        const bool valid = e_next >= 0 && e_next < p.S;
+        [[maybe_unused]] const float x = x_next;
+        if (j + 2 < tiles) {
+          e_next = entry(j + 2);
+          x_next = score(j + 2);
+        }
+        if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), ((g + j) / NACC) & 1, abort_flag))) break;
         tc_fence_after();
         const uint32_t acc = lane_addr + tmem + (512 / NACC) * ab;
         auto release = [&]() {
@@ -432,22 +464,25 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         };
         if constexpr (KL) {
           float a0 = 0.f, a1 = 0.f;
-          for (int c = 0; c < p.HP / 32; ++c) {
-            uint32_t v[32];
-            tmem_ld32(acc + 32 * c, v);
+          for (int c = 0; c < p.HP / 64; ++c) {
+            uint32_t v[64];
+            tmem_ld32(acc + 64 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+            tmem_ld32(acc + 64 * c + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
             tmem_wait_ld();
+            if (c == p.HP / 64 - 1) release();
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              a0 += ex2_approx(fmaf(__uint_as_float(v[i]), p.scale_log2, -hs[32 * c + i]));
-              a1 += ex2_approx(fmaf(__uint_as_float(v[i + 1]), p.scale_log2, -hs[32 * c + i + 1]));
+            for (int i = 0; i < 64; i += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(hs + 64 * c + i);
+              a0 += ex2_approx(fmaf(__uint_as_float(v[i]), p.scale_log2, l.x));
+              a1 += ex2_approx(fmaf(__uint_as_float(v[i + 1]), p.scale_log2, l.y));
+              a0 += ex2_approx(fmaf(__uint_as_float(v[i + 2]), p.scale_log2, l.z));
+              a1 += ex2_approx(fmaf(__uint_as_float(v[i + 3]), p.scale_log2, l.w));
             }
           }
-          release();
           if (slot < p.k) {
             const float a = valid ? a0 + a1 : 0.f;
-            p.dsel[base + slot] = a;       // the same thread reads it back below
+            p.dsel[base + slot] = a;       // read back below, behind a barrier
             if (valid) {
-              const float x = p.sel[base + slot];
               s_a += a;
               if (x > m_i) {
                 z_i = z_i * ex2_approx((m_i - x) * kLog2e) + 1.f;
@@ -458,55 +493,57 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
           }
         } else {
-          uint16_t* out = p.pds + (static_cast<long long>(t) * p.kp + slot) * (2 * p.HP);
-          const int blocks = p.HP / 32;
-#pragma unroll 2
-          for (int c = 0; c < blocks; ++c) {
-            uint32_t s[32], d[32];
+          // the warp's 32 keys; kp is a multiple of 128: they lie on one side of it
+          uint8_t* turn = cta.smem + M::OFF_TURN + (4 * grp + quad) * 2048;
+          const int slot0 = slot - lane;
+          uint16_t* out = p.pds + (static_cast<long long>(t) * p.kp + slot0) * (2 * p.HP);
+          const uint32_t keep = valid ? 0xffffffffu : 0u;     // an empty slot's S or dP may be NaN: its bits go
+#pragma unroll 1
+          for (int c = 0; c < p.HP / 32; ++c) {
+            uint32_t s[32], d[32], ps[16], ds[16];
             tmem_ld32(acc + 32 * c, s);
             tmem_ld32(acc + p.HP + 32 * c, d);
             tmem_wait_ld();
-            if (c == blocks - 1) release();
+            if (c == p.HP / 32 - 1) release();
+            const float* hl = hs + 32 * c;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float pr = ex2_approx(fmaf(__uint_as_float(s[i]), p.scale_log2, -hs[32 * c + i]));
-              const float ds = pr * (__uint_as_float(d[i]) - hs[128 + 32 * c + i]) * p.scale;
-              s[i] = __float_as_uint(valid ? pr : 0.f);
-              d[i] = __float_as_uint(valid ? ds : 0.f);
+            for (int i = 0; i < 32; i += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(hl + i), m = *reinterpret_cast<const float4*>(hl + 128 + i);
+              const float p0 = ex2_approx(fmaf(__uint_as_float(s[i]), p.scale_log2, l.x));
+              const float p1 = ex2_approx(fmaf(__uint_as_float(s[i + 1]), p.scale_log2, l.y));
+              const float p2 = ex2_approx(fmaf(__uint_as_float(s[i + 2]), p.scale_log2, l.z));
+              const float p3 = ex2_approx(fmaf(__uint_as_float(s[i + 3]), p.scale_log2, l.w));
+              ps[i / 2] = pack_bf16(p0, p1) & keep;
+              ps[i / 2 + 1] = pack_bf16(p2, p3) & keep;
+              ds[i / 2] = pack_bf16(p0 * fmaf(__uint_as_float(d[i]), p.scale, m.x),
+                                    p1 * fmaf(__uint_as_float(d[i + 1]), p.scale, m.y)) & keep;
+              ds[i / 2 + 1] = pack_bf16(p2 * fmaf(__uint_as_float(d[i + 2]), p.scale, m.z),
+                                        p3 * fmaf(__uint_as_float(d[i + 3]), p.scale, m.w)) & keep;
             }
-            if (slot < p.kp) {
-              // 32 bytes a store: whole sectors (with 16-byte stores the pass took 1466 us instead of XXX)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                auto put = [&](uint16_t* at, const uint32_t (&v)[32]) {
-                  uint32_t w[8];
-#pragma unroll
-                  for (int q = 0; q < 8; ++q)
-                    w[q] = pack_bf16(__uint_as_float(v[16 * i + 2 * q]), __uint_as_float(v[16 * i + 2 * q + 1]));
-                  st_global_32(at + 16 * i, w);
-                };
-                put(out + 32 * c, d);
-                put(out + p.HP + 32 * c, s);
-              }
+            if (slot0 < p.kp) {
+              store_rows<4>(turn, ds, out + 32 * c, 4 * p.HP);
+              store_rows<4>(turn, ps, out + p.HP + 32 * c, 4 * p.HP);
             }
           }
         }
       }
-      if (!(ok = named_bar_all(1, 128, ok))) break;
+      g += tiles;
+      if (!(ok = named_bar_all(1, 256, ok))) break;
       if constexpr (KL) {
-        // the token's sums over the pair's 256 threads, then g (softmax(I) - p) for each slot
+        // the token's sums over the pair's 512 threads, then g (softmax(I) - p) for each slot
         float mm = m_i;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-        float* rs = hs + 128;              // [4 warps][max, sum of exp, sum of a]
+        float* rs = hs + 128;              // [8 warps][max, sum of exp, sum of a]
         float z = m_i == -INFINITY ? 0.f : z_i * ex2_approx((m_i - mm) * kLog2e);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
           z += __shfl_xor_sync(0xffffffffu, z, d);
           s_a += __shfl_xor_sync(0xffffffffu, s_a, d);
         }
-        if (lane == 0) { rs[3 * quad] = mm; rs[3 * quad + 1] = z; rs[3 * quad + 2] = s_a; }
-        named_bar_sync(1, 128);
+        const int wi = 4 * grp + quad;
+        if (lane == 0) { rs[3 * wi] = mm; rs[3 * wi + 1] = z; rs[3 * wi + 2] = s_a; }
+        named_bar_sync(1, 256);
         auto join = [&](float& ma, float& za, float mb, float zb) {
           const float mx = fmaxf(ma, mb);
           const float fa = ma > -INFINITY ? ex2_approx((ma - mx) * kLog2e) : 0.f;
@@ -516,20 +553,20 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         };
         float m_all = rs[0], z_all = rs[1], a_all = rs[2];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) {
+        for (int w = 1; w < 8; ++w) {
           join(m_all, z_all, rs[3 * w], rs[3 * w + 1]);
           a_all += rs[3 * w + 2];
         }
         // the other CTA's sums (buffer n & 1: it cannot be two tokens ahead, as it needs this CTA's sums of each)
         const int sb = n & 1;
-        if (row == 0) {
+        if (row == 0 && grp == 0) {
           mbar_arrive_expect_tx(cta.bar(B_SUMS + sb), 16);
           st_async_v4(map_cluster(sbase + OFF_SUMS + 16 * sb, rank ^ 1),
                       make_uint4(__float_as_uint(m_all), __float_as_uint(z_all), __float_as_uint(a_all), 0),
                       map_cluster(cta.bar(B_SUMS + sb), rank ^ 1));
         }
         ok = warp_wait<true>(cta.bar(B_SUMS + sb), (n >> 1) & 1, abort_flag);
-        if (!(ok = named_bar_all(1, 128, ok))) break;
+        if (!(ok = named_bar_all(1, 256, ok))) break;
         const float4 other = *reinterpret_cast<const float4*>(cta.smem + OFF_SUMS + 16 * sb);
         if (rank == 0) {                   // both CTAs join the two halves in the same order
           join(m_all, z_all, other.x, other.y);
@@ -543,11 +580,11 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         const float up = p.dkl ? p.dkl[t] : 1.f;
         const float iz = z_all > 0.f ? 1.f / z_all : 0.f, ia = a_all > 0.f ? 1.f / a_all : 0.f;
-        for (int i = rank * NK + row; i < min(tiles * 2 * NK, p.k); i += 2 * NK) {
+        for (int i = (2 * grp + rank) * NK + row; i < min(tiles * 2 * NK, p.k); i += 4 * NK) {
           const int e = __ldg(p.idx + base + i);
           const float x = p.sel[base + i];
           const float soft = x > -INFINITY ? ex2_approx((x - m_all) * kLog2e) * iz : 0.f;
-          p.dsel[base + i] = (e >= 0 && e < p.S) ? up * (soft - p.dsel[base + i] * ia) : 0.f;
+          p.dsel[base + i] = (e >= 0 && e < p.S) ? up * (soft - __ldcg(p.dsel + base + i) * ia) : 0.f;
         }
       }
       ++n;
@@ -559,8 +596,7 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 // Contributions to dc: out[t kp + slot][d] = sum_h dS q[t][h][d] + P dout[t][h][d] for 192 dims d per item.
 __global__ void __launch_bounds__(mbw::dc::THREADS, 1)
 mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_constant__ CUtensorMap tm_q,
-                  const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_out,
-                  const MlaBwdParams p) {
+                  const __grid_constant__ CUtensorMap tm_do, const MlaBwdParams p) {
   using namespace mbw;
   using namespace mbw::dc;
   extern __shared__ uint8_t smem_raw[];
@@ -608,12 +644,14 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
       int issued = 0;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         const int t = item / 3, tiles = (p.n_end[t] + NK - 1) / NK;
-        for (int i = 0; i < tiles * units; ++i, rp.advance(), ++issued) {
-          if (!(ok = mbar_wait(cta.bar(B_RING_EMPTY + rp.stage), rp.phase ^ 1, abort_flag))) break;
-          mbar_arrive_expect_tx(cta.bar(B_RING_FULL + rp.stage), CHUNK);
-          tma_load_2d(ring + rp.stage * CHUNK, &tm_pds, cta.bar(B_RING_FULL + rp.stage), 64 * (i % units),
-                      t * p.kp + (i / units) * NK);
-        }
+        for (int j = 0; j < tiles && ok; ++j)
+          for (int u = 0; u < 2; ++u, rp.advance(), ++issued) {        // dS, then P
+            if (!(ok = mbar_wait(cta.bar(B_RING_EMPTY + rp.stage), rp.phase ^ 1, abort_flag))) break;
+            const uint32_t full = cta.bar(B_RING_FULL + rp.stage);
+            mbar_arrive_expect_tx(full, hb * CHUNK);
+            for (int i = 0; i < hb; ++i)
+              tma_load_2d(ring + (2 * rp.stage + i) * CHUNK, &tm_pds, full, 64 * (u * hb + i), t * p.kp + j * NK);
+          }
       }
       if (*abort_flag)
         for (int i = max(0, issued - NS); i < issued; ++i)
@@ -630,20 +668,24 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
         const int ab = g & 1;
         if (!(ok = warp_wait(cta.bar(B_ACC_EMPTY + ab), ((g >> 1) & 1) ^ 1, abort_flag))) break;
         tc_fence_after();
-        for (int u = 0; u < units; ++u, rp.advance()) {
-          if (j == 0 && !(ok = warp_wait(cta.bar(B_RES_FULL + u), n & 1, abort_flag))) break;
-          if (!(ok = warp_wait(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
+        for (int half = 0; half < 2; ++half, rp.advance()) {   // dS . q, then P . dout
+          if (j == 0)
+            for (int i = 0; i < hb && ok; ++i) ok = warp_wait(cta.bar(B_RES_FULL + half * hb + i), n & 1, abort_flag);
+          if (!(ok = ok && warp_wait(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
           tc_fence_after();
-          const uint64_t ad = smem_desc(ring + rp.stage * CHUNK, 16, 1024, kLayoutSW128);
+          const uint64_t ad = smem_desc(ring + 2 * rp.stage * CHUNK, 16, 1024, kLayoutSW128);
           // heads x dims, dims contiguous (MN-major): 64-dim atoms 8 KB apart, 8-head groups 1 KB apart
-          const uint64_t bd = smem_desc(res + u * UNIT, HCHUNK, 1024, kLayoutSW128);
-          const uint32_t idesc = idesc_bf16(128, (u >= hb && d3 == 2) ? 128 : 192, true);
+          const uint64_t bd = smem_desc(res + half * hb * UNIT, HCHUNK, 1024, kLayoutSW128);
+          const uint32_t idesc = idesc_bf16(128, (half && d3 == 2) ? 128 : 192, true);
           if (elect_one()) {
+            for (int i = 0; i < hb; ++i) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_bf16_ss(tmem + 256 * ab, ad + 2 * k, bd + ((k * 2048) >> 4), idesc, (u | k) ? 1u : 0u);
+              for (int k = 0; k < 4; ++k)
+                mma_bf16_ss(tmem + 256 * ab, ad + ((i * CHUNK) >> 4) + 2 * k, bd + ((i * UNIT + k * 2048) >> 4), idesc,
+                            (half | i | k) ? 1u : 0u);
+              if (j == tiles - 1) mma_commit(cta.bar(B_RES_EMPTY + half * hb + i));
+            }
             mma_commit(cta.bar(B_RING_EMPTY + rp.stage));
-            if (j == tiles - 1) mma_commit(cta.bar(B_RES_EMPTY + u));
           }
           __syncwarp();
         }
@@ -655,48 +697,36 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
     }
   } else if (warp >= 4) {
     // ===================================================================== contributions out (one key a thread)
+    // two groups of four warps take tiles in turn, each with an accumulator of its own
+    const int grp = (warp - 4) >> 2;
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     int g = 0;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const int t = item / 3, d3 = item % 3, tiles = (p.n_end[t] + NK - 1) / NK;
-      for (int j = 0; j < tiles; ++j, ++g) {
-        const int ab = g & 1;
-        if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), (g >> 1) & 1, abort_flag))) break;
+      for (int j = (g ^ grp) & 1; j < tiles; j += 2) {
+        const int ab = grp;
+        if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), ((g + j) >> 1) & 1, abort_flag))) break;
         tc_fence_after();
+        uint16_t* out = p.contrib + (static_cast<long long>(t) * p.kp + j * NK + quad * 32) * D + 192 * d3;
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
-          // each warp stages and stores its own 32 rows, 64 dims at a time: the store of this piece one tile ago has
-          // read its staging area once at most the two later ones are pending
-          uint32_t v[64];
-          uint32_t (&v0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
-          uint32_t (&v1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32]);
-          tmem_ld32(lane_addr + tmem + 256 * ab + 64 * c, v0);
-          tmem_ld32(lane_addr + tmem + 256 * ab + 64 * c + 32, v1);
-          if (lane == 0) bulk_wait_read<2>();
-          __syncwarp();
+          uint32_t v[64], w[32];
+          tmem_ld32(lane_addr + tmem + 256 * ab + 64 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+          tmem_ld32(lane_addr + tmem + 256 * ab + 64 * c + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
           tmem_wait_ld();
-          if (c == 2) tc_fence_before();
-          __syncwarp();
-          if (c == 2 && lane == 0) mbar_arrive(cta.bar(B_ACC_EMPTY + ab));
-          // 128-byte swizzled rows of 64 dims: 16-byte unit u of row r at unit u ^ (r % 8)
-          uint8_t* line = cta.smem + OFF_OUT + c * CHUNK + row * 128;
+          if (c == 2) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(cta.bar(B_ACC_EMPTY + ab));
+          }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            auto pk = [&](int q) { return pack_bf16(__uint_as_float(v[8 * i + 2 * q]), __uint_as_float(v[8 * i + 2 * q + 1])); };
-            *reinterpret_cast<uint4*>(line + ((i ^ (row & 7)) << 4)) = make_uint4(pk(0), pk(1), pk(2), pk(3));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&tm_out, sbase + OFF_OUT + c * CHUNK + quad * 32 * 128, 192 * d3 + 64 * c,
-                         t * p.kp + j * NK + quad * 32);
-            bulk_commit();
-          }
+          for (int i = 0; i < 32; ++i) w[i] = pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+          store_rows<8>(cta.smem + OFF_TURN + (4 * grp + quad) * 4096, w, out + 64 * c, 2 * D);
         }
       }
+      g += tiles;
     }
-    if (lane == 0) bulk_wait_all();
   }
   bwd_end(cta);
 }
