@@ -134,40 +134,46 @@ def _check(fn: str, code: int):
         raise DsaError(fn, code)
 
 
-def _want(fn: str, device, **args):
-    """Each argument name=(tensor or None, dtype, shape): a contiguous tensor of that type and shape on `device`."""
-    for name, (t, dtype, shape) in args.items():
+def _want(fn: str, device, args):
+    """Each argument (name, tensor or None, dtype, shape) is a contiguous tensor of that type and shape on `device`;
+    returns their device pointers (None for None).  Kept short: a call's checks run on every step of a loop."""
+    ptrs = []
+    for name, t, dtype, shape in args:
         if t is None:
+            ptrs.append(None)
             continue
-        if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
+        if t.dtype is not dtype or t.shape != shape or t.device != device:
             raise ValueError(f"{fn}: {name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {shape} on "
                              f"{device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name}: libdsa takes contiguous tensors")
+        ptrs.append(t.data_ptr())
+    return ptrs
 
 
-class _On:
-    """The device of a call's tensors and the stream it runs on: the given one, or the device's current one.  Buffers
-    allocated inside belong to that stream."""
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, fn: str, device, stream):
-        if device.type != "cuda":
-            raise ValueError(f"{fn}: libdsa takes device tensors")
-        self.device = device
-        self.own = stream is None
-        self.stream = torch.cuda.current_stream(device) if self.own else stream
-        if self.stream.device != device:
-            raise ValueError(f"{fn}: the stream is on {self.stream.device}, the tensors on {device}")
-        self.guard = None
 
-    def __enter__(self):
-        if not self.own or torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.stream(self.stream)       # also makes its device current
-            self.guard.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+def _elsewhere(fn: str, device, stream):
+    """None when a call runs on the current device's current stream; else a context that makes the tensors' device and
+    the given stream (or that device's current one) current, in which the call is made again: what it allocates then
+    belongs to the stream it runs on."""
+    if stream is None and device.type == "cuda" and _current_device() == device.index:
+        return None
+    if device.type != "cuda":
+        raise ValueError(f"{fn}: libdsa takes device tensors")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream)
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+
+def _ws(fn: str, ws, need: int, device):
+    """The workspace (allocated when None) as (tensor, pointer, bytes)."""
+    if ws is None:
+        ws = torch.empty((need,), dtype=torch.uint8, device=device)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"{fn}: the workspace is a contiguous tensor on {device}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def dsa_num_sms() -> int:
@@ -234,19 +240,21 @@ def dsa_sparse_mla_attn_backward(q, c, idx, out, lse, dout, scale: float, dq=Non
     T, H, _ = q.shape
     S, k, dev = c.shape[0], idx.shape[1], q.device
     bf16 = torch.bfloat16
-    _want(fn, dev, q=(q, bf16, (T, H, 576)), c=(c, bf16, (S, 576)), idx=(idx, torch.int32, (T, k)),
-          out=(out, bf16, (T, H, 512)), lse=(lse, torch.float32, (T, H)), dout=(dout, bf16, (T, H, 512)),
-          dq=(dq, bf16, (T, H, 576)), dc=(dc, bf16, (S, 576)))
-    with _On(fn, dev, stream) as st:
-        if dq is None:
-            dq = torch.empty((T, H, 576), dtype=bf16, device=dev)
-        if dc is None:
-            dc = torch.empty((S, 576), dtype=bf16, device=dev)
-        if ws is None:
-            ws = torch.empty((dsa_sparse_mla_attn_backward_workspace_size(T, S, H, k),), dtype=torch.uint8, device=dev)
-        _check(fn, _lib.dsa_sparse_mla_attn_backward(
-            _ptr(q), _ptr(c), S, _ptr(idx), _ptr(out), _ptr(lse), _ptr(dout), T, H, k, float(scale), _ptr(dq), _ptr(dc),
-            _ptr(ws), ws.numel(), st))
+    at = _elsewhere(fn, dev, stream)
+    if at is not None:
+        with at:
+            return dsa_sparse_mla_attn_backward(q, c, idx, out, lse, dout, scale, dq, dc, ws)
+    if dq is None:
+        dq = torch.empty((T, H, 576), dtype=bf16, device=dev)
+    if dc is None:
+        dc = torch.empty((S, 576), dtype=bf16, device=dev)
+    pq, pc, pi, po, pl, pd, pdq, pdc = _want(fn, dev, (
+        ("q", q, bf16, (T, H, 576)), ("c", c, bf16, (S, 576)), ("idx", idx, torch.int32, (T, k)),
+        ("out", out, bf16, (T, H, 512)), ("lse", lse, torch.float32, (T, H)), ("dout", dout, bf16, (T, H, 512)),
+        ("dq", dq, bf16, (T, H, 576)), ("dc", dc, bf16, (S, 576))))
+    ws, pw, nw = _ws(fn, ws, 0 if ws is not None else _lib.dsa_sparse_mla_attn_backward_workspace_size(T, S, H, k),
+                     dev)
+    _check(fn, _lib.dsa_sparse_mla_attn_backward(pq, pc, S, pi, po, pl, pd, T, H, k, scale, pdq, pdc, pw, nw, _current_stream(dev.index)))
     return dq, dc
 
 
@@ -274,17 +282,19 @@ def dsa_indexer_kl_backward(q, c, idx, sel_scores, lse, dkl, scale: float, dsel=
     fn = "dsa_indexer_kl_backward"
     T, H, _ = q.shape
     S, k, dev = c.shape[0], idx.shape[1], q.device
-    f32 = torch.float32
-    _want(fn, dev, q=(q, torch.bfloat16, (T, H, 576)), c=(c, torch.bfloat16, (S, 576)), idx=(idx, torch.int32, (T, k)),
-          sel_scores=(sel_scores, f32, (T, k)), lse=(lse, f32, (T, H)), dkl=(dkl, f32, (T,)), dsel=(dsel, f32, (T, k)))
-    with _On(fn, dev, stream) as st:
-        if dsel is None:
-            dsel = torch.empty((T, k), dtype=f32, device=dev)
-        if ws is None:
-            ws = torch.empty((dsa_indexer_kl_backward_workspace_size(T),), dtype=torch.uint8, device=dev)
-        _check(fn, _lib.dsa_indexer_kl_backward(
-            _ptr(q), _ptr(c), S, _ptr(idx), _ptr(sel_scores), _ptr(lse), _ptr(dkl), T, H, k, float(scale), _ptr(dsel),
-            _ptr(ws), ws.numel(), st))
+    f32, bf16 = torch.float32, torch.bfloat16
+    at = _elsewhere(fn, dev, stream)
+    if at is not None:
+        with at:
+            return dsa_indexer_kl_backward(q, c, idx, sel_scores, lse, dkl, scale, dsel, ws)
+    if dsel is None:
+        dsel = torch.empty((T, k), dtype=f32, device=dev)
+    pq, pc, pi, ps, pl, pk, pd = _want(fn, dev, (
+        ("q", q, bf16, (T, H, 576)), ("c", c, bf16, (S, 576)), ("idx", idx, torch.int32, (T, k)),
+        ("sel_scores", sel_scores, f32, (T, k)), ("lse", lse, f32, (T, H)), ("dkl", dkl, f32, (T,)),
+        ("dsel", dsel, f32, (T, k))))
+    ws, pw, nw = _ws(fn, ws, 0 if ws is not None else _lib.dsa_indexer_kl_backward_workspace_size(T), dev)
+    _check(fn, _lib.dsa_indexer_kl_backward(pq, pc, S, pi, ps, pl, pk, T, H, k, scale, pd, pw, nw, _current_stream(dev.index)))
     return dsel
 
 
@@ -300,22 +310,25 @@ def dsa_indexer_scores_backward(q_idx, q_scale, k_idx, k_scale, w, idx, dsel, dq
     T, H_I, d_I = q_idx.shape
     S, k, dev = k_idx.shape[0], idx.shape[1], q_idx.device
     f32, bf16, e4m3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
-    _want(fn, dev, q_idx=(q_idx, e4m3, (T, H_I, d_I)), q_scale=(q_scale, f32, (T,)), k_idx=(k_idx, e4m3, (S, d_I)),
-          k_scale=(k_scale, f32, (S,)), w=(w, f32, (T, H_I)), idx=(idx, torch.int32, (T, k)), dsel=(dsel, f32, (T, k)),
-          dq=(dq, bf16, (T, H_I, d_I)), dk=(dk, bf16, (S, d_I)), dw=(dw, f32, (T, H_I)))
-    with _On(fn, dev, stream) as st:
-        if dq is None:
-            dq = torch.empty((T, H_I, d_I), dtype=bf16, device=dev)
-        if dk is None:
-            dk = torch.empty((S, d_I), dtype=bf16, device=dev)
-        if dw is None:
-            dw = torch.empty((T, H_I), dtype=f32, device=dev)
-        if ws is None:
-            ws = torch.empty((dsa_indexer_scores_backward_workspace_size(T, S, H_I, d_I, k),), dtype=torch.uint8,
-                             device=dev)
-        _check(fn, _lib.dsa_indexer_scores_backward(
-            _ptr(q_idx), _ptr(q_scale), _ptr(k_idx), _ptr(k_scale), _ptr(w), _ptr(idx), _ptr(dsel), T, S, H_I, d_I, k,
-            _ptr(dq), _ptr(dk), _ptr(dw), _ptr(ws), ws.numel(), st))
+    at = _elsewhere(fn, dev, stream)
+    if at is not None:
+        with at:
+            return dsa_indexer_scores_backward(q_idx, q_scale, k_idx, k_scale, w, idx, dsel, dq, dk, dw, ws)
+    if dq is None:
+        dq = torch.empty((T, H_I, d_I), dtype=bf16, device=dev)
+    if dk is None:
+        dk = torch.empty((S, d_I), dtype=bf16, device=dev)
+    if dw is None:
+        dw = torch.empty((T, H_I), dtype=f32, device=dev)
+    pq, pqs, pk, pks, pw_, pi, pe, pdq, pdk, pdw = _want(fn, dev, (
+        ("q_idx", q_idx, e4m3, (T, H_I, d_I)), ("q_scale", q_scale, f32, (T,)), ("k_idx", k_idx, e4m3, (S, d_I)),
+        ("k_scale", k_scale, f32, (S,)), ("w", w, f32, (T, H_I)), ("idx", idx, torch.int32, (T, k)),
+        ("dsel", dsel, f32, (T, k)), ("dq", dq, bf16, (T, H_I, d_I)), ("dk", dk, bf16, (S, d_I)),
+        ("dw", dw, f32, (T, H_I))))
+    ws, pw, nw = _ws(fn, ws, 0 if ws is not None else
+                     _lib.dsa_indexer_scores_backward_workspace_size(T, S, H_I, d_I, k), dev)
+    _check(fn, _lib.dsa_indexer_scores_backward(pq, pqs, pk, pks, pw_, pi, pe, T, S, H_I, d_I, k, pdq, pdk, pdw, pw,
+                                                nw, _current_stream(dev.index)))
     return dq, dk, dw
 
 
@@ -334,22 +347,30 @@ def dsa_rope_frequencies(rot_dim: int, base: float = 10000.0, factor: float = 1.
 
 
 def _rope(fn: str, x, inv_freq, positions, pos0, rot_off, interleaved, mscale, out, stream):
-    if x.dim() != 3 or (out is not None and out.shape != x.shape):
+    dtype, dev = x.dtype, x.device
+    if dtype not in _ROPE_DTYPES:
+        raise ValueError(f"{fn}: takes bf16 or fp32 tensors")
+    if x.dim() != 3:
         raise ValueError(f"{fn}: takes [T, H, D] tensors")
     T, H, D = x.shape
-    dev = x.device
-    if x.dtype not in _ROPE_DTYPES or (out is not None and (out.dtype != x.dtype or out.device != dev)):
-        raise ValueError(f"{fn}: takes bf16 or fp32 tensors, both of one type and device")
-    if (D > 1 and x.stride(2) != 1) or (out is not None and D > 1 and out.stride(2) != 1):
+    R = 2 * inv_freq.numel()
+    at = _elsewhere(fn, dev, stream)
+    if at is not None:
+        with at:
+            return _rope(fn, x, inv_freq, positions, pos0, rot_off, interleaved, mscale, out, None)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=dtype, device=dev)
+    elif out.shape != x.shape or out.dtype is not dtype or out.device != dev:
+        raise ValueError(f"{fn}: input and result are of one shape, type and device")
+    xt, xh, x1 = x.stride()
+    ot, oh, o1 = out.stride()
+    if D > 1 and (x1 != 1 or o1 != 1):
         raise ValueError(f"{fn}: the dims of a head must be adjacent")
-    _want(fn, dev, inv_freq=(inv_freq, torch.float64, (inv_freq.numel(),)), positions=(positions, torch.int32, (T,)))
-    with _On(fn, dev, stream) as st:
-        if out is None:
-            out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
-        _check(fn, getattr(_lib, fn)(
-            ctypes.c_void_p(x.data_ptr()), x.stride(0), x.stride(1), ctypes.c_void_p(out.data_ptr()), out.stride(0),
-            out.stride(1), _ptr(positions), pos0, _ptr(inv_freq), T, H, D, rot_off, 2 * inv_freq.numel(),
-            1 if interleaved else 0, float(mscale), _ROPE_DTYPES[x.dtype], st))
+    pf, pp = _want(fn, dev, (("inv_freq", inv_freq, torch.float64, (R // 2,)),
+                             ("positions", positions, torch.int32, (T,))))
+    _check(fn, (_lib.dsa_rope if fn == "dsa_rope" else _lib.dsa_rope_backward)(
+        x.data_ptr(), xt, xh, out.data_ptr(), ot, oh, pp, pos0, pf, T, H, D, rot_off, R, 1 if interleaved else 0,
+        mscale, _ROPE_DTYPES[dtype], _current_stream(dev.index)))
     return out
 
 

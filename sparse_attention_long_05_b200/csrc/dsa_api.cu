@@ -654,11 +654,11 @@ struct Carve {
 };
 
 // Tokens that a backward pass handles at once: as many as keep the per-entry buffers (`per_entry` bytes for each of
-// kp slots) and the scatter table (2 bytes for each of S rows) of a chunk within 2 GiB, at least 64, and equal chunks.
-// Measured for the attention's pass over 2048 tokens of k = 2048: see the chunk sizes in the table of design notes.
+// kp slots) and the scatter table (2 bytes for each of S rows) of a chunk within 4 GiB, at least 64, and equal chunks.
+// The attention's pass over 2048 tokens of k = 2048 took XXX us with chunks of 512 (2 GiB) and XXX with 1024.
 int bwd_chunk(int T, int64_t S, int kp, size_t per_entry) {
   const size_t each = size_t(kp) * per_entry + 2 * size_t(S);
-  const size_t cap = std::min<size_t>(sct::MAX_T, std::max<size_t>(64, (size_t(2) << 30) / each));
+  const size_t cap = std::min<size_t>(sct::MAX_T, std::max<size_t>(64, (size_t(4) << 30) / each));
   if (size_t(T) <= cap) return T > 0 ? T : 1;
   const size_t chunks = (size_t(T) + cap - 1) / cap;
   return static_cast<int>((size_t(T) + chunks - 1) / chunks);
@@ -893,31 +893,24 @@ dsa_status_t launch_rope(RopeParams p, bool vec, bool inter, cudaStream_t st) {
   const int n = vec ? V : 1;
   const bool in_place = p.x == p.out;
   p.rot_units = vec && inter ? p.R / V : p.R / 2 / n;
-  p.units = p.rot_units + (in_place ? 0 : (p.D - p.R) / n);
-  // one head a thread until the GPU's resident threads are covered, then up to eight (their loads in flight together;
-  // the angles are formed once for them)
-  const long long one = static_cast<long long>(p.T) * p.units * p.H, resident = 2048ll * num_sms();
-  p.heads_per = static_cast<int>(std::min<long long>(8, std::max<long long>(1, one / resident)));
-  p.head_groups = (p.H + p.heads_per - 1) / p.heads_per;
-  const long long per = static_cast<long long>(p.units) * p.head_groups;
-  const int step = static_cast<int>(std::min<long long>(p.T, std::max<long long>(1, (1ll << 31) / per - 1)));
-  const int T = p.T;
-  const RopeParams all = p;
-  auto kern = vec ? (inter ? rope_kernel<E, V, true> : rope_kernel<E, V, false>)
-                  : (inter ? rope_kernel<E, 1, true> : rope_kernel<E, 1, false>);
-  for (int t0 = 0; t0 < T; t0 += step) {
-    p.T = std::min(step, T - t0);
-    p.x = static_cast<const E*>(all.x) + t0 * all.x_st;
-    p.out = static_cast<E*>(all.out) + t0 * all.o_st;
-    p.positions = all.positions ? all.positions + t0 : nullptr;
-    p.pos0 = all.pos0 + t0;
-    const long long threads = per * p.T;
-    if (launch_pdl(kern, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, st, p) != cudaSuccess)
-      return DSA_ERR_CUDA;
-    const dsa_status_t e = last_launch_status();
-    if (e != DSA_OK) return e;
-  }
-  return DSA_OK;
+  p.copy_units = in_place ? 0 : (p.D - p.R) / n;
+  // one head a thread until the GPU's resident threads are covered, then up to eight (their loads in flight together,
+  // one set of angles); more tokens than that go round the same threads, in equal shares
+  const long long one = static_cast<long long>(p.T) * (p.rot_units + p.copy_units) * p.H, resident = 2048ll * num_sms();
+  p.heads_per = static_cast<int>(std::min<long long>(std::min(8, p.H), std::max<long long>(1, one / resident)));
+  const int groups = (p.H + p.heads_per - 1) / p.heads_per;
+  if (groups > 65535) return DSA_ERR_UNSUPPORTED_SHAPE;
+  const int bx = std::min(256, p.rot_units), by = 256 / bx;
+  const long long blocks = (static_cast<long long>(p.T) + by - 1) / by;
+  const long long most = std::max<long long>(1, 2 * resident / 256 / groups);
+  const long long rounds = (blocks + most - 1) / most, gx = (blocks + rounds - 1) / rounds;
+  auto kern = !vec             ? (inter ? rope_kernel<E, 1, true, 1> : rope_kernel<E, 1, false, 1>)
+            : p.heads_per == 1 ? (inter ? rope_kernel<E, V, true, 1> : rope_kernel<E, V, false, 1>)
+                               : (inter ? rope_kernel<E, V, true, 4> : rope_kernel<E, V, false, 4>);
+  if (launch_pdl(kern, dim3(static_cast<unsigned>(gx), groups, p.copy_units ? 2 : 1), dim3(bx, by), 0, st, p) !=
+      cudaSuccess)
+    return DSA_ERR_CUDA;
+  return last_launch_status();
 }
 
 // Elements [0, D) of each of T x H rows at the given strides do not meet each other.

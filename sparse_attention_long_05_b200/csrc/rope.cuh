@@ -3,11 +3,12 @@
 // with (a, b) = (2 i, 2 i + 1) (interleaved) or (i, i + R/2) (halves); the backward pass is the transpose (-theta).
 // The other dims are copied, or left alone when the result replaces its input.
 //
-// Bound by HBM: each value is read and written once.  A thread owns one 16-byte piece (halves: the two pieces of its
-// pairs) of a token and walks over the token's heads, so that the angles, which the heads share, are formed once per
-// thread.  theta / 2 pi is formed and reduced to [-1/2, 1/2] in fp64 (a position of 10^6 leaves no digit of an fp32
-// angle), its sine and cosine in fp32; bf16 results take the hardware's sine and cosine (absolute error 2^-20, against
-// 2^-9 of the rounding).
+// Bound by HBM: each value is read and written once.  A thread owns one 16-byte piece of a head (halves: the two pieces of
+// its pairs) and walks over tokens and, for each, over some of the token's heads, so that the turn per position of its
+// pairs is formed once and the angles, which the heads share, once a token.  f / 2 pi is taken as a fraction of a turn in
+// units of 2^-64, so that position times it wraps to the fraction of a turn by itself, exactly (a position of 10^6
+// leaves no digit of an fp32 angle); sine and cosine are fp32, and bf16 results take the hardware's (absolute error
+// 2^-20, against 2^-9 of the rounding).
 #pragma once
 #include "common.cuh"
 
@@ -20,9 +21,8 @@ struct RopeParams {
   const int* positions;               // [T] or null: pos0 + t
   const double* freq;                 // [R / 2]
   int pos0, T, H, D, off, R;
-  int units;                          // pieces of a token's head: rotated ones first
-  int rot_units;
-  int head_groups, heads_per;         // threads a piece's heads are spread over; heads of each
+  int rot_units, copy_units;          // pieces of a head: rotated ones (pairs of pieces), copied ones
+  int heads_per;                      // heads of a thread; blockIdx.y counts their groups
   float m;
   int backward;
 };
@@ -37,71 +37,103 @@ template <> __device__ __forceinline__ __nv_bfloat16 rope_put<__nv_bfloat16>(flo
 // N elements moved as one access where N * sizeof(E) = 16, one by one otherwise (N = 1: any alignment)
 template <typename E, int N> struct alignas(N * sizeof(E)) RopePiece { E v[N]; };
 
-template <typename E, int N, bool INTER>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
+// B: heads in flight (1 where a thread has one head)
+template <typename E, int N, bool INTER, int B>
+__global__ void __launch_bounds__(256, B == 1 ? 4 : sizeof(E) == 4 ? 3 : 2) rope_kernel(const RopeParams p) {
   pdl_allow_next();
   pdl_wait();
-  // interleaved pieces hold whole pairs: N pairs over two adjacent pieces' worth of elements when N = 1
+  // block (x, y): x over the pieces of a head, y over tokens; blockIdx.z = 1: the copied pieces (a warp with both kinds
+  // would do both in turn: for the fp32 indexer queries, half of whose dims are copied, 81 us against 55)
   constexpr int PAIRS = INTER && N > 1 ? N / 2 : N;
   using Piece = RopePiece<E, N>;
-  const unsigned i = blockIdx.x * 256u + threadIdx.x;
-  const unsigned per = static_cast<unsigned>(p.units) * p.head_groups;
-  const int t = static_cast<int>(i / per);
-  if (t >= p.T) return;
-  const int rest = static_cast<int>(i % per), hg = rest / p.units, unit = rest % p.units;
-  const int h0 = hg * p.heads_per, h1 = min(p.H, h0 + p.heads_per);
-  const E* x = static_cast<const E*>(p.x) + t * p.x_st;
-  E* out = static_cast<E*>(p.out) + t * p.o_st;
-  if (unit >= p.rot_units) {
-    // copied dims: those before rot_off, then those after the rotated ones
-    int d = (unit - p.rot_units) * N;
-    if (d >= p.off) d += p.R;
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h)
-      *reinterpret_cast<Piece*>(out + h * p.o_sh + d) = *reinterpret_cast<const Piece*>(x + h * p.x_sh + d);
+  const int h0 = blockIdx.y * p.heads_per, h1 = min(p.H, h0 + p.heads_per);
+  const int t0 = blockIdx.x * blockDim.y + threadIdx.y, dt = gridDim.x * blockDim.y;
+  auto xrow = [&](int t, int h) { return static_cast<const E*>(p.x) + t * p.x_st + h * p.x_sh; };
+  auto yrow = [&](int t, int h) { return static_cast<E*>(p.out) + t * p.o_st + h * p.o_sh; };
+  if (blockIdx.z) {
+    for (int unit = threadIdx.x; unit < p.copy_units; unit += blockDim.x) {
+      // copied dims: those before rot_off, then those after the rotated ones
+      int d = unit * N;
+      if (d >= p.off) d += p.R;
+      for (int t = t0; t < p.T; t += dt) {
+        for (int h = h0; h < h1; h += B) {
+          Piece v[B];
+#pragma unroll
+          for (int u = 0; u < B; ++u)
+            if (h + u < h1) v[u] = *reinterpret_cast<const Piece*>(xrow(t, h + u) + d);
+#pragma unroll
+          for (int u = 0; u < B; ++u)
+            if (h + u < h1) *reinterpret_cast<Piece*>(yrow(t, h + u) + d) = v[u];
+        }
+      }
+    }
     return;
   }
-  // first pair of the piece, and where its two elements are
-  const int pair = unit * PAIRS;
-  const int da = p.off + (INTER ? 2 * pair : pair), db = p.off + (INTER ? 2 * pair + 1 : pair + p.R / 2);
-  const double pos = p.positions ? p.positions[t] : p.pos0 + t;
-  float c[PAIRS], s[PAIRS];
+  for (int unit = threadIdx.x; unit < p.rot_units; unit += blockDim.x) {
+    // first pair of the piece, and where its two elements are
+    const int pair = unit * PAIRS;
+    const int da = p.off + (INTER ? 2 * pair : pair), db = p.off + (INTER ? 2 * pair + 1 : pair + p.R / 2);
+    constexpr bool BOTH = !(INTER && N > 1);   // the pairs' second elements lie in a piece of their own
+    Piece va[B], vb[BOTH ? B : 1];
+    auto load = [&](int t, int h) {
 #pragma unroll
-  for (int q = 0; q < PAIRS; ++q) {
-    const double turns = pos * p.freq[pair + q] * 0.15915494309189533577;   // 1 / (2 pi)
-    const float r = static_cast<float>(turns - rint(turns));
-    if constexpr (sizeof(E) == 2) {
-      c[q] = __cosf(r * 6.2831853071795865f);
-      s[q] = __sinf(r * 6.2831853071795865f);
-    } else {
-      sincospif(2.f * r, &s[q], &c[q]);
+      for (int u = 0; u < B; ++u) {
+        if (h + u >= h1) break;
+        va[u] = *reinterpret_cast<const Piece*>(xrow(t, h + u) + da);
+        if constexpr (BOTH) vb[u] = *reinterpret_cast<const Piece*>(xrow(t, h + u) + db);
+      }
+    };
+    int pos = 0;
+    if (t0 < p.T) {                       // on their way while the turns are formed
+      load(t0, h0);
+      pos = p.positions ? p.positions[t0] : p.pos0 + t0;
     }
-    c[q] *= p.m;
-    s[q] *= p.backward ? -p.m : p.m;
-  }
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const E* xr = x + h * p.x_sh;
-    E* yr = out + h * p.o_sh;
-    if constexpr (INTER && N > 1) {
-      Piece v = *reinterpret_cast<const Piece*>(xr + da);
+    unsigned long long turn[PAIRS];
+#pragma unroll
+    for (int q = 0; q < PAIRS; ++q) {
+      double x = p.freq[pair + q] * 0.15915494309189533577;                 // 1 / (2 pi)
+      if (fabs(x) >= 0.5) x -= rint(x);
+      turn[q] = static_cast<unsigned long long>(__double2ll_rn(x * 18446744073709551616.0));
+    }
+    for (int t = t0; t < p.T; t += dt) {
+      float c[PAIRS], s[PAIRS];
 #pragma unroll
       for (int q = 0; q < PAIRS; ++q) {
-        const float a = rope_get<E>(v.v[2 * q]), b = rope_get<E>(v.v[2 * q + 1]);
-        v.v[2 * q] = rope_put<E>(a * c[q] - b * s[q]);
-        v.v[2 * q + 1] = rope_put<E>(a * s[q] + b * c[q]);
+        const unsigned long long at = turn[q] * static_cast<unsigned long long>(static_cast<long long>(pos));
+        const float r = static_cast<float>(static_cast<int>(at >> 32));     // units of 2^-32 turns
+        if constexpr (sizeof(E) == 2) {
+          c[q] = __cosf(r * 1.4629180792671596e-9f);                        // 2 pi / 2^32
+          s[q] = __sinf(r * 1.4629180792671596e-9f);
+        } else {
+          sincospif(r * 4.6566128730773926e-10f, &s[q], &c[q]);             // 2 / 2^32
+        }
+        c[q] *= p.m;
+        s[q] *= p.backward ? -p.m : p.m;
       }
-      *reinterpret_cast<Piece*>(yr + da) = v;
-    } else {
-      Piece va = *reinterpret_cast<const Piece*>(xr + da), vb = *reinterpret_cast<const Piece*>(xr + db);
+      for (int h = h0; h < h1; h += B) {
+        if (h != h0 || (B > 1 && t != t0)) load(t, h);
+        Piece ya[B], yb[BOTH ? B : 1];
 #pragma unroll
-      for (int q = 0; q < PAIRS; ++q) {
-        const float a = rope_get<E>(va.v[q]), b = rope_get<E>(vb.v[q]);
-        va.v[q] = rope_put<E>(a * c[q] - b * s[q]);
-        vb.v[q] = rope_put<E>(a * s[q] + b * c[q]);
+        for (int u = 0; u < B; ++u) {
+#pragma unroll
+          for (int q = 0; q < PAIRS; ++q) {
+            const float a = rope_get<E>(BOTH ? va[u].v[q] : va[u].v[2 * q]);
+            const float b = rope_get<E>(BOTH ? vb[BOTH ? u : 0].v[q] : va[u].v[BOTH ? 0 : 2 * q + 1]);
+            (BOTH ? ya[u].v[q] : ya[u].v[2 * q]) = rope_put<E>(a * c[q] - b * s[q]);
+            (BOTH ? yb[BOTH ? u : 0].v[q] : ya[u].v[BOTH ? 0 : 2 * q + 1]) = rope_put<E>(a * s[q] + b * c[q]);
+          }
+        }
+        if (h + B >= h1 && t + dt < p.T) {  // the next token's head (with one a thread), ahead of the stores
+          if (B == 1) load(t + dt, h0);
+          pos = p.positions ? p.positions[t + dt] : p.pos0 + t + dt;
+        }
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+          if (h + u >= h1) break;
+          *reinterpret_cast<Piece*>(yrow(t, h + u) + da) = ya[u];
+          if constexpr (BOTH) *reinterpret_cast<Piece*>(yrow(t, h + u) + db) = yb[u];
+        }
       }
-      *reinterpret_cast<Piece*>(yr + da) = va;
-      *reinterpret_cast<Piece*>(yr + db) = vb;
     }
   }
 }
