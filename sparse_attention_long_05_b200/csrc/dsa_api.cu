@@ -683,14 +683,13 @@ ScatterWs carve_scatter(Carve& w, int Tc, int64_t S, int kp, int width, bool man
   return s;
 }
 
-dsa_status_t scatter_begin(const ScatterWs& w, const int* idx, int T, int64_t S, int k, cudaStream_t st) {
-  const long long n = static_cast<long long>(S) * w.ld / 8;
-  const int grid = static_cast<int>(std::min<long long>((n + 255) / 256, 8ll * num_sms()));
-  if (launch_pdl(scatter_clear_kernel, dim3(grid), dim3(256), 0, st, reinterpret_cast<uint4*>(w.table), n) !=
-      cudaSuccess)
-    return DSA_ERR_CUDA;
-  dsa_status_t e = last_launch_status();
-  if (e != DSA_OK) return e;
+// 16-byte pieces of the table, and the blocks that clear them
+long long table_pieces(const ScatterWs& w, int64_t S) { return static_cast<long long>(S) * w.ld / 8; }
+long long table_blocks(const ScatterWs& w, int64_t S) {
+  return std::min<long long>((table_pieces(w, S) + 255) / 256, 8ll * num_sms());
+}
+
+dsa_status_t scatter_build(const ScatterWs& w, const int* idx, int T, int64_t S, int k, cudaStream_t st) {
   if (launch_pdl(scatter_build_kernel, dim3(T), dim3(256), 0, st, idx, k, static_cast<long long>(S), w.n_end,
                  w.table, w.ld) != cudaSuccess)
     return DSA_ERR_CUDA;
@@ -778,13 +777,14 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
     p.S = S;
     p.scale = scale;
     p.scale_log2 = scale * 1.4426950408889634f;
-    dsa_status_t e = scatter_begin(w.sc, p.idx, n, S, k, st);
-    if (e != DSA_OK) return e;
     const long long dr = static_cast<long long>(n) * H;
-    if (launch_pdl(mla_bwd_delta_kernel, dim3(static_cast<unsigned>((dr + 7) / 8)), dim3(256), 0, st,
-                   dout + o * H * mbw::DV, out + o * H * mbw::DV, dr, w.delta) != cudaSuccess)
+    if (launch_pdl(mla_bwd_begin_kernel, dim3(static_cast<unsigned>(std::max((dr + 7) / 8, table_blocks(w.sc, S)))),
+                   dim3(256), 0, st, dout + o * H * mbw::DV, out + o * H * mbw::DV, dr, w.delta,
+                   reinterpret_cast<uint4*>(w.sc.table), table_pieces(w.sc, S)) != cudaSuccess)
       return DSA_ERR_CUDA;
-    if ((e = last_launch_status()) != DSA_OK) return e;
+    dsa_status_t e = last_launch_status();
+    if (e != DSA_OK) return e;
+    if ((e = scatter_build(w.sc, p.idx, n, S, k, st)) != DSA_OK) return e;
     if (launch_pdl(mla_bwd_p_kernel<false>, dim3(2 * std::min(sms / 2, n)), dim3(mbw::p::THREADS),
                    mbw::p::Map<false>::SMEM, st, tq, tdo, tc, p) != cudaSuccess)
       return DSA_ERR_CUDA;
@@ -874,8 +874,12 @@ dsa_status_t run_index_bwd(IndexerBwdParams p, int T, uint16_t* dk, const IndexB
     p.dsel = all.dsel + o * p.k;
     p.dq = all.dq + o * HI * DI;
     p.dw = all.dw + o * HI;
-    dsa_status_t e = scatter_begin(w.sc, p.idx, p.T, p.S, p.k, st);
+    if (launch_pdl(scatter_clear_kernel, dim3(static_cast<unsigned>(table_blocks(w.sc, p.S))), dim3(256), 0, st,
+                   reinterpret_cast<uint4*>(w.sc.table), table_pieces(w.sc, p.S)) != cudaSuccess)
+      return DSA_ERR_CUDA;
+    dsa_status_t e = last_launch_status();
     if (e != DSA_OK) return e;
+    if ((e = scatter_build(w.sc, p.idx, p.T, p.S, p.k, st)) != DSA_OK) return e;
     if (launch_pdl(indexer_bwd_kernel<HI, DI>, dim3(std::min(num_sms(), p.T)), dim3(ixb::THREADS), ixb::SMEM, st, tout,
                    p) != cudaSuccess)
       return DSA_ERR_CUDA;

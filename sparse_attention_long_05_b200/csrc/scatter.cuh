@@ -18,12 +18,16 @@ constexpr uint16_t EMPTY = 0xffff;
 constexpr uint16_t TWICE = 0x0800;        // the token selected the row again in later slots
 }  // namespace sct
 
-__global__ void __launch_bounds__(256) scatter_clear_kernel(uint4* table, long long n) {
-  pdl_allow_next();
-  pdl_wait();
+// the whole grid's share of the table
+__device__ __forceinline__ void scatter_clear(uint4* table, long long n) {
   const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
   for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step)
     table[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+}
+__global__ void __launch_bounds__(256) scatter_clear_kernel(uint4* table, long long n) {
+  pdl_allow_next();
+  pdl_wait();
+  scatter_clear(table, n);
 }
 
 // One CTA per token: n_end (slots up to the last valid entry), and with a table its entries.  A row selected more than once by a token is entered with its lowest slot and

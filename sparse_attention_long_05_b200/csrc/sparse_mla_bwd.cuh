@@ -25,6 +25,7 @@
 // relative to the sum of their sizes (half the bf16 step that the results are rounded to anyway).  All sums are fp32.
 #pragma once
 #include "common.cuh"
+#include "scatter.cuh"
 #include "sparse_mla.cuh"
 
 namespace dsa {
@@ -879,29 +880,37 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
   bwd_end(cta);
 }
 
-// delta[t][h] = dout . out over the 512 value dims, one warp a row.
-__global__ void __launch_bounds__(256) mla_bwd_delta_kernel(const uint16_t* dout, const uint16_t* out, long long rows,
-                                                            float* delta) {
+// What the other kernels of a chunk start from: delta[t][h] = dout . out over the 512 value dims (one warp a row, eight rows
+// a block) and the scatter table, cleared in equal shares by all blocks.
+__global__ void __launch_bounds__(256) mla_bwd_begin_kernel(const uint16_t* dout, const uint16_t* out, long long rows,
+                                                            float* delta, uint4* table, long long n) {
   pdl_allow_next();
   pdl_wait();
   const long long r = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (r >= rows) return;
-  const uint4* a = reinterpret_cast<const uint4*>(dout + r * mbw::DV);
-  const uint4* b = reinterpret_cast<const uint4*>(out + r * mbw::DV);
-  float s = 0.f;
+  if (r < rows) {
+    const uint4* a = reinterpret_cast<const uint4*>(dout + r * mbw::DV);
+    const uint4* b = reinterpret_cast<const uint4*>(out + r * mbw::DV);
+    uint4 x[2], y[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 x = a[lane_id() + 32 * i], y = b[lane_id() + 32 * i];
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      s = fmaf(__uint_as_float(xs[u] << 16), __uint_as_float(ys[u] << 16), s);
-      s = fmaf(__uint_as_float(xs[u] & 0xffff0000u), __uint_as_float(ys[u] & 0xffff0000u), s);
+    for (int i = 0; i < 2; ++i) {
+      x[i] = __ldcs(a + lane_id() + 32 * i);
+      y[i] = __ldcs(b + lane_id() + 32 * i);
     }
-  }
+    float s = 0.f;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  if (lane_id() == 0) delta[r] = s;
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, ys[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        s = fmaf(__uint_as_float(xs[u] << 16), __uint_as_float(ys[u] << 16), s);
+        s = fmaf(__uint_as_float(xs[u] & 0xffff0000u), __uint_as_float(ys[u] & 0xffff0000u), s);
+      }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (lane_id() == 0) delta[r] = s;
+  }
+  scatter_clear(table, n);
 }
 
 }  // namespace dsa
