@@ -313,6 +313,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
       : DSA_R8(0), DSA_R8(8), DSA_R8(16), DSA_R8(24)
       : "r"(taddr));
 }
+// 32 lanes x 16 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : DSA_R8(0), DSA_R8(8)
+      : "r"(taddr));
+}
 // 16 lanes x 256 bits, 8 repetitions along the columns (64 columns): thread i receives, for repetition m,
 // v[4m], v[4m+1] = lane (i / 4), columns 8m + 2(i % 4) + {0, 1}, and v[4m+2], v[4m+3] = lane (i / 4 + 8), the
 // same columns (lanes counted from the lane field of taddr)

@@ -35,20 +35,21 @@ struct IndexerBwdParams {
 };
 
 namespace ixb {
-constexpr int THREADS = 576, PRODUCERS = 8;      // w0 index rows, w1 MMA, w2 w3 w8..13 keys, w4..7 G, w14..17 results
+// w0 index rows, w1 MMA, w2 w3 w8..13 keys, w4..7 w18..21 G, w14..17 results
+constexpr int THREADS = 704, PRODUCERS = 8;
 constexpr int NK = 128, HP = 64;
 constexpr int KCH = 128 * 128, QCH = 64 * 128;   // 128 keys (64 heads) x 64 dims bf16
 constexpr int K_BYTES = 2 * KCH, Q_BYTES = 2 * QCH, G_BYTES = 128 * 128;
 constexpr int B_IDX_FULL = 0, B_IDX_EMPTY = 2, B_Q_FULL = 4, B_Q_EMPTY = 6, B_K_FULL = 8, B_K_EMPTY = 10;
 constexpr int B_X_FULL = 12, B_X_EMPTY = 14, B_G_FULL = 16, B_G_EMPTY = 18, B_DK_FULL = 20, B_DK_EMPTY = 22;
 constexpr int B_DQ_FULL = 24, B_DQ_EMPTY = 26;
-constexpr int OFF_W = 1024, OFF_DW = OFF_W + 512;            // w of the token (2 buffers), dw of the four warps
+constexpr int OFF_W = 1024, OFF_DW = OFF_W + 512;            // w of the token (2 buffers), dw of the eight warps
 constexpr int OFF_IDX = 4096, OFF_Q = OFF_IDX + 2 * mla::KMAX * 4, OFF_K = OFF_Q + 2 * Q_BYTES;
 constexpr int OFF_G = OFF_K + 2 * K_BYTES;                   // 2 x (G, G ks)
 constexpr int OFF_OUT = OFF_G + 4 * G_BYTES;
 constexpr int SMEM = OFF_OUT + 2 * KCH + 1024;
 constexpr uint32_t TX = 0, TDK = 128, TDQ = 384;             // x 2 x 64, dk 2 x 128, dq 2 x 64 columns
-static_assert(SMEM <= 232448 && OFF_DW + 1024 <= OFF_IDX, "shared memory");
+static_assert(SMEM <= 232448 && OFF_DW + 2048 <= OFF_IDX, "shared memory");
 }  // namespace ixb
 
 // two e4m3 -> two bf16 (exact)
@@ -244,74 +245,83 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
       __syncwarp();
       step(b);
     }
-  } else if (warp < 8) {
+  } else if (warp < 8 || warp >= 18) {
     // ===================================================================== G, G ks and dw (one key a thread)
+    // Two groups of four warps take tiles in turn (one group alone: 707 us for 2048 tokens, against XXX).  The entry of
+    // a thread's next tile but one, and the gradient and key scale of its next tile, are on their way meanwhile.
+    const int grp = warp >= 18 ? 1 : 0;
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+    constexpr int BLOCKS = (HI + 15) / 16;               // 16 heads at a time
     float* dw_s = reinterpret_cast<float*>(cta.smem + OFF_DW);
     int g = 0;
     for (int t = blockIdx.x; t < p.T && ok; t += gridDim.x) {
       const int tiles = tiles_of(t);
       if (tiles <= 0) {
-        if (row < HI) p.dw[static_cast<long long>(t) * HI + row] = 0.f;
+        if (grp == 0 && row < HI) p.dw[static_cast<long long>(t) * HI + row] = 0.f;
         continue;
       }
       float* ws = reinterpret_cast<float*>(cta.smem + OFF_W) + 64 * (n & 1);
-      if (row < 64) ws[row] = row < HI ? p.w[static_cast<long long>(t) * HI + row] : 0.f;
-      if (!(ok = named_bar_all(1, 128, ok))) break;
-      float dw[2] = {0.f, 0.f};
-      for (int j = 0; j < tiles; ++j, ++g) {
-        const int s = g & 1, slot = j * NK + row;
-        float e = 0.f, ks = 0.f;
-        if (slot < p.k) {
-          const long long at = static_cast<long long>(t) * p.k + slot;
-          const int id = p.idx[at];
-          if (id >= 0 && id < p.S) {
-            e = p.dsel[at];
-            ks = p.k_scale ? p.k_scale[id] : 1.f;
-          }
-        }
-        ok = warp_wait(cta.bar(B_X_FULL + s), (g >> 1) & 1, abort_flag);
-        ok = ok && warp_wait(cta.bar(B_G_EMPTY + s), ((g >> 1) & 1) ^ 1, abort_flag);
+      if (grp == 0 && row < 64) ws[row] = row < HI ? p.w[static_cast<long long>(t) * HI + row] : 0.f;
+      const long long base = static_cast<long long>(t) * p.k;
+      auto entry = [&](int j) {
+        const int slot = j * NK + row;
+        const int id = j < tiles && slot < p.k ? __ldg(p.idx + base + slot) : -1;
+        return id < p.S ? id : -1;
+      };
+      auto grad = [&](int j, int id) { return id >= 0 ? __ldg(p.dsel + base + j * NK + row) : 0.f; };
+      auto scale = [&](int id) { return id < 0 ? 0.f : p.k_scale ? __ldg(p.k_scale + id) : 1.f; };
+      const int j0 = (g ^ grp) & 1;
+      int id = entry(j0), id_next = entry(j0 + 2);
+      float e = grad(j0, id), ks = scale(id);
+      if (!(ok = named_bar_all(1, 256, ok))) break;
+      float dw[BLOCKS] = {};
+      for (int j = j0; j < tiles; j += 2) {
+        const int s = grp;                               // (g + j) % 2
+        const float e_next = grad(j + 2, id_next), ks_next = scale(id_next);
+        id_next = entry(j + 4);
+        ok = warp_wait(cta.bar(B_X_FULL + s), ((g + j) >> 1) & 1, abort_flag);
+        ok = ok && warp_wait(cta.bar(B_G_EMPTY + s), (((g + j) >> 1) & 1) ^ 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         uint8_t* gl = cta.smem + OFF_G + 2 * s * G_BYTES + row * 128;
         const float eks = e * ks;
 #pragma unroll
-        for (int c = 0; c < (HI + 31) / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld32(lane_addr + tmem + TX + 64 * s + 32 * c, v);
+        for (int c = 0; c < BLOCKS; ++c) {
+          uint32_t v[16];
+          tmem_ld16(lane_addr + tmem + TX + 64 * s + 16 * c, v);
           tmem_wait_ld();
-          if (c == (HI + 31) / 32 - 1) {
+          if (c == BLOCKS - 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(cta.bar(B_X_EMPTY + s));
           }
-          float x[32];
+          float x[16];
+          uint32_t a[8], b[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t a[4], b[4];
+          for (int i = 0; i < 16; i += 4) {
+            const float4 w4 = *reinterpret_cast<const float4*>(ws + 16 * c + i);
+            const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
+            float gv[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              float lo[2], hi[2];
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const int h = 8 * i + 2 * q + r;
-                const float xv = __uint_as_float(v[h]);
-                const bool live = xv > 0.f;
-                const float gv = live ? e * ws[32 * c + h] : 0.f;
-                lo[r] = gv;
-                hi[r] = gv * ks;
-                x[h] = live ? eks * xv : 0.f;
-              }
-              a[q] = pack_bf16(lo[0], lo[1]);
-              b[q] = pack_bf16(hi[0], hi[1]);
+              const float xv = __uint_as_float(v[i + q]);
+              const bool live = xv > 0.f;
+              gv[q] = live ? e * wv[q] : 0.f;
+              x[i + q] = live ? eks * xv : 0.f;
             }
-            const int unit = ((4 * c + i) ^ (row & 7)) << 4;
-            *reinterpret_cast<uint4*>(gl + unit) = make_uint4(a[0], a[1], a[2], a[3]);
-            *reinterpret_cast<uint4*>(gl + G_BYTES + unit) = make_uint4(b[0], b[1], b[2], b[3]);
+            a[i / 2] = pack_bf16(gv[0], gv[1]);
+            a[i / 2 + 1] = pack_bf16(gv[2], gv[3]);
+            b[i / 2] = pack_bf16(gv[0] * ks, gv[1] * ks);
+            b[i / 2 + 1] = pack_bf16(gv[2] * ks, gv[3] * ks);
           }
-          // sums over the warp's 32 keys: five halving steps, lane l ends with head 32 c + l
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int unit = ((2 * c + i) ^ (row & 7)) << 4;
+            *reinterpret_cast<uint4*>(gl + unit) = make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+            *reinterpret_cast<uint4*>(gl + G_BYTES + unit) = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
+          }
+          // sums over the warp's 32 keys: four halving steps, then the two half-warps; lane l ends with head 16 c + l % 16
 #define DSA_IXB_HALVE(O)                                                                \
   {                                                                                     \
     const bool up = (lane & (O)) != 0;                                                  \
@@ -321,25 +331,30 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
       x[i] = keep + __shfl_xor_sync(0xffffffffu, send, (O));                            \
     }                                                                                   \
   }
-          DSA_IXB_HALVE(16)
           DSA_IXB_HALVE(8)
           DSA_IXB_HALVE(4)
           DSA_IXB_HALVE(2)
           DSA_IXB_HALVE(1)
 #undef DSA_IXB_HALVE
-          dw[c] += x[0];
+          dw[c] += x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(cta.bar(B_G_FULL + s));
+        e = e_next;
+        ks = ks_next;
       }
-      dw_s[quad * 64 + lane] = dw[0];
-      dw_s[quad * 64 + 32 + lane] = dw[1];
-      if (!(ok = named_bar_all(1, 128, ok))) break;
-      if (row < HI) {
-        const float qs = p.q_scale ? p.q_scale[t] : 1.f;
-        p.dw[static_cast<long long>(t) * HI + row] =
-            ((dw_s[row] + dw_s[64 + row]) + (dw_s[128 + row] + dw_s[192 + row])) * qs;
+      g += tiles;
+      if (lane < 16) {
+#pragma unroll
+        for (int c = 0; c < BLOCKS; ++c) dw_s[(4 * grp + quad) * 64 + 16 * c + lane] = dw[c];
+      }
+      if (!(ok = named_bar_all(1, 256, ok))) break;
+      if (grp == 0 && row < HI) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) sum += dw_s[64 * w + row];
+        p.dw[static_cast<long long>(t) * HI + row] = sum * (p.q_scale ? p.q_scale[t] : 1.f);
       }
       // the next token's first barrier comes before anyone writes dw_s again
       ++n;
