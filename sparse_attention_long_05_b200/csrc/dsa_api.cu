@@ -785,11 +785,14 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
     dsa_status_t e = last_launch_status();
     if (e != DSA_OK) return e;
     if ((e = scatter_build(w.sc, p.idx, n, S, k, st)) != DSA_OK) return e;
-    if (launch_pdl(mla_bwd_p_kernel<false>, dim3(2 * std::min(sms / 2, n)), dim3(mbw::p::THREADS),
+    // few tokens: their tiles are dealt to as many CTAs as there are (with at least a tile of 256 keys each)
+    p.splits = n >= sms / 2 ? 1 : std::min((sms / 2) / n, (k + 255) / 256);
+    const int items = n * p.splits;
+    if (launch_pdl(mla_bwd_p_kernel<false>, dim3(2 * std::min(sms / 2, items)), dim3(mbw::p::THREADS),
                    mbw::p::Map<false>::SMEM, st, tq, tdo, tc, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
-    if (launch_pdl(mla_bwd_dc_kernel, dim3(std::min(sms, 3 * n)), dim3(mbw::dc::THREADS), mbw::dc::SMEM, st, tp128,
+    if (launch_pdl(mla_bwd_dc_kernel, dim3(std::min(sms, 3 * items)), dim3(mbw::dc::THREADS), mbw::dc::SMEM, st, tp128,
                    tq, tdo, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;

@@ -46,10 +46,15 @@ __global__ void __launch_bounds__(256) scatter_build_kernel(const int* idx, int 
   constexpr int PER = sct::MAX_K / 256;
   int e[PER];
   int my_last = 0;
+  bool rising = true;                    // ascending entries, then empty slots: no row repeats
 #pragma unroll
   for (int u = 0; u < PER; ++u) {
     const int i = u * 256 + threadIdx.x;
     e[u] = i < k ? row[i] : -1;
+    if (i + 1 < k) {
+      const int next = row[i + 1];
+      rising &= !valid(next) || (valid(e[u]) && next > e[u]);
+    }
     if (valid(e[u])) {
       my_last = i + 1;
       if (table) *cell(e[u]) = static_cast<uint16_t>(i);
@@ -60,9 +65,9 @@ __global__ void __launch_bounds__(256) scatter_build_kernel(const int* idx, int 
   }
   my_last = __reduce_max_sync(0xffffffffu, my_last);
   if (lane_id() == 0) atomicMax(&last, my_last);
-  __syncthreads();
+  rising = __syncthreads_and(rising);
   if (threadIdx.x == 0) n_end[t] = last;
-  if (!table) return;
+  if (!table || rising) return;
   // the lowest slot wins: repeated until no slot is below the one entered (one round where no row repeats)
   bool again = false;
   while (true) {

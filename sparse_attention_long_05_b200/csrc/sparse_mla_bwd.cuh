@@ -40,6 +40,7 @@ struct MlaBwdParams {
   uint16_t* contrib;           // [T * kp, 576] bf16: each entry's contribution to dc
   uint16_t* dq;                // [T, H, 576]
   int T, t0;                   // tokens of the chunk; the first one's index in q and dout
+  int splits;                  // a token's tiles are dealt to this many items (P and dS, contributions)
   int H, HP;                   // heads; heads rounded up to 64
   int k, kp;                   // slots of a token; rounded up to 128
   long long S;
@@ -125,8 +126,17 @@ __device__ __forceinline__ void store_rows(uint8_t* buf, const uint32_t (&v)[4 *
   char* to = static_cast<char*>(dst) + sub * stride + 16 * unit;
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    *reinterpret_cast<uint4*>(to + (32 / N) * i * stride) = *at((32 / N) * i + sub, unit);
+    __stwt(reinterpret_cast<uint4*>(to + (32 / N) * i * stride), *at((32 / N) * i + sub, unit));
   __syncwarp();
+}
+
+// Tiles [j0, j1) of a token with n_end slots that split `sp` of `splits` works on (`keys` a tile).
+struct TileSpan {
+  int j0, j1;
+};
+__device__ __forceinline__ TileSpan tile_span(int n_end, int keys, int sp, int splits) {
+  const int tiles = (n_end + keys - 1) / keys, per = (tiles + splits - 1) / splits;
+  return {min(tiles, sp * per), min(tiles, (sp + 1) * per)};
 }
 
 namespace mbw {
@@ -302,15 +312,19 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const uint32_t res = sbase + OFF_RES, ring = sbase + M::OFF_RING;
   const uint32_t lead = map_cluster(sbase, 0);     // CTA 0's barriers, where every load of the pair completes
   const int first = static_cast<int>(blockIdx.x >> 1), stride = static_cast<int>(gridDim.x >> 1);
-  auto tiles_of = [&](int t) { return (p.n_end[t] + 2 * NK - 1) / (2 * NK); };
+  const int splits = KL ? 1 : p.splits, items = p.T * splits;
+  auto token = [&](int item) { return splits == 1 ? item : item / splits; };
+  auto span = [&](int item) { return tile_span(p.n_end[token(item)], 2 * NK, splits == 1 ? 0 : item % splits, splits); };
   bool ok = true;
-  int n = 0;                              // tokens with entries, walked so far
+  int n = 0;                              // items with tiles, walked so far
 
   if (warp == 0) {
     // ===================================================================== resident rows of q (and dout)
     if (lane == 0) {
-      for (int t = first; t < p.T && ok; t += stride) {
-        if (p.n_end[t] <= 0) continue;
+      for (int item = first; item < items && ok; item += stride) {
+        const TileSpan sp = span(item);
+        if (sp.j0 >= sp.j1) continue;
+        const int t = token(item);
         for (int c = 0; c < DCH; ++c) {
           if (!(ok = mbar_wait(cta.bar(B_RES_EMPTY + c), (n & 1) ^ 1, abort_flag))) break;
           const uint32_t dst = res + c * M::RES_CHUNK, full = lead + 8 * (B_RES_FULL + c);
@@ -336,22 +350,22 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int grp = gw / M::WPS, gi = (gw % M::WPS) * PER + lane, cc = gi / 32, rg = gi % 32;
     const bool active = lane < PER;
     int m = 0;                             // stages of the tiles before this one
-    for (int t = first; t < p.T && ok; t += stride) {
-      const int tiles = tiles_of(t);
-      if (tiles <= 0) continue;
-      const int* ids = p.idx + static_cast<long long>(t) * p.k;
+    for (int item = first; item < items && ok; item += stride) {
+      const TileSpan sp = span(item);
+      if (sp.j0 >= sp.j1) continue;
+      const int* ids = p.idx + static_cast<long long>(token(item)) * p.k;
       auto entries = [&](int j) {          // k is a multiple of 64, a lane's four slots lie on one side of it
         const int slot = (2 * j + rank) * NK + 4 * rg;
         return slot < p.k ? __ldg(reinterpret_cast<const int4*>(ids + slot)) : make_int4(-1, -1, -1, -1);
       };
-      int4 e = entries(0);
-      for (int j = 0; j < tiles && ok; ++j, m += SPT) {
+      int4 e = entries(sp.j0);
+      for (int j = sp.j0; j < sp.j1 && ok; ++j, m += SPT) {
         const int slot = (2 * j + rank) * NK + 4 * rg;
         auto row = [&](int x, int i) {
           return (x >= 0 && x < p.S) ? x : static_cast<int>(slot + i < p.S ? slot + i : 0);
         };
         const int r0 = row(e.x, 0), r1 = row(e.y, 1), r2 = row(e.z, 2), r3 = row(e.w, 3);
-        if (j + 1 < tiles) e = entries(j + 1);
+        if (j + 1 < sp.j1) e = entries(j + 1);
         for (int s = (grp + (GROUPS - 1) * m) % GROUPS; s < SPT; s += GROUPS) {   // (m + s) % GROUPS == grp
           const int st = (m + s) % NS;
           const uint32_t full = lead + 8 * (B_RING_FULL + st);
@@ -372,15 +386,15 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       Pipe<NS> rp;
       int g = 0;
       const uint32_t wide = idesc_bf16(256, KL ? p.HP : 2 * p.HP, false), narrow = idesc_bf16(256, p.HP, false);
-      for (int t = first; t < p.T && ok; t += stride) {
-        const int tiles = tiles_of(t);
-        if (tiles <= 0) continue;
-        for (int j = 0; j < tiles && ok; ++j, ++g) {
+      for (int item = first; item < items && ok; item += stride) {
+        const TileSpan sp = span(item);
+        if (sp.j0 >= sp.j1) continue;
+        for (int j = sp.j0; j < sp.j1 && ok; ++j, ++g) {
           const int ab = g % NACC;
           if (!(ok = warp_wait<true>(cta.bar(B_ACC_EMPTY + ab), ((g / NACC) & 1) ^ 1, abort_flag))) break;
           tc_fence_after();
           for (int sg = 0; sg < SPT; ++sg, rp.advance()) {
-            if (j == 0)
+            if (j == sp.j0)
               for (int c = sg * SC; c < (sg + 1) * SC && ok; ++c)
                 ok = warp_wait<true>(cta.bar(B_RES_FULL + c), n & 1, abort_flag);
             if (!(ok = ok && warp_wait<true>(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
@@ -395,7 +409,7 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int k = 0; k < 4; ++k)
                   mma2_bf16_ss(tmem + (512 / NACC) * ab, ad + 2 * k, bd + 2 * k, c < 8 ? wide : narrow,
                                (c | k) ? 1u : 0u);
-                if (j == tiles - 1) mma2_commit(cta.bar(B_RES_EMPTY + c));
+                if (j == sp.j1 - 1) mma2_commit(cta.bar(B_RES_EMPTY + c));
               }
               mma2_commit(cta.bar(B_RING_EMPTY + rp.stage));
             }
@@ -417,13 +431,14 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     constexpr float kLog2e = 1.4426950408889634f;
     int g = 0;
-    for (int t = first; t < p.T && ok; t += stride) {
-      const int tiles = tiles_of(t);
+    for (int item = first; item < items && ok; item += stride) {
+      const TileSpan sp = span(item);
+      const int t = token(item);
       const long long base = static_cast<long long>(t) * p.k;
       if constexpr (KL) {
-        for (int i = (2 * (tiles + grp) + rank) * NK + row; i < p.k; i += 4 * NK) p.dsel[base + i] = 0.f;
+        for (int i = (2 * (sp.j1 + grp) + rank) * NK + row; i < p.k; i += 4 * NK) p.dsel[base + i] = 0.f;
       }
-      if (tiles <= 0) continue;
+      if (sp.j0 >= sp.j1) continue;
       // the token's -lse (in log2 units) and -scale delta.  A head without any probability mass (lse = -inf) and the heads
       // that only fill up the tile get -inf: P = 0.
       float* hs = reinterpret_cast<float*>(cta.smem + OFF_HEADS) + (n & 1) * 256;
@@ -444,18 +459,19 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int slot = (2 * j + rank) * NK + row;
         return KL && slot < p.k ? __ldg(p.sel + base + slot) : 0.f;
       };
-      const int j0 = (g ^ grp) & 1;          // this group's first tile: (g + j) % 2 == grp
-      int e_next = j0 < tiles ? entry(j0) : -1;
-      [[maybe_unused]] float x_next = j0 < tiles ? score(j0) : 0.f;
-      for (int j = j0; j < tiles; j += 2) {
-        const int ab = (g + j) % NACC, slot = (2 * j + rank) * NK + row;
+      // tile j is the CTA's tile g + j - j0; this group takes those of its parity
+      const int j0 = sp.j0 + ((g ^ grp) & 1);
+      int e_next = j0 < sp.j1 ? entry(j0) : -1;
+      [[maybe_unused]] float x_next = j0 < sp.j1 ? score(j0) : 0.f;
+      for (int j = j0; j < sp.j1; j += 2) {
+        const int gj = g + j - sp.j0, ab = gj % NACC, slot = (2 * j + rank) * NK + row;
         const bool valid = e_next >= 0 && e_next < p.S;
         [[maybe_unused]] const float x = x_next;
-        if (j + 2 < tiles) {
+        if (j + 2 < sp.j1) {
           e_next = entry(j + 2);
           x_next = score(j + 2);
         }
-        if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), ((g + j) / NACC) & 1, abort_flag))) break;
+        if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), (gj / NACC) & 1, abort_flag))) break;
         tc_fence_after();
         const uint32_t acc = lane_addr + tmem + (512 / NACC) * ab;
         auto release = [&]() {
@@ -528,7 +544,7 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
         }
       }
-      g += tiles;
+      g += sp.j1 - sp.j0;
       if (!(ok = named_bar_all(1, 256, ok))) break;
       if constexpr (KL) {
         // the token's sums over the pair's 512 threads, then g (softmax(I) - p) for each slot
@@ -581,7 +597,7 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         const float up = p.dkl ? p.dkl[t] : 1.f;
         const float iz = z_all > 0.f ? 1.f / z_all : 0.f, ia = a_all > 0.f ? 1.f / a_all : 0.f;
-        for (int i = (2 * grp + rank) * NK + row; i < min(tiles * 2 * NK, p.k); i += 4 * NK) {
+        for (int i = (2 * grp + rank) * NK + row; i < min(sp.j1 * 2 * NK, p.k); i += 4 * NK) {
           const int e = __ldg(p.idx + base + i);
           const float x = p.sel[base + i];
           const float soft = x > -INFINITY ? ex2_approx((x - m_all) * kLog2e) * iz : 0.f;
@@ -614,7 +630,13 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
   const uint32_t tmem = cta.tmem;
   const uint32_t res = sbase + OFF_RES, ring = sbase + OFF_RING;
   const int hb = p.HP / 64, units = 2 * hb;        // 64-head blocks of dS, then of P
-  const int items = 3 * p.T;
+  const int items = 3 * p.T * p.splits;
+  auto part = [&](int item, int& t, int& d3) {         // item: (token, split, 192 dims)
+    d3 = item % 3;
+    const int ts = item / 3;
+    t = p.splits == 1 ? ts : ts / p.splits;
+    return tile_span(p.n_end[t], NK, p.splits == 1 ? 0 : ts % p.splits, p.splits);
+  };
   bool ok = true;
   int n = 0;
 
@@ -622,8 +644,9 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
     // ===================================================================== resident q and dout
     if (lane == 0) {
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        const int t = item / 3, d3 = item % 3;
-        if (p.n_end[t] <= 0) continue;
+        int t, d3;
+        const TileSpan sp = part(item, t, d3);
+        if (sp.j0 >= sp.j1) continue;
         for (int u = 0; u < units; ++u) {
           if (!(ok = mbar_wait(cta.bar(B_RES_EMPTY + u), (n & 1) ^ 1, abort_flag))) break;
           const int boxes = (u >= hb && d3 == 2) ? 2 : 3;          // dout ends at dim 512
@@ -644,8 +667,9 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
       Pipe<NS> rp;
       int issued = 0;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        const int t = item / 3, tiles = (p.n_end[t] + NK - 1) / NK;
-        for (int j = 0; j < tiles && ok; ++j)
+        int t, d3;
+        const TileSpan sp = part(item, t, d3);
+        for (int j = sp.j0; j < sp.j1 && ok; ++j)
           for (int u = 0; u < 2; ++u, rp.advance(), ++issued) {        // dS, then P
             if (!(ok = mbar_wait(cta.bar(B_RING_EMPTY + rp.stage), rp.phase ^ 1, abort_flag))) break;
             const uint32_t full = cta.bar(B_RING_FULL + rp.stage);
@@ -663,14 +687,15 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
     Pipe<NS> rp;
     int g = 0;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const int t = item / 3, d3 = item % 3, tiles = (p.n_end[t] + NK - 1) / NK;
-      if (tiles <= 0) continue;
-      for (int j = 0; j < tiles && ok; ++j, ++g) {
+      int t, d3;
+      const TileSpan sp = part(item, t, d3);
+      if (sp.j0 >= sp.j1) continue;
+      for (int j = sp.j0; j < sp.j1 && ok; ++j, ++g) {
         const int ab = g & 1;
         if (!(ok = warp_wait(cta.bar(B_ACC_EMPTY + ab), ((g >> 1) & 1) ^ 1, abort_flag))) break;
         tc_fence_after();
         for (int half = 0; half < 2; ++half, rp.advance()) {   // dS . q, then P . dout
-          if (j == 0)
+          if (j == sp.j0)
             for (int i = 0; i < hb && ok; ++i) ok = warp_wait(cta.bar(B_RES_FULL + half * hb + i), n & 1, abort_flag);
           if (!(ok = ok && warp_wait(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
           tc_fence_after();
@@ -684,7 +709,7 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
               for (int k = 0; k < 4; ++k)
                 mma_bf16_ss(tmem + 256 * ab, ad + ((i * CHUNK) >> 4) + 2 * k, bd + ((i * UNIT + k * 2048) >> 4), idesc,
                             (half | i | k) ? 1u : 0u);
-              if (j == tiles - 1) mma_commit(cta.bar(B_RES_EMPTY + half * hb + i));
+              if (j == sp.j1 - 1) mma_commit(cta.bar(B_RES_EMPTY + half * hb + i));
             }
             mma_commit(cta.bar(B_RING_EMPTY + rp.stage));
           }
@@ -700,14 +725,15 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
     // ===================================================================== contributions out (one key a thread)
     // two groups of four warps take tiles in turn, each with an accumulator of its own
     const int grp = (warp - 4) >> 2;
-    const int quad = warp & 3, row = quad * 32 + lane;
+    const int quad = warp & 3;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     int g = 0;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const int t = item / 3, d3 = item % 3, tiles = (p.n_end[t] + NK - 1) / NK;
-      for (int j = (g ^ grp) & 1; j < tiles; j += 2) {
-        const int ab = grp;
-        if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), ((g + j) >> 1) & 1, abort_flag))) break;
+      int t, d3;
+      const TileSpan sp = part(item, t, d3);
+      for (int j = sp.j0 + ((g ^ grp) & 1); j < sp.j1; j += 2) {
+        const int ab = grp;                // tile j is the CTA's tile g + j - j0, of this group's parity
+        if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), ((g + j - sp.j0) >> 1) & 1, abort_flag))) break;
         tc_fence_after();
         uint16_t* out = p.contrib + (static_cast<long long>(t) * p.kp + j * NK + quad * 32) * D + 192 * d3;
 #pragma unroll
@@ -726,7 +752,7 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
           store_rows<8>(cta.smem + OFF_TURN + (4 * grp + quad) * 4096, w, out + 64 * c, 2 * D);
         }
       }
-      g += tiles;
+      g += sp.j1 - sp.j0;
     }
   }
   bwd_end(cta);
