@@ -721,12 +721,38 @@ bool make_rows_map(CUtensorMap* m, const uint16_t* base, long long rows, int wid
   return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Splits of each of n items' `tiles` tiles over `workers` CTAs (or pairs) that minimise the rounds' length: cost = rounds x
+// (tiles of a split + `setup`, what an item costs beside its tiles, in tiles).
+int choose_splits(long long n, int workers, int tiles, double setup) {
+  int best = 1;
+  double best_cost = 1e300;
+  for (int s = 1; s <= tiles; ++s) {
+    const double cost = static_cast<double>((n * s + workers - 1) / workers) * ((tiles + s - 1) / s + setup);
+    if (cost < best_cost - 1e-9) { best_cost = cost; best = s; }
+  }
+  return best;
+}
+// The same where the splits' sums have to be joined: only for at most two rounds of items, so that the parts stay small.
+int choose_joined_splits(long long n, int workers, int tiles, double setup) {
+  return n > 2 * workers ? 1 : choose_splits(n, workers, tiles, setup);
+}
+
+dsa_status_t join_splits(const float* part, const int* n_end, int keys, int splits, int T, int width, int tail,
+                         uint16_t* out, float* out_tail, cudaStream_t st) {
+  if (launch_pdl(join_splits_kernel, dim3((width + tail + 1023) / 1024, T), dim3(256), 0, st, part, n_end, keys, splits,
+                 width, tail, out, out_tail) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  return last_launch_status();
+}
+
 // Workspace of the attention's backward pass.
 struct AttnBwdWs {
   int Tc, HP, kp;
   ScatterWs sc;
   float* delta;
   uint16_t* pds;
+  int dq_splits;              // of a chunk of all T tokens (the only chunk where there are few)
+  float* dq_part;
   size_t bytes;
 };
 AttnBwdWs attn_bwd_ws(void* ws, int T, int64_t S, int H, int k) {
@@ -738,6 +764,9 @@ AttnBwdWs attn_bwd_ws(void* ws, int T, int64_t S, int H, int k) {
   a.sc = carve_scatter(w, a.Tc, S, a.kp, mbw::D, a.Tc < T);
   a.delta = w.take<float>(size_t(a.Tc) * H);
   a.pds = w.take<uint16_t>(size_t(a.Tc) * a.kp * 2 * a.HP);
+  // 3 stages of 64 keys are about what an item's start and end take
+  a.dq_splits = a.Tc < T ? 1 : choose_joined_splits(3ll * T, num_sms(), a.kp / mbw::dq::KT, 6.0);
+  a.dq_part = a.dq_splits > 1 ? w.take<float>(size_t(T) * a.dq_splits * H * mbw::D) : nullptr;
   a.bytes = w.at;
   return a;
 }
@@ -785,21 +814,25 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
     dsa_status_t e = last_launch_status();
     if (e != DSA_OK) return e;
     if ((e = scatter_build(w.sc, p.idx, n, S, k, st)) != DSA_OK) return e;
-    // few tokens: their tiles are dealt to as many CTAs as there are (with at least a tile of 256 keys each)
-    p.splits = n >= sms / 2 ? 1 : std::min((sms / 2) / n, (k + 255) / 256);
-    const int items = n * p.splits;
-    if (launch_pdl(mla_bwd_p_kernel<false>, dim3(2 * std::min(sms / 2, items)), dim3(mbw::p::THREADS),
+    p.splits = choose_splits(n, sms / 2, (k + 255) / 256, 0.8);
+    if (launch_pdl(mla_bwd_p_kernel<false>, dim3(2 * std::min(sms / 2, n * p.splits)), dim3(mbw::p::THREADS),
                    mbw::p::Map<false>::SMEM, st, tq, tdo, tc, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
-    if (launch_pdl(mla_bwd_dc_kernel, dim3(std::min(sms, 3 * items)), dim3(mbw::dc::THREADS), mbw::dc::SMEM, st, tp128,
-                   tq, tdo, p) != cudaSuccess)
+    p.splits = choose_splits(3ll * n, sms, w.kp / 128, 1.5);
+    if (launch_pdl(mla_bwd_dc_kernel, dim3(std::min(sms, 3 * n * p.splits)), dim3(mbw::dc::THREADS), mbw::dc::SMEM, st,
+                   tp128, tq, tdo, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
-    if (launch_pdl(mla_bwd_dq_kernel, dim3(std::min(sms, 3 * n)), dim3(mbw::dq::THREADS), mbw::dq::SMEM, st, tp64,
-                   p) != cudaSuccess)
+    p.splits = w.dq_splits;
+    p.dq_part = w.dq_part;
+    if (launch_pdl(mla_bwd_dq_kernel, dim3(std::min(sms, 3 * n * p.splits)), dim3(mbw::dq::THREADS), mbw::dq::SMEM, st,
+                   tp64, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
+    if (p.splits > 1 && (e = join_splits(w.dq_part, w.sc.n_end, mbw::dq::KT, p.splits, n, H * mbw::D, 0, p.dq, nullptr,
+                                         st)) != DSA_OK)
+      return e;
     e = scatter_end<mbw::D>(w.sc, p.idx, n, S, k, w.kp, t0 == 0, t0 + n >= T, dc, st);
     if (e != DSA_OK) return e;
   }
@@ -845,16 +878,19 @@ dsa_status_t run_kl_bwd(const uint16_t* q, const uint16_t* c, int S, const int32
 
 // Workspace of the index scores' backward pass.
 struct IndexBwdWs {
-  int Tc, kp;
+  int Tc, kp, splits;
   ScatterWs sc;
+  float* part;
   size_t bytes;
 };
-IndexBwdWs index_bwd_ws(void* ws, int T, int64_t S, int d_I, int k) {
+IndexBwdWs index_bwd_ws(void* ws, int T, int64_t S, int H_I, int d_I, int k) {
   IndexBwdWs a{};
   a.kp = round_up(k, 128);
   a.Tc = bwd_chunk(T, S, a.kp, size_t(d_I) * 2);
   Carve w{static_cast<char*>(ws)};
   a.sc = carve_scatter(w, a.Tc, S, a.kp, d_I, a.Tc < T);
+  a.splits = a.Tc < T ? 1 : choose_joined_splits(T, num_sms(), a.kp / ixb::NK, 2.0);
+  a.part = a.splits > 1 ? w.take<float>(size_t(T) * a.splits * (size_t(H_I) * d_I + H_I)) : nullptr;
   a.bytes = w.at;
   return a;
 }
@@ -866,6 +902,8 @@ dsa_status_t run_index_bwd(IndexerBwdParams p, int T, uint16_t* dk, const IndexB
   if (set_smem(indexer_bwd_kernel<HI, DI>, ixb::SMEM) != cudaSuccess) return DSA_ERR_CUDA;
   p.n_end = w.sc.n_end;
   p.kp = w.kp;
+  p.splits = w.splits;
+  p.part = w.part;
   const IndexerBwdParams all = p;
   for (int t0 = 0; t0 < T; t0 += w.Tc) {
     const size_t o = static_cast<size_t>(t0);
@@ -883,10 +921,12 @@ dsa_status_t run_index_bwd(IndexerBwdParams p, int T, uint16_t* dk, const IndexB
     dsa_status_t e = last_launch_status();
     if (e != DSA_OK) return e;
     if ((e = scatter_build(w.sc, p.idx, p.T, p.S, p.k, st)) != DSA_OK) return e;
-    if (launch_pdl(indexer_bwd_kernel<HI, DI>, dim3(std::min(num_sms(), p.T)), dim3(ixb::THREADS), ixb::SMEM, st, tout,
+    if (launch_pdl(indexer_bwd_kernel<HI, DI>, dim3(std::min(num_sms(), p.T * p.splits)), dim3(ixb::THREADS), ixb::SMEM, st, tout,
                    p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
+    if (p.splits > 1 && (e = join_splits(w.part, w.sc.n_end, ixb::NK, p.splits, p.T, HI * DI, HI, p.dq, p.dw, st)) != DSA_OK)
+      return e;
     e = scatter_end<DI>(w.sc, p.idx, p.T, p.S, p.k, w.kp, t0 == 0, t0 + p.T >= T, dk, st);
     if (e != DSA_OK) return e;
   }
@@ -1679,7 +1719,7 @@ dsa_status_t dsa_indexer_kl_backward(const uint16_t* q, const uint16_t* c, int S
 
 size_t dsa_indexer_scores_backward_workspace_size(int T, int S, int H_I, int d_I, int k) {
   if (T <= 0 || S <= 0 || !indexer_shape_ok(H_I, d_I) || !mla_k_ok(k)) return 0;
-  return index_bwd_ws(nullptr, T, S, d_I, k).bytes;
+  return index_bwd_ws(nullptr, T, S, H_I, d_I, k).bytes;
 }
 
 dsa_status_t dsa_indexer_scores_backward(const uint8_t* q_idx, const float* q_scale, const uint8_t* k_idx,
@@ -1694,7 +1734,7 @@ dsa_status_t dsa_indexer_scores_backward(const uint8_t* q_idx, const float* q_sc
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (T == 0)
     return cudaMemsetAsync(dk, 0, size_t(S) * d_I * 2, st) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
-  const IndexBwdWs a = index_bwd_ws(ws, T, S, d_I, k);
+  const IndexBwdWs a = index_bwd_ws(ws, T, S, H_I, d_I, k);
   if (!ws || ws_bytes < a.bytes) return DSA_ERR_WORKSPACE;
   IndexerBwdParams p{};
   p.q_idx = q_idx;

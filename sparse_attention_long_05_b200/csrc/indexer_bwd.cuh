@@ -6,7 +6,7 @@
 // with G = e w_j 1[x > 0]: three products of 2 x 64 heads x 128 dims per entry.  dq and dk are gradients of the
 // dequantised values (what a straight-through quantiser passes on).
 //
-// One CTA per token, keys are the M dimension.  e4m3 rows are gathered with plain 16-byte loads and written as bf16
+// One CTA per token (or per split of a token's tiles, where tokens are few), keys are the M dimension.  e4m3 rows are gathered with plain 16-byte loads and written as bf16
 // (exact) in the swizzled form the tensor core reads, so the one copy serves x (K-major), dq (transposed, MN-major)
 // and, for q, dk; kind::f16 needs both operands bf16 and G is.  x is exact: products of e4m3 are, and their sum is
 // held in fp32.  G and G ks are rounded to bf16 once (2^-9).  dw is summed from the fp32 x.  Per token: 16 tiles of
@@ -30,7 +30,8 @@ struct IndexerBwdParams {
   const int* n_end;            // [T]
   uint16_t* dq;                // [T, HI, DI] bf16
   float* dw;                   // [T, HI]
-  int T, k, kp;
+  float* part;                 // splits > 1: [T * splits, HI * DI + HI] dq and dw of each split
+  int T, k, kp, splits;        // a token's tiles are dealt to `splits` items
   long long S;
 };
 
@@ -112,14 +113,20 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
   bwd_begin(cta);
   const uint32_t tmem = cta.tmem;
   bool ok = true;
-  int n = 0;                             // tokens with entries, walked so far
-  auto tiles_of = [&](int t) { return (p.n_end[t] + NK - 1) / NK; };
+  int n = 0;                             // items with tiles, walked so far
+  const int items = p.T * p.splits;
+  auto token = [&](int item) { return p.splits == 1 ? item : item / p.splits; };
+  auto span = [&](int item) {
+    return tile_span(p.n_end[token(item)], NK, p.splits == 1 ? 0 : item % p.splits, p.splits);
+  };
 
   if (warp == 0) {
     // ===================================================================== index rows
     if (lane == 0) {
-      for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
-        if (tiles_of(t) <= 0) continue;
+      for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const TileSpan sp = span(item);
+        if (sp.j0 >= sp.j1) continue;
+        const int t = token(item);
         const int ib = n & 1;
         if (!(ok = mbar_wait(cta.bar(B_IDX_EMPTY + ib), ((n >> 1) & 1) ^ 1, abort_flag))) break;
         mbar_arrive_expect_tx(cta.bar(B_IDX_FULL + ib), p.k * 4);
@@ -138,9 +145,10 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
     constexpr int STEPS = NK / PRODUCERS / ROWS;  // 4 (DI = 128), 2 (64)
     const int sub = lane / U, u = lane % U;
     int g = 0;
-    for (int t = blockIdx.x; t < p.T && ok; t += gridDim.x) {
-      const int tiles = tiles_of(t);
-      if (tiles <= 0) continue;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const TileSpan sp = span(item);
+      if (sp.j0 >= sp.j1) continue;
+      const int t = token(item);
       const int ib = n & 1;
       if (!(ok = warp_wait(cta.bar(B_IDX_FULL + ib), (n >> 1) & 1, abort_flag))) break;
       const int* ids = reinterpret_cast<const int*>(cta.smem + OFF_IDX + ib * mla::KMAX * 4);
@@ -155,7 +163,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
         }
       };
       uint4 v[STEPS];
-      load(0, v);
+      load(sp.j0, v);
       if (!(ok = warp_wait(cta.bar(B_Q_EMPTY + ib), ((n >> 1) & 1) ^ 1, abort_flag))) break;
       const uint4* qrow = reinterpret_cast<const uint4*>(p.q_idx + static_cast<long long>(t) * HI * DI);
       for (int i = pw * 32 + lane; i < HI * U; i += PRODUCERS * 32)
@@ -163,10 +171,10 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(cta.bar(B_Q_FULL + ib));
-      for (int j = 0; j < tiles; ++j, ++g) {
+      for (int j = sp.j0; j < sp.j1; ++j, ++g) {
         const int kb = g & 1;
         uint4 next[STEPS];
-        if (j + 1 < tiles) load(j + 1, next);
+        if (j + 1 < sp.j1) load(j + 1, next);
         if (!(ok = warp_wait(cta.bar(B_K_EMPTY + kb), ((g >> 1) & 1) ^ 1, abort_flag))) break;
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
@@ -182,13 +190,16 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
     }
   } else if (warp == 1) {
     // ===================================================================== MMA issue
-    struct Cursor { int t, j, tiles, n, g; } a{static_cast<int>(blockIdx.x), 0, 0, 0, 0}, b;
-    auto seek = [&](Cursor& c) {          // first token at or after c.t with entries
-      while (c.t < p.T && (c.tiles = tiles_of(c.t)) <= 0) c.t += gridDim.x;
+    struct Cursor { int item, j, tiles, n, g; } a{static_cast<int>(blockIdx.x), 0, 0, 0, 0}, b;
+    auto seek = [&](Cursor& c) {          // first item at or after c.item with tiles
+      for (; c.item < items; c.item += gridDim.x) {
+        const TileSpan sp = span(c.item);
+        if ((c.tiles = sp.j1 - sp.j0) > 0) break;
+      }
     };
     auto step = [&](Cursor& c) {
       ++c.g;
-      if (++c.j == c.tiles) { c.j = 0; ++c.n; c.t += gridDim.x; seek(c); }
+      if (++c.j == c.tiles) { c.j = 0; ++c.n; c.item += gridDim.x; seek(c); }
     };
     seek(a);
     b = a;
@@ -213,9 +224,9 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
       step(a);
       return true;
     };
-    if (a.t < p.T) ok = scores();
-    while (ok && b.t < p.T) {
-      if (a.t < p.T && !(ok = scores())) break;
+    if (a.item < items) ok = scores();
+    while (ok && b.item < items) {
+      if (a.item < items && !(ok = scores())) break;
       const int s = b.g & 1, qb = b.n & 1;
       if (b.j == 0 && !(ok = warp_wait(cta.bar(B_DQ_EMPTY + qb), ((b.n >> 1) & 1) ^ 1, abort_flag))) break;
       if (!(ok = warp_wait(cta.bar(B_DK_EMPTY + s), ((b.g >> 1) & 1) ^ 1, abort_flag))) break;
@@ -255,10 +266,14 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
     constexpr int BLOCKS = (HI + 15) / 16;               // 16 heads at a time
     float* dw_s = reinterpret_cast<float*>(cta.smem + OFF_DW);
     int g = 0;
-    for (int t = blockIdx.x; t < p.T && ok; t += gridDim.x) {
-      const int tiles = tiles_of(t);
-      if (tiles <= 0) {
-        if (grp == 0 && row < HI) p.dw[static_cast<long long>(t) * HI + row] = 0.f;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const TileSpan sp = span(item);
+      const int t = token(item);
+      // where dw goes: the token's results, or the split's part
+      float* dw_out = p.splits == 1 ? p.dw + static_cast<long long>(t) * HI
+                                    : p.part + static_cast<long long>(item) * (HI * DI + HI) + HI * DI;
+      if (sp.j0 >= sp.j1) {                              // (an empty split is not read)
+        if (p.splits == 1 && grp == 0 && row < HI) dw_out[row] = 0.f;
         continue;
       }
       float* ws = reinterpret_cast<float*>(cta.smem + OFF_W) + 64 * (n & 1);
@@ -266,22 +281,22 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
       const long long base = static_cast<long long>(t) * p.k;
       auto entry = [&](int j) {
         const int slot = j * NK + row;
-        const int id = j < tiles && slot < p.k ? __ldg(p.idx + base + slot) : -1;
+        const int id = j < sp.j1 && slot < p.k ? __ldg(p.idx + base + slot) : -1;
         return id < p.S ? id : -1;
       };
       auto grad = [&](int j, int id) { return id >= 0 ? __ldg(p.dsel + base + j * NK + row) : 0.f; };
       auto scale = [&](int id) { return id < 0 ? 0.f : p.k_scale ? __ldg(p.k_scale + id) : 1.f; };
-      const int j0 = (g ^ grp) & 1;
+      const int j0 = sp.j0 + ((g ^ grp) & 1);            // tile j is the CTA's tile g + j - j0
       int id = entry(j0), id_next = entry(j0 + 2);
       float e = grad(j0, id), ks = scale(id);
       if (!(ok = named_bar_all(1, 256, ok))) break;
       float dw[BLOCKS] = {};
-      for (int j = j0; j < tiles; j += 2) {
-        const int s = grp;                               // (g + j) % 2
+      for (int j = j0; j < sp.j1; j += 2) {
+        const int s = grp, use = (g + j - sp.j0) >> 1;
         const float e_next = grad(j + 2, id_next), ks_next = scale(id_next);
         id_next = entry(j + 4);
-        ok = warp_wait(cta.bar(B_X_FULL + s), ((g + j) >> 1) & 1, abort_flag);
-        ok = ok && warp_wait(cta.bar(B_G_EMPTY + s), (((g + j) >> 1) & 1) ^ 1, abort_flag);
+        ok = warp_wait(cta.bar(B_X_FULL + s), use & 1, abort_flag);
+        ok = ok && warp_wait(cta.bar(B_G_EMPTY + s), (use & 1) ^ 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         uint8_t* gl = cta.smem + OFF_G + 2 * s * G_BYTES + row * 128;
@@ -344,7 +359,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
         e = e_next;
         ks = ks_next;
       }
-      g += tiles;
+      g += sp.j1 - sp.j0;
       if (lane < 16) {
 #pragma unroll
         for (int c = 0; c < BLOCKS; ++c) dw_s[(4 * grp + quad) * 64 + 16 * c + lane] = dw[c];
@@ -354,7 +369,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) sum += dw_s[64 * w + row];
-        p.dw[static_cast<long long>(t) * HI + row] = sum * (p.q_scale ? p.q_scale[t] : 1.f);
+        dw_out[row] = sum * (p.q_scale ? p.q_scale[t] : 1.f);
       }
       // the next token's first barrier comes before anyone writes dw_s again
       ++n;
@@ -364,15 +379,17 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     int g = 0;
-    for (int t = blockIdx.x; t < p.T && ok; t += gridDim.x) {
-      const int tiles = tiles_of(t);
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const TileSpan sp = span(item);
+      const int t = token(item);
       uint16_t* dq = p.dq + static_cast<long long>(t) * HI * DI;
-      if (tiles <= 0) {
+      if (sp.j0 >= sp.j1) {
+        if (p.splits > 1) continue;
         for (int i = row; i < HI * DI / 8; i += 128) reinterpret_cast<uint4*>(dq)[i] = make_uint4(0, 0, 0, 0);
         continue;
       }
       const float qs = p.q_scale ? p.q_scale[t] : 1.f;
-      for (int j = 0; j < tiles; ++j, ++g) {
+      for (int j = sp.j0; j < sp.j1; ++j, ++g) {
         const int s = g & 1;
         if (!(ok = warp_wait(cta.bar(B_DK_FULL + s), (g >> 1) & 1, abort_flag))) break;
         tc_fence_after();
@@ -416,11 +433,16 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
         uint32_t v[32];
         tmem_ld32(lane_addr + tmem + TDQ + 64 * qb + 32 * c, v);
         tmem_wait_ld();
-        if (row < DI) {
+        if (row < DI && p.splits == 1) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (32 * c + i < HI)
               dq[(32 * c + i) * DI + row] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[i])));
+        } else if (row < DI) {
+          float* part = p.part + static_cast<long long>(item) * (HI * DI + HI) + row;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * c + i < HI) part[(32 * c + i) * DI] = __uint_as_float(v[i]);
         }
       }
       tc_fence_before();

@@ -39,6 +39,7 @@ struct MlaBwdParams {
   uint16_t* pds;               // [T * kp, 2 HP] bf16: dS of HP heads, then P of HP heads, for every slot
   uint16_t* contrib;           // [T * kp, 576] bf16: each entry's contribution to dc
   uint16_t* dq;                // [T, H, 576]
+  float* dq_part;              // splits > 1: [T * splits, H, 576] sums of each split
   int T, t0;                   // tokens of the chunk; the first one's index in q and dout
   int splits;                  // a token's tiles are dealt to this many items (P and dS, contributions)
   int H, HP;                   // heads; heads rounded up to 64
@@ -758,7 +759,8 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
   bwd_end(cta);
 }
 
-// dq[t][:, 192 dims] = dS^T . C per item, accumulated over the token's keys in tensor memory (lane = head).
+// dq[t][:, 192 dims] = dS^T . C per item, accumulated over the token's keys (or, with splits, over the split's) in tensor
+// memory (lane = head).
 __global__ void __launch_bounds__(mbw::dq::THREADS, 1)
 mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams p) {
   using namespace mbw;
@@ -781,7 +783,13 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
   bwd_begin(cta);
   const uint32_t tmem = cta.tmem;
   const uint32_t ring = sbase + OFF_RING;
-  const int items = 3 * p.T;
+  const int items = 3 * p.T * p.splits;
+  auto part = [&](int item, int& ts, int& d3) {        // item: (token, split, 192 dims)
+    d3 = item % 3;
+    ts = item / 3;
+    return p.splits == 1 ? tile_span(p.n_end[ts], KT, 0, 1) : tile_span(p.n_end[ts / p.splits], KT, ts % p.splits, p.splits);
+  };
+  auto token = [&](int ts) { return p.splits == 1 ? ts : ts / p.splits; };
   bool ok = true;
   int n = 0;
 
@@ -791,8 +799,10 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
       Pipe<NS> rp;
       int issued = 0;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        const int t = item / 3, tiles = (p.n_end[t] + KT - 1) / KT;
-        for (int j = 0; j < tiles; ++j, rp.advance(), ++issued) {
+        int ts, d3;
+        const TileSpan sp = part(item, ts, d3);
+        const int t = token(ts);
+        for (int j = sp.j0; j < sp.j1; ++j, rp.advance(), ++issued) {
           if (!(ok = mbar_wait(cta.bar(B_RING_EMPTY + rp.stage), rp.phase ^ 1, abort_flag))) break;
           const uint32_t full = cta.bar(B_RING_FULL + rp.stage), dst = ring + rp.stage * STAGE;
           mbar_arrive_expect_tx(full, A_BYTES);
@@ -813,16 +823,17 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
     const int grp = gw >> 2, rows = (gw & 3) * 16, sub = lane >> 3, unit = lane & 7;
     int m = 0;                             // stages of the items before this one
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const int t = item / 3, d3 = item % 3, tiles = (p.n_end[t] + KT - 1) / KT;
-      const int* ids = p.idx + static_cast<long long>(t) * p.k;
+      int ts, d3;
+      const TileSpan sp = part(item, ts, d3);
+      const int* ids = p.idx + static_cast<long long>(token(ts)) * p.k;
       // k is a multiple of the tile: every slot of a tile is below k
-      auto entry = [&](int j) { return j < tiles ? __ldg(ids + j * KT + rows + (lane & 15)) : -1; };
-      const int j0 = (grp + m) & 1;
+      auto entry = [&](int j) { return j < sp.j1 ? __ldg(ids + j * KT + rows + (lane & 15)) : -1; };
+      const int j0 = sp.j0 + ((grp + m) & 1);            // tile j is the CTA's stage m + j - j0
       int mine = entry(j0);
-      for (int j = j0; j < tiles; j += 2) {
-        const int st = (m + j) % NS;
+      for (int j = j0; j < sp.j1; j += 2) {
+        const int at = m + j - sp.j0, st = at % NS;
         const int next = entry(j + 2);
-        if (!(ok = warp_wait(cta.bar(B_RING_EMPTY + st), (((m + j) / NS) & 1) ^ 1, abort_flag))) break;
+        if (!(ok = warp_wait(cta.bar(B_RING_EMPTY + st), ((at / NS) & 1) ^ 1, abort_flag))) break;
         const uint32_t dst = ring + st * STAGE + A_BYTES + (rows + sub) * 128;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -830,14 +841,14 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
           const bool valid = e >= 0 && e < p.S;
           const char* src = reinterpret_cast<const char*>(p.c) + (valid ? static_cast<long long>(e) * (D * 2) : 0) +
                             384 * d3 + 16 * unit;
-          const uint32_t at = dst + i * 512 + ((unit ^ ((4 * i + sub) & 7)) << 4);
+          const uint32_t to = dst + i * 512 + ((unit ^ ((4 * i + sub) & 7)) << 4);
 #pragma unroll
-          for (int c = 0; c < 3; ++c) cp_async16(at + c * HCHUNK, src + 128 * c, valid);
+          for (int c = 0; c < 3; ++c) cp_async16(to + c * HCHUNK, src + 128 * c, valid);
         }
         cp_async_arrive(cta.bar(B_RING_FULL + st));
         mine = next;
       }
-      m += tiles;
+      m += sp.j1 - sp.j0;
     }
     cp_async_wait_all();
   } else if (warp == 1) {
@@ -845,12 +856,13 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
     Pipe<NS> rp;
     constexpr uint32_t idesc = idesc_bf16_major(128, 192, true, true);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const int t = item / 3, tiles = (p.n_end[t] + KT - 1) / KT;
-      if (tiles <= 0) continue;
+      int ts, d3;
+      const TileSpan sp = part(item, ts, d3);
+      if (sp.j0 >= sp.j1) continue;
       const int ab = n & 1;
       if (!(ok = warp_wait(cta.bar(B_ACC_EMPTY + ab), ((n >> 1) & 1) ^ 1, abort_flag))) break;
       tc_fence_after();
-      for (int j = 0; j < tiles; ++j, rp.advance()) {
+      for (int j = sp.j0; j < sp.j1; ++j, rp.advance()) {
         if (!(ok = warp_wait(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
         fence_proxy_async_smem();            // the gathered keys were written through the generic proxy
         tc_fence_after();
@@ -860,7 +872,7 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
-            mma_bf16_ss(tmem + 256 * ab, ad + ((k * 2048) >> 4), bd + ((k * 2048) >> 4), idesc, (j | k) ? 1u : 0u);
+            mma_bf16_ss(tmem + 256 * ab, ad + ((k * 2048) >> 4), bd + ((k * 2048) >> 4), idesc, (j > sp.j0 || k) ? 1u : 0u);
           mma_commit(cta.bar(B_RING_EMPTY + rp.stage));
         }
         __syncwarp();
@@ -875,11 +887,12 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
     const int quad = warp & 3, h = quad * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const int t = item / 3, d3 = item % 3;
-      uint4* dst = reinterpret_cast<uint4*>(p.dq + (static_cast<long long>(t) * p.H + h) * D + 192 * d3);
-      if (p.n_end[t] <= 0) {               // nothing selected: dq = 0
-        if (h < p.H)
-          for (int i = 0; i < 24; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+      int ts, d3;
+      const TileSpan sp = part(item, ts, d3);
+      const long long at = (static_cast<long long>(ts) * p.H + h) * D + 192 * d3;
+      if (sp.j0 >= sp.j1) {                // nothing selected: dq = 0 (an empty split is not read)
+        if (h < p.H && p.splits == 1)
+          for (int i = 0; i < 24; ++i) reinterpret_cast<uint4*>(p.dq + at)[i] = make_uint4(0, 0, 0, 0);
         continue;
       }
       const int ab = n & 1;
@@ -889,12 +902,18 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
         uint32_t v[32];
         tmem_ld32(lane_addr + tmem + 256 * ab + 32 * c, v);
         tmem_wait_ld();
-        if (h < p.H) {
+        if (h >= p.H) continue;
+        if (p.splits == 1) {
+          uint4* dst = reinterpret_cast<uint4*>(p.dq + at + 32 * c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             auto pk = [&](int q) { return pack_bf16(__uint_as_float(v[8 * i + 2 * q]), __uint_as_float(v[8 * i + 2 * q + 1])); };
-            dst[4 * c + i] = make_uint4(pk(0), pk(1), pk(2), pk(3));
+            dst[i] = make_uint4(pk(0), pk(1), pk(2), pk(3));
           }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.dq_part + at + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
       }
       tc_fence_before();
@@ -904,6 +923,28 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
     }
   }
   bwd_end(cta);
+}
+
+// The splits' sums of a token joined in order: out[t][i] = sum over its splits of part[t splits + sp][i], i < width (bf16),
+// and the last `tail` values of a part (fp32 results).  width and tail are multiples of 4.
+__global__ void __launch_bounds__(256) join_splits_kernel(const float* part, const int* n_end, int keys, int splits,
+                                                          int width, int tail, uint16_t* out, float* out_tail) {
+  pdl_allow_next();
+  pdl_wait();
+  const int t = blockIdx.y, i = 4 * (blockIdx.x * 256 + threadIdx.x);
+  if (i >= width + tail) return;
+  const int tiles = (n_end[t] + keys - 1) / keys, per = (tiles + splits - 1) / splits;
+  const int used = tiles > 0 ? (tiles + per - 1) / per : 0;
+  const float* at = part + static_cast<long long>(t) * splits * (width + tail) + i;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int sp = 0; sp < used; ++sp, at += width + tail) {
+    const float4 v = *reinterpret_cast<const float4*>(at);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  if (i < width)
+    *reinterpret_cast<uint2*>(out + static_cast<long long>(t) * width + i) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+  else
+    *reinterpret_cast<float4*>(out_tail + static_cast<long long>(t) * tail + i - width) = s;
 }
 
 // What the other kernels of a chunk start from: delta[t][h] = dout . out over the 512 value dims (one warp a row, eight rows
