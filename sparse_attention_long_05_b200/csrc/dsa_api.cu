@@ -696,13 +696,19 @@ dsa_status_t scatter_build(const ScatterWs& w, const int* idx, int T, int64_t S,
   return last_launch_status();
 }
 
+constexpr long long kShortList = 16;
+
 template <int W>
 dsa_status_t scatter_end(const ScatterWs& w, const int* idx, int T, int64_t S, int k, int kp, bool first, bool last, uint16_t* out,
                          cudaStream_t st) {
   const ScatterParams p{w.contrib, w.table, idx, T, w.ld, k, kp, w.acc, first ? 1 : 0, last ? 1 : 0, out};
-  if (launch_pdl(scatter_sum_kernel<W>, dim3(static_cast<unsigned>(S)), dim3(ScatterCfg<W>::THREADS), 0, st, p) !=
-      cudaSuccess)
-    return DSA_ERR_CUDA;
+  // by the mean length of a row's list (T k / S at most): short ones a warp each
+  const bool brief = static_cast<long long>(T) * k < kShortList * static_cast<long long>(S);
+  const cudaError_t err =
+      brief ? launch_pdl(scatter_sum_short_kernel<W>, dim3(static_cast<unsigned>((S + kSumWarps - 1) / kSumWarps)),
+                         dim3(32 * kSumWarps), 0, st, p, static_cast<long long>(S))
+            : launch_pdl(scatter_sum_kernel<W>, dim3(static_cast<unsigned>(S)), dim3(ScatterCfg<W>::THREADS), 0, st, p);
+  if (err != cudaSuccess) return DSA_ERR_CUDA;
   return last_launch_status();
 }
 

@@ -227,4 +227,105 @@ __global__ void __launch_bounds__(ScatterCfg<W>::THREADS, 6) scatter_sum_kernel(
   }
 }
 
+// The same for short lists: one warp per row, 32-bit loads (a warp reads a contribution in W / 64 of them), four rows in
+// flight, nothing shared between warps.  With few entries a row the time is the chain table -> entries -> result, which
+// eight rows a CTA walk at once here.
+constexpr int kSumWarps = 8;
+template <int W>
+__global__ void __launch_bounds__(32 * kSumWarps) scatter_sum_short_kernel(const ScatterParams p, long long S) {
+  constexpr int V = W / 64;                // 32-bit words of a lane
+  __shared__ uint32_t lists[kSumWarps][256];
+  pdl_allow_next();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long s = static_cast<long long>(blockIdx.x) * kSumWarps + warp;
+  if (s >= S) return;
+  uint32_t* list = lists[warp];
+  const uint4* row = reinterpret_cast<const uint4*>(p.table + s * p.ld);
+  float sum[2 * V] = {};
+  auto read = [&](uint32_t t, int slot, uint32_t (&v)[V]) {
+    const uint32_t* at = reinterpret_cast<const uint32_t*>(p.contrib + (static_cast<long long>(t) * p.kp + slot) * W);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = __ldcs(at + 32 * i + lane);
+  };
+  auto add = [&](const uint32_t (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      sum[2 * i] += __uint_as_float(v[i] << 16);
+      sum[2 * i + 1] += __uint_as_float(v[i] & 0xffff0000u);
+    }
+  };
+  for (int q0 = 0; q0 < p.ld / 8; q0 += 32) {
+    // 256 tokens: eight a lane, listed in token order
+    const uint4 q = q0 + lane < p.ld / 8 ? row[q0 + lane] : make_uint4(~0u, ~0u, ~0u, ~0u);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    int mine = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) mine += ((w[u >> 1] >> (16 * (u & 1))) & 0xffffu) != sct::EMPTY;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    const int n = __shfl_sync(0xffffffffu, upto, 31);
+    int to = upto - mine;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t v = (w[u >> 1] >> (16 * (u & 1))) & 0xffffu;
+      if (v != sct::EMPTY)
+        list[to++] = (static_cast<uint32_t>(8 * (q0 + lane) + u) << 11) | (v & (sct::TWICE - 1)) | ((v & sct::TWICE) << 20);
+    }
+    __syncwarp();
+    for (int i = 0; i < n; i += 4) {
+      uint32_t v[4][V];
+      uint32_t any = 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t e = i + u < n ? list[i + u] : 0;
+        any |= e;
+        if (i + u < n) {
+          read((e >> 11) & 0xfffff, e & (sct::TWICE - 1), v[u]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[u][j] = 0;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) add(v[u]);
+      if (any >> 31) {                     // the row's later slots of a token that selected it more than once
+#pragma unroll 1
+        for (int u = i; u < min(n, i + 4); ++u) {
+          const uint32_t e = list[u], t = (e >> 11) & 0xfffff;
+          if (!(e >> 31)) continue;
+          const int* ids = p.idx + static_cast<long long>(t) * p.k;
+#pragma unroll 1
+          for (int j = (e & (sct::TWICE - 1)) + 1; j < p.k; ++j)
+            if (ids[j] == s) {
+              read(t, j, v[0]);
+              add(v[0]);
+            }
+        }
+      }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const long long at = s * (W / 2) + 32 * i + lane;    // in pairs of values
+    float2 total = make_float2(sum[2 * i], sum[2 * i + 1]);
+    if (p.acc && !p.first) {
+      const float2 v = reinterpret_cast<const float2*>(p.acc)[at];
+      total.x += v.x;
+      total.y += v.y;
+    }
+    if (p.last) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(total.x, total.y);
+      reinterpret_cast<uint32_t*>(p.out)[at] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      reinterpret_cast<float2*>(p.acc)[at] = total;
+    }
+  }
+}
+
 }  // namespace dsa

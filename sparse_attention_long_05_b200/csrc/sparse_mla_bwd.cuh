@@ -95,6 +95,10 @@ __device__ __forceinline__ void mma2_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                :: "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
+               :: "l"(map), "r"(x), "r"(y), "r"(z) : "memory");
+}
 // loads into this CTA's shared memory that complete on a barrier of either CTA of the pair (a cluster address)
 __device__ __forceinline__ void tma2_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
   asm volatile(
@@ -321,31 +325,42 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
   if (warp == 0) {
     // ===================================================================== resident rows of q (and dout)
-    if (lane == 0) {
-      for (int item = first; item < items && ok; item += stride) {
-        const TileSpan sp = span(item);
-        if (sp.j0 >= sp.j1) continue;
-        const int t = token(item);
-        for (int c = 0; c < DCH; ++c) {
-          if (!(ok = mbar_wait(cta.bar(B_RES_EMPTY + c), (n & 1) ^ 1, abort_flag))) break;
-          const uint32_t dst = res + c * M::RES_CHUNK, full = lead + 8 * (B_RES_FULL + c);
-          if (KL || c == 8) {
-            mbar_arrive_expect_tx_remote(full, HCHUNK);
-            tma2_load_3d(dst, &tm_q, full, 64 * c, rank * (p.HP / 2), p.t0 + t);
-          } else {
-            mbar_arrive_expect_tx_remote(full, (p.HP / 64) * HCHUNK);
-            for (int i = 0; i < p.HP / 64; ++i)
-              tma2_load_3d(dst + i * HCHUNK, rank ? &tm_do : &tm_q, full, 64 * c, 64 * i, p.t0 + t);
-          }
+    // Three lanes take a chunk each: one thread alone needs about 300 ns a load, 5 us an item, which nothing overlaps.
+    // The next item's rows are brought into L2 meanwhile.
+    for (int item = first; item < items && ok; item += stride) {
+      const TileSpan sp = span(item);
+      if (sp.j0 >= sp.j1) continue;
+      const int t = token(item);
+      auto rows = [&](int c, int tok, bool ahead) {      // this CTA's boxes of chunk c
+        const CUtensorMap* map = !KL && c < 8 && rank ? &tm_do : &tm_q;
+        const bool part = KL || c == 8;
+        const int boxes = part ? 1 : p.HP / 64, h0 = part ? rank * (p.HP / 2) : 0;
+        const uint32_t full = lead + 8 * (B_RES_FULL + c);
+        if (!ahead) mbar_arrive_expect_tx_remote(full, boxes * HCHUNK);
+        for (int i = 0; i < boxes; ++i) {
+          if (ahead) tma_prefetch_3d(map, 64 * c, h0 + 64 * i, p.t0 + tok);
+          else tma2_load_3d(res + c * M::RES_CHUNK + i * HCHUNK, map, full, 64 * c, h0 + 64 * i, p.t0 + tok);
         }
-        ++n;
+      };
+      for (int c0 = 0; c0 < DCH && ok; c0 += 3) {
+        bool got = true;
+        if (lane < 3) {
+          got = mbar_wait(cta.bar(B_RES_EMPTY + c0 + lane), (n & 1) ^ 1, abort_flag);
+          if (got) rows(c0 + lane, t, false);
+        }
+        ok = __all_sync(0xffffffffu, got);
       }
+      if (item + stride < items && token(item + stride) != t && lane < DCH) rows(lane, token(item + stride), true);
+      __syncwarp();
+      ++n;
     }
   } else if (warp == 2 || warp == 3 || (warp >= 8 && warp < 14)) {
     // ===================================================================== gathers (gather4: four rows x 64 dims)
     // One lane issues one gather4 of a stage; the warps that fill a stage share its 32 SC of them, and stages go round
     // the groups of such warps.  The entries of the next tile are read while this one is gathered.
-    // An empty or invalid slot reads row `slot` (any row would do: its P and dS are set to zero).
+    // An empty or invalid slot reads row slot % S (any row would do, its P and dS are set to zero; one row for all would be
+    // one L2 line for the whole GPU: 30 us against 18 for 96 short tokens); a CTA whose keys of a tile are all behind the
+    // token's last entry reads nothing.
     constexpr int PER = SC * 32 / M::WPS, GROUPS = 8 / M::WPS;
     const int gw = (warp < 8) ? warp - 2 : warp - 6;
     const int grp = gw / M::WPS, gi = (gw % M::WPS) * PER + lane, cc = gi / 32, rg = gi % 32;
@@ -355,6 +370,7 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const TileSpan sp = span(item);
       if (sp.j0 >= sp.j1) continue;
       const int* ids = p.idx + static_cast<long long>(token(item)) * p.k;
+      const int n_end = p.n_end[token(item)];
       auto entries = [&](int j) {          // k is a multiple of 64, a lane's four slots lie on one side of it
         const int slot = (2 * j + rank) * NK + 4 * rg;
         return slot < p.k ? __ldg(reinterpret_cast<const int4*>(ids + slot)) : make_int4(-1, -1, -1, -1);
@@ -363,8 +379,9 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       for (int j = sp.j0; j < sp.j1 && ok; ++j, m += SPT) {
         const int slot = (2 * j + rank) * NK + 4 * rg;
         auto row = [&](int x, int i) {
-          return (x >= 0 && x < p.S) ? x : static_cast<int>(slot + i < p.S ? slot + i : 0);
+          return (x >= 0 && x < p.S) ? x : static_cast<int>(slot + i < p.S ? slot + i : (slot + i) % p.S);
         };
+        const bool any = (2 * j + rank) * NK < n_end;
         const int r0 = row(e.x, 0), r1 = row(e.y, 1), r2 = row(e.z, 2), r3 = row(e.w, 3);
         if (j + 1 < sp.j1) e = entries(j + 1);
         for (int s = (grp + (GROUPS - 1) * m) % GROUPS; s < SPT; s += GROUPS) {   // (m + s) % GROUPS == grp
@@ -373,10 +390,11 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           bool got = true;
           if (lane == 0) {
             got = mbar_wait(cta.bar(B_RING_EMPTY + st), (((m + s) / NS) & 1) ^ 1, abort_flag);
-            if (got) mbar_arrive_expect_tx_remote(full, PER * 512);
+            if (got && any) mbar_arrive_expect_tx_remote(full, PER * 512);
+            else if (got) mbar_arrive_remote(full);
           }
           if (!(ok = __shfl_sync(0xffffffffu, got, 0))) break;
-          if (active)
+          if (active && any)
             tma2_gather4(ring + (st * SC + cc) * CHUNK + rg * 512, &tm_c, full, 64 * (s * SC + cc), r0, r1, r2, r3);
         }
       }
@@ -643,25 +661,24 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
 
   if (warp == 0) {
     // ===================================================================== resident q and dout
-    if (lane == 0) {
-      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        int t, d3;
-        const TileSpan sp = part(item, t, d3);
-        if (sp.j0 >= sp.j1) continue;
-        for (int u = 0; u < units; ++u) {
-          if (!(ok = mbar_wait(cta.bar(B_RES_EMPTY + u), (n & 1) ^ 1, abort_flag))) break;
-          const int boxes = (u >= hb && d3 == 2) ? 2 : 3;          // dout ends at dim 512
-          const uint32_t full = cta.bar(B_RES_FULL + u);
-          mbar_arrive_expect_tx(full, boxes * HCHUNK);
-          for (int i = 0; i < boxes; ++i)
-            tma_load_3d(res + u * UNIT + i * HCHUNK, u < hb ? &tm_q : &tm_do, full, 192 * d3 + 64 * i, 64 * (u % hb),
-                        p.t0 + t);
-        }
-        ++n;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      int t, d3;
+      const TileSpan sp = part(item, t, d3);
+      if (sp.j0 >= sp.j1) continue;
+      for (int u = 0; u < units; ++u) {                  // a box of 64 dims a lane
+        const int boxes = (u >= hb && d3 == 2) ? 2 : 3;  // dout ends at dim 512
+        const uint32_t full = cta.bar(B_RES_FULL + u);
+        if (!(ok = warp_wait(cta.bar(B_RES_EMPTY + u), (n & 1) ^ 1, abort_flag))) break;
+        if (lane == 0) mbar_arrive_expect_tx(full, boxes * HCHUNK);
+        __syncwarp();
+        if (lane < boxes)
+          tma_load_3d(res + u * UNIT + lane * HCHUNK, u < hb ? &tm_q : &tm_do, full, 192 * d3 + 64 * lane,
+                      64 * (u % hb), p.t0 + t);
       }
-      if (*abort_flag && n > 0)
-        for (int u = 0; u < units; ++u) mbar_wait_drain(cta.bar(B_RES_FULL + u), (n - 1) & 1);
+      ++n;
     }
+    if (lane == 0 && *abort_flag && n > 0)
+      for (int u = 0; u < units; ++u) mbar_wait_drain(cta.bar(B_RES_FULL + u), (n - 1) & 1);
   } else if (warp == 2) {
     // ===================================================================== dS and P tiles
     if (lane == 0) {
