@@ -2,14 +2,14 @@
 //
 // I[t,i] = sum_j w_j relu(q_j . k_s), s = idx[t][i], q_j = qs_t q_idx[t][j] and k_s = ks_s k_idx[s] the dequantised
 // operands.  With the gradient e = dsel[t][i], x = q_idx[t][j] . k_idx[s] and the live pairs 1[x > 0]:
-//   dw_j = qs sum_i e ks relu(x)       dq_j = sum_i (e w_j 1[x > 0] ks) k_idx[s]       dk_s = sum_(t,i) qs sum_j G q_idx[j]
-// with G = e w_j 1[x > 0]: three products of 2 x 64 heads x 128 dims per entry.  dq and dk are gradients of the
+//   dw_j = qs sum_i e ks relu(x)       dq_j = sum_i (e w_j 1[x > 0] ks) k_idx[s]       dk_s = sum_(t,i) sum_j (G qs) q_idx[j]
+// with G = e w_j 1[x > 0]: three products of 2 x 64 heads x 128 dims per entry (G qs and G ks are what is stored).  dq and dk are gradients of the
 // dequantised values (what a straight-through quantiser passes on).
 //
 // One CTA per token (or per split of a token's tiles, where tokens are few), keys are the M dimension.  e4m3 rows are gathered with plain 16-byte loads and written as bf16
 // (exact) in the swizzled form the tensor core reads, so the one copy serves x (K-major), dq (transposed, MN-major)
 // and, for q, dk; kind::f16 needs both operands bf16 and G is.  x is exact: products of e4m3 are, and their sum is
-// held in fp32.  G and G ks are rounded to bf16 once (2^-9).  dw is summed from the fp32 x.  Per token: 16 tiles of
+// held in fp32.  G qs and G ks are rounded to bf16 once (2^-9).  dw is summed from the fp32 x.  Per token: 16 tiles of
 // 128 keys, each x -> G -> (dk, dq); x of the next tile is issued before G of this one is waited for.
 // HBM sees each entry's contribution to dk twice (written here, summed by scatter.cuh).
 // The small indexer (4 heads, 64 dims) runs in the same layout, its missing heads and dims zero.
@@ -46,7 +46,7 @@ constexpr int B_X_FULL = 12, B_X_EMPTY = 14, B_G_FULL = 16, B_G_EMPTY = 18, B_DK
 constexpr int B_DQ_FULL = 24, B_DQ_EMPTY = 26;
 constexpr int OFF_W = 1024, OFF_DW = OFF_W + 512;            // w of the token (2 buffers), dw of the eight warps
 constexpr int OFF_IDX = 4096, OFF_Q = OFF_IDX + 2 * mla::KMAX * 4, OFF_K = OFF_Q + 2 * Q_BYTES;
-constexpr int OFF_G = OFF_K + 2 * K_BYTES;                   // 2 x (G, G ks)
+constexpr int OFF_G = OFF_K + 2 * K_BYTES;                   // 2 x (G qs, G ks)
 constexpr int OFF_OUT = OFF_G + 4 * G_BYTES;
 constexpr int SMEM = OFF_OUT + 2 * KCH + 1024;
 constexpr uint32_t TX = 0, TDK = 128, TDQ = 384;             // x 2 x 64, dk 2 x 128, dq 2 x 64 columns
@@ -257,7 +257,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
       step(b);
     }
   } else if (warp < 8 || warp >= 18) {
-    // ===================================================================== G, G ks and dw (one key a thread)
+    // ===================================================================== G qs, G ks and dw (one key a thread)
     // Two groups of four warps take tiles in turn (one group alone: 707 us for 2048 tokens, against XXX).  The entry of
     // a thread's next tile but one, and the gradient and key scale of its next tile, are on their way meanwhile.
     const int grp = warp >= 18 ? 1 : 0;
@@ -279,6 +279,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
       float* ws = reinterpret_cast<float*>(cta.smem + OFF_W) + 64 * (n & 1);
       if (grp == 0 && row < 64) ws[row] = row < HI ? p.w[static_cast<long long>(t) * HI + row] : 0.f;
       const long long base = static_cast<long long>(t) * p.k;
+      const float qs = p.q_scale ? p.q_scale[t] : 1.f;
       auto entry = [&](int j) {
         const int slot = j * NK + row;
         const int id = j < sp.j1 && slot < p.k ? __ldg(p.idx + base + slot) : -1;
@@ -300,7 +301,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
         if (!ok) break;
         tc_fence_after();
         uint8_t* gl = cta.smem + OFF_G + 2 * s * G_BYTES + row * 128;
-        const float eks = e * ks;
+        const float eks = e * ks, eqs = e * qs;
 #pragma unroll
         for (int c = 0; c < BLOCKS; ++c) {
           uint32_t v[16];
@@ -322,13 +323,13 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
             for (int q = 0; q < 4; ++q) {
               const float xv = __uint_as_float(v[i + q]);
               const bool live = xv > 0.f;
-              gv[q] = live ? e * wv[q] : 0.f;
+              gv[q] = live ? wv[q] : 0.f;
               x[i + q] = live ? eks * xv : 0.f;
             }
-            a[i / 2] = pack_bf16(gv[0], gv[1]);
-            a[i / 2 + 1] = pack_bf16(gv[2], gv[3]);
-            b[i / 2] = pack_bf16(gv[0] * ks, gv[1] * ks);
-            b[i / 2 + 1] = pack_bf16(gv[2] * ks, gv[3] * ks);
+            a[i / 2] = pack_bf16(eqs * gv[0], eqs * gv[1]);
+            a[i / 2 + 1] = pack_bf16(eqs * gv[2], eqs * gv[3]);
+            b[i / 2] = pack_bf16(eks * gv[0], eks * gv[1]);
+            b[i / 2 + 1] = pack_bf16(eks * gv[2], eks * gv[3]);
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -369,7 +370,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) sum += dw_s[64 * w + row];
-        dw_out[row] = sum * (p.q_scale ? p.q_scale[t] : 1.f);
+        dw_out[row] = sum * qs;
       }
       // the next token's first barrier comes before anyone writes dw_s again
       ++n;
@@ -388,7 +389,6 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
         for (int i = row; i < HI * DI / 8; i += 128) reinterpret_cast<uint4*>(dq)[i] = make_uint4(0, 0, 0, 0);
         continue;
       }
-      const float qs = p.q_scale ? p.q_scale[t] : 1.f;
       for (int j = sp.j0; j < sp.j1; ++j, ++g) {
         const int s = g & 1;
         if (!(ok = warp_wait(cta.bar(B_DK_FULL + s), (g >> 1) & 1, abort_flag))) break;
@@ -408,13 +408,12 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
           __syncwarp();
           if (c == DI / 64 - 1 && lane == 0) mbar_arrive(cta.bar(B_DK_EMPTY + s));
           uint8_t* line = cta.smem + OFF_OUT + c * KCH + row * 128;
+          uint32_t w[32];
+          scatter_pack64(v, w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            auto pk = [&](int q) {
-              return pack_bf16(__uint_as_float(v[8 * i + 2 * q]) * qs, __uint_as_float(v[8 * i + 2 * q + 1]) * qs);
-            };
-            *reinterpret_cast<uint4*>(line + ((i ^ (row & 7)) << 4)) = make_uint4(pk(0), pk(1), pk(2), pk(3));
-          }
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(line + ((i ^ (row & 7)) << 4)) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {

@@ -1,12 +1,18 @@
 // Sums of per-entry contributions into the rows they belong to: out[s] = sum over tokens t and slots i with
 // idx[t][i] = s of contrib[t][i], in a fixed order.
 //
-// The backward passes write one bf16 row per selected entry (a chunk of tokens at a time).  A table of the chunk,
+// The backward passes write one row of 16-bit values per selected entry (a chunk of tokens at a time): fp16 with a
+// power-of-two scale for each 64, whose exponent sits in the lowest bits of every eight.  A value is rounded by less than
+// 2^-9 of itself in the worst case and 2^-12 on average (2^-38 of the largest of its 64, where it is smaller than 2^-28 of
+// that), over the whole range of fp32.  bf16 rows, no longer, would round four times as much: as much as the
+// operands that made them, and gradients would be 1.7 steps of their own rounding off instead of 1.4.  A table of the chunk,
 // slot[s][t] = the slot in which token t selected row s (16 bits, empty: 0xffff), turns the scatter into a gather:
 // one CTA per row s lists the row's entries in token order and adds them up.  Every sum has one order whatever the
 // kernels' timing, so results repeat bit for bit; with atomics they would not.  Bound by HBM: each contribution is
 // read once (2 W bytes), the table once (2 bytes per row and token).
 #pragma once
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace dsa {
@@ -24,6 +30,49 @@ __device__ __forceinline__ void scatter_clear(uint4* table, long long n) {
   for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step)
     table[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
 }
+// 64 values as pieces of eight: fp16 of x 2^(141 - E), E the exponent of the largest magnitude of the 64 (kept where
+// 2^(141 - E) and its inverse are normal), bit i of E in the lowest bit of a piece's value 2 i, bit i + 4 in that of value
+// 2 i + 1.  E = 0: 64 values with infinities among them, unscaled.
+__device__ __forceinline__ void scatter_pack64(const uint32_t (&v)[64], uint32_t (&w)[32]) {
+  float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 64; i += 2)
+    top[(i >> 1) & 3] = fmaxf(fmaxf(top[(i >> 1) & 3], fabsf(__uint_as_float(v[i]))), fabsf(__uint_as_float(v[i + 1])));
+  const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  uint32_t e = max(15u, __float_as_uint(most) >> 23);
+  float f = __uint_as_float((268u - e) << 23);
+  if (e > 254u) {
+    e = 0;
+    f = 1.f;
+  }
+  const uint32_t bits = e | (e << 12);
+  const uint32_t b4[4] = {bits & 0x00010001u, (bits >> 1) & 0x00010001u, (bits >> 2) & 0x00010001u,
+                          (bits >> 3) & 0x00010001u};
+  const uint64_t ff = pack_f32x2(f, f);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    float lo, hi;
+    unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ff), lo, hi);
+    const __half2 h = __floats2half2_rn(lo, hi);
+    w[i] = (*reinterpret_cast<const uint32_t*>(&h) & 0xfffefffeu) | b4[i & 3];
+  }
+}
+// sum += the piece's values
+__device__ __forceinline__ void scatter_add(uint4 v, float (&sum)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const uint32_t t = (w[0] & 0x00010001u) | ((w[1] & 0x00010001u) << 1) | ((w[2] & 0x00010001u) << 2) |
+                     ((w[3] & 0x00010001u) << 3);
+  const uint32_t e = (t | (t >> 12)) & 0xffu;
+  const float f = e ? __uint_as_float((e - 14u) << 23) : 1.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = w[i] & 0xfffefffeu;
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x));
+    sum[2 * i] = fmaf(y.x, f, sum[2 * i]);
+    sum[2 * i + 1] = fmaf(y.y, f, sum[2 * i + 1]);
+  }
+}
+
 __global__ void __launch_bounds__(256) scatter_clear_kernel(uint4* table, long long n) {
   pdl_allow_next();
   pdl_wait();
@@ -99,7 +148,7 @@ __global__ void __launch_bounds__(256) scatter_build_kernel(const int* idx, int 
 }
 
 struct ScatterParams {
-  const uint16_t* contrib;    // [T * kp, W] bf16
+  const uint16_t* contrib;    // [T * kp, W] in pieces of eight (scatter_pack64)
   const uint16_t* table;      // [S, ld]
   const int* idx;             // [T, k]
   int T, ld, k, kp;
@@ -170,14 +219,6 @@ __global__ void __launch_bounds__(ScatterCfg<W>::THREADS, 6) scatter_sum_kernel(
   auto read = [&](uint32_t t, int slot) {
     return __ldcs(reinterpret_cast<const uint4*>(p.contrib + (static_cast<long long>(t) * p.kp + slot) * W) + col);
   };
-  auto add = [&](uint4 v) {
-    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      sum[2 * q] += __uint_as_float(x[q] << 16);
-      sum[2 * q + 1] += __uint_as_float(x[q] & 0xffff0000u);
-    }
-  };
   const int each = (n + C::GROUPS - 1) / C::GROUPS, end = min(n, (group + 1) * each);
   for (int i = group * each; i < end; i += 8) {
     uint4 v[8];
@@ -189,7 +230,7 @@ __global__ void __launch_bounds__(ScatterCfg<W>::THREADS, 6) scatter_sum_kernel(
       v[u] = i + u < end ? read((e >> 11) & 0xfffff, e & (sct::TWICE - 1)) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) add(v[u]);
+    for (int u = 0; u < 8; ++u) scatter_add(v[u], sum);
     if (any >> 31) {                     // the row's later slots of a token that selected it more than once
 #pragma unroll 1
       for (int u = i; u < min(end, i + 8); ++u) {
@@ -198,7 +239,7 @@ __global__ void __launch_bounds__(ScatterCfg<W>::THREADS, 6) scatter_sum_kernel(
         const int* ids = p.idx + static_cast<long long>(t) * p.k;
 #pragma unroll 1
         for (int j = (e & (sct::TWICE - 1)) + 1; j < p.k; ++j)
-          if (ids[j] == s) add(read(t, j));
+          if (ids[j] == s) scatter_add(read(t, j), sum);
       }
     }
   }
@@ -227,13 +268,16 @@ __global__ void __launch_bounds__(ScatterCfg<W>::THREADS, 6) scatter_sum_kernel(
   }
 }
 
-// The same for short lists: one warp per row, 32-bit loads (a warp reads a contribution in W / 64 of them), four rows in
-// flight, nothing shared between warps.  With few entries a row the time is the chain table -> entries -> result, which
-// eight rows a CTA walk at once here.
+// The same for short lists: one warp per row, nothing shared between warps.  W >= 256: the warp reads an entry's pieces in
+// W / 256 rounds of loads, four entries in flight; less: 256 / W entries at once, one to each part of the warp, whose sums
+// are joined at the end.  With few entries a row the time is the chain table -> entries -> result, which eight rows a CTA
+// walk at once here (20 tokens over 20020 rows, W = 576: 16 us against 58).
 constexpr int kSumWarps = 8;
 template <int W>
 __global__ void __launch_bounds__(32 * kSumWarps) scatter_sum_short_kernel(const ScatterParams p, long long S) {
-  constexpr int V = W / 64;                // 32-bit words of a lane
+  constexpr int PIECES = W / 8;
+  constexpr int PARTS = PIECES < 32 ? 32 / PIECES : 1;       // entries at once
+  constexpr int L = (PIECES + 31) / 32;                      // pieces of a lane
   __shared__ uint32_t lists[kSumWarps][256];
   pdl_allow_next();
   pdl_wait();
@@ -242,18 +286,13 @@ __global__ void __launch_bounds__(32 * kSumWarps) scatter_sum_short_kernel(const
   if (s >= S) return;
   uint32_t* list = lists[warp];
   const uint4* row = reinterpret_cast<const uint4*>(p.table + s * p.ld);
-  float sum[2 * V] = {};
-  auto read = [&](uint32_t t, int slot, uint32_t (&v)[V]) {
-    const uint32_t* at = reinterpret_cast<const uint32_t*>(p.contrib + (static_cast<long long>(t) * p.kp + slot) * W);
+  const int part = PARTS > 1 ? lane / PIECES : 0, col = PARTS > 1 ? lane % PIECES : lane;
+  float sum[L][8] = {};
+  auto read = [&](uint32_t t, int slot, uint4 (&v)[L]) {
+    const uint4* at = reinterpret_cast<const uint4*>(p.contrib + (static_cast<long long>(t) * p.kp + slot) * W);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = __ldcs(at + 32 * i + lane);
-  };
-  auto add = [&](const uint32_t (&v)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      sum[2 * i] += __uint_as_float(v[i] << 16);
-      sum[2 * i + 1] += __uint_as_float(v[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < L; ++i)
+      v[i] = col + 32 * i < PIECES ? __ldcs(at + col + 32 * i) : make_uint4(0, 0, 0, 0);
   };
   for (int q0 = 0; q0 < p.ld / 8; q0 += 32) {
     // 256 tokens: eight a lane, listed in token order
@@ -277,33 +316,36 @@ __global__ void __launch_bounds__(32 * kSumWarps) scatter_sum_short_kernel(const
         list[to++] = (static_cast<uint32_t>(8 * (q0 + lane) + u) << 11) | (v & (sct::TWICE - 1)) | ((v & sct::TWICE) << 20);
     }
     __syncwarp();
-    for (int i = 0; i < n; i += 4) {
-      uint32_t v[4][V];
+    for (int i = part; i < n; i += 4 * PARTS) {
+      uint4 v[4][L];
       uint32_t any = 0;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const uint32_t e = i + u < n ? list[i + u] : 0;
+        const uint32_t e = i + u * PARTS < n ? list[i + u * PARTS] : 0;
         any |= e;
-        if (i + u < n) {
+        if (i + u * PARTS < n) {
           read((e >> 11) & 0xfffff, e & (sct::TWICE - 1), v[u]);
         } else {
 #pragma unroll
-          for (int j = 0; j < V; ++j) v[u][j] = 0;
+          for (int j = 0; j < L; ++j) v[u][j] = make_uint4(0, 0, 0, 0);
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) add(v[u]);
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int j = 0; j < L; ++j) scatter_add(v[u][j], sum[j]);
       if (any >> 31) {                     // the row's later slots of a token that selected it more than once
 #pragma unroll 1
-        for (int u = i; u < min(n, i + 4); ++u) {
-          const uint32_t e = list[u], t = (e >> 11) & 0xfffff;
+        for (int u = 0; u < 4 && i + u * PARTS < n; ++u) {
+          const uint32_t e = list[i + u * PARTS], t = (e >> 11) & 0xfffff;
           if (!(e >> 31)) continue;
           const int* ids = p.idx + static_cast<long long>(t) * p.k;
 #pragma unroll 1
           for (int j = (e & (sct::TWICE - 1)) + 1; j < p.k; ++j)
             if (ids[j] == s) {
               read(t, j, v[0]);
-              add(v[0]);
+#pragma unroll
+              for (int x = 0; x < L; ++x) scatter_add(v[0][x], sum[x]);
             }
         }
       }
@@ -311,19 +353,34 @@ __global__ void __launch_bounds__(32 * kSumWarps) scatter_sum_short_kernel(const
     __syncwarp();
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const long long at = s * (W / 2) + 32 * i + lane;    // in pairs of values
-    float2 total = make_float2(sum[2 * i], sum[2 * i + 1]);
+  for (int d = PIECES; d < 32; d *= 2)     // the parts' sums
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum[0][q] += __shfl_xor_sync(0xffffffffu, sum[0][q], d);
+  if (part != 0) return;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    if (col + 32 * i >= PIECES) break;
+    const long long at = s * W + 8 * (col + 32 * i);
+    float* x = sum[i];
     if (p.acc && !p.first) {
-      const float2 v = reinterpret_cast<const float2*>(p.acc)[at];
-      total.x += v.x;
-      total.y += v.y;
+#pragma unroll
+      for (int q = 0; q < 8; q += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p.acc + at + q);
+        x[q] += v.x; x[q + 1] += v.y; x[q + 2] += v.z; x[q + 3] += v.w;
+      }
     }
     if (p.last) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(total.x, total.y);
-      reinterpret_cast<uint32_t*>(p.out)[at] = *reinterpret_cast<const uint32_t*>(&b);
+      uint32_t b[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * q], x[2 * q + 1]);
+        b[q] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(p.out + at) = make_uint4(b[0], b[1], b[2], b[3]);
     } else {
-      reinterpret_cast<float2*>(p.acc)[at] = total;
+#pragma unroll
+      for (int q = 0; q < 8; q += 4)
+        *reinterpret_cast<float4*>(p.acc + at + q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
     }
   }
 }

@@ -14,15 +14,14 @@
 //   mla_bwd_p_kernel   (token, 64 heads): keys are the M dimension; q and dout rows of the 64 heads, stacked to
 //                      N = 128, stay in shared memory; every gathered chunk of 128 keys x 64 dims meets both at once;
 //   mla_bwd_dc_kernel  (token, 192 dims): [dS | P] (128 keys x heads) times [q ; dout] (heads x 192 dims), resident;
-//                      writes each entry's own contribution to dc (bf16);
+//                      writes each entry's own contribution to dc (16 bits a value, see scatter.cuh);
 //   mla_bwd_dq_kernel  (token, 192 dims): dS^T (heads x keys) times the gathered keys (keys x 192 dims), accumulated
 //                      over the token's keys in tensor memory.
 // A last kernel (scatter.cuh) sums the contributions of each row of c in token order: the result does not depend on
 // the order of execution, which atomics would not give.
 //
-// P, dS and the contributions are rounded to bf16, each by at most 2^-9 of its value: the operands of the second
-// products have to be bf16, and a sum of independently rounded contributions is off by no more than one of them is,
-// relative to the sum of their sizes (half the bf16 step that the results are rounded to anyway).  All sums are fp32.
+// P and dS are rounded to bf16, by at most 2^-9 of their value, as the operands of the second products have to be.  All
+// sums are fp32.
 #pragma once
 #include "common.cuh"
 #include "scatter.cuh"
@@ -37,7 +36,7 @@ struct MlaBwdParams {
   const float* lse;            // [T, H]
   const float* delta;          // [T, H]
   uint16_t* pds;               // [T * kp, 2 HP] bf16: dS of HP heads, then P of HP heads, for every slot
-  uint16_t* contrib;           // [T * kp, 576] bf16: each entry's contribution to dc
+  uint16_t* contrib;           // [T * kp, 576]: each entry's contribution to dc (scatter_pack64)
   uint16_t* dq;                // [T, H, 576]
   float* dq_part;              // splits > 1: [T * splits, H, 576] sums of each split
   int T, t0;                   // tokens of the chunk; the first one's index in q and dout
@@ -765,8 +764,7 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(cta.bar(B_ACC_EMPTY + ab));
           }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] = pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+          scatter_pack64(v, w);
           store_rows<8>(cta.smem + OFF_TURN + (4 * grp + quad) * 4096, w, out + 64 * c, 2 * D);
         }
       }
