@@ -154,9 +154,9 @@ DSA_API size_t dsa_sparse_mla_attn_backward_workspace_size(int T, int S, int H, 
  *     a caller that accumulates adds them itself.  The selection and lse pass no gradient on.
  * A row of c selected twice by a token counts twice, as in the forward.  A token without entries (lse = -INFINITY)
  * has dq = 0.  An entry outside [-1, S) is treated as -1 and recorded as DSA_ERR_BAD_INDEX.
- * P, dS and each entry's contribution to dc are rounded to bf16 once; every sum is fp32.
+ * P and dS are rounded to bf16 once, each entry's contribution to dc to about 11 bits; every sum is fp32.
  *   ws: dsa_sparse_mla_attn_backward_workspace_size() bytes, 16-byte aligned.  Long T are worked through in chunks of
- *     tokens (about 2 GiB of workspace).
+ *     tokens (about 4 GiB of workspace and, with more than one, an fp32 copy of dc).
  */
 DSA_API dsa_status_t dsa_sparse_mla_attn_backward(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx,
                                                   const uint16_t* out, const float* lse, const uint16_t* dout, int T,
@@ -210,7 +210,8 @@ DSA_API size_t dsa_indexer_scores_backward_workspace_size(int T, int S, int H_I,
  *     where idx is -1), as dsa_indexer_kl_backward writes it;
  *   dq [T, H_I, d_I] bf16, dk [S, d_I] bf16, dw [T, H_I] fp32 (out); every row is written.
  * k as in dsa_sparse_mla_attn; entries outside [-1, S) count as -1 and are recorded as DSA_ERR_BAD_INDEX.  The weights
- * dsel w_j (and their product with k_scale) and each entry's contribution to dk are rounded to bf16 once; sums are fp32.
+ * dsel w_j q_scale and dsel w_j k_scale are rounded to bf16 once, each entry's contribution to dk to about 11 bits; sums
+ * are fp32, and dw is computed in fp32 throughout.
  *   ws: dsa_indexer_scores_backward_workspace_size() bytes, 16-byte aligned.
  */
 DSA_API dsa_status_t dsa_indexer_scores_backward(const uint8_t* q_idx, const float* q_scale, const uint8_t* k_idx,
@@ -243,7 +244,7 @@ DSA_API dsa_status_t dsa_rope_frequencies(int rot_dim, double base, double facto
  *     x itself (same strides: only the rotated dims are touched) and may otherwise share no element with it
  *     (DSA_ERR_INVALID_ARG).
  *   positions [T] int32 (device), or NULL: token t is at position pos0 + t.  inv_freq [rot_dim / 2] fp64 (DEVICE).
- * Angles are formed in fp64.  Pieces of 16 bytes are moved where pointers, strides and offsets allow, single elements
+ * Angles are exact to 2^-32 turns at any position.  At most 2^30 tokens and 2^18 heads a call.  Pieces of 16 bytes are moved where pointers, strides and offsets allow, single elements
  * otherwise.  Needs no workspace.
  */
 DSA_API dsa_status_t dsa_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, void* out, int64_t out_stride_t,

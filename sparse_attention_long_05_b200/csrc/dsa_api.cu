@@ -951,8 +951,8 @@ dsa_status_t launch_rope(RopeParams p, bool vec, bool inter, cudaStream_t st) {
   // one set of angles); more tokens than that go round the same threads, in equal shares
   const long long one = static_cast<long long>(p.T) * (p.rot_units + p.copy_units) * p.H, resident = 2048ll * num_sms();
   p.heads_per = static_cast<int>(std::min<long long>(std::min(8, p.H), std::max<long long>(1, one / resident)));
+  if (p.H > 65535 * p.heads_per) p.heads_per = 8;       // blockIdx.y counts the groups
   const int groups = (p.H + p.heads_per - 1) / p.heads_per;
-  if (groups > 65535) return DSA_ERR_UNSUPPORTED_SHAPE;
   const int bx = std::min(256, p.rot_units), by = 256 / bx;
   const long long blocks = (static_cast<long long>(p.T) + by - 1) / by;
   const long long most = std::max<long long>(1, 2 * resident / 256 / groups);
@@ -980,6 +980,7 @@ dsa_status_t run_rope(const void* x, int64_t x_st, int64_t x_sh, void* out, int6
       (T > 0 && (!x || !out || !inv_freq)) || x_st < 0 || x_sh < 0 || (dtype != DSA_BF16 && dtype != DSA_FP32))
     return DSA_ERR_INVALID_ARG;
   if (T == 0) return DSA_OK;
+  if (T > (1 << 30) || H > (1 << 18)) return DSA_ERR_UNSUPPORTED_SHAPE;
   if (!positions && pos0 > INT32_MAX - (T - 1)) return DSA_ERR_INVALID_ARG;
   const int es = dtype == DSA_BF16 ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(x) % es || reinterpret_cast<uintptr_t>(out) % es ||

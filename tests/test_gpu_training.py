@@ -2,11 +2,10 @@
 backward pass, the gradient of the indexer's objective, the backward pass of the index scores, and a run of them
 together.
 
-Tolerances.  u = 2^-9 bounds bf16's rounding of a value on average over its mantissas and 2^-8 in the worst case
-(half a step).  A bf16 gradient is a sum of products whose factors were rounded at most twice (an operand of the
-product and the entry's contribution) plus its own rounding: each element is within 3 x 2^-8 of the sum of the
-products' sizes, taken here as a bound on the elements, and the relative L2 error of independent roundings stays below
-2^-8 (three of them of rms 2^-8 / sqrt(12) x sqrt(2) make 0.0033 at most; 2^-8 is 0.0039).  fp32 results that are sums
+Tolerances.  bf16 rounds a value by at most 2^-9 to 2^-8 of itself (half a step), by 2^-8 / sqrt(12) x sqrt(2) rms at
+most.  A bf16 gradient is a sum of products whose factors were rounded at most twice (an operand of the product and the
+entry's contribution, to bf16 or finer) plus its own rounding: the relative L2 error of three independent roundings
+stays below 2^-8 (they make 0.0033 at most; 2^-8 is 0.0039).  fp32 results that are sums
 of n fp32 terms with logits off by 2^-20 stay within 1e-5 in relative L2."""
 import math
 
@@ -102,6 +101,7 @@ def _run_attention(dsa, q, c, idx, dout, **kw):
     return out, lse, dq, dc
 
 
+# the sums of a chunk's rows take two ways, by the mean length of their lists (16): both occur among these
 CASES = [(1, 1, 1, 128, "causal"), (1, 300, 128, 128, "causal"), (3, 130, 8, 192, "causal"), (5, 700, 64, 320, "holes"),
          (9, 200, 65, 128, "twice"), (8, 150, 37, 128, "blank"), (4, 50, 128, 256, "one"), (17, 2300, 128, 2048, "causal"),
          (160, 161, 16, 128, "causal"), (6, 900, 128, 576, "holes")]
@@ -193,6 +193,39 @@ def test_attention_backward_nan_rows_nobody_selects(dsa):
     out, lse = (t.cuda() for t in (clean[0].cpu(), clean[1].cpu()))
     dq, dc = dsa.dsa_sparse_mla_attn_backward(q2.cuda(), c2.cuda(), idx.cuda(), out, lse, dout.cuda(), SCALE)
     assert torch.equal(dq, clean[2]) and torch.equal(dc, clean[3])
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -40, 2.0 ** 60, 2.0 ** 100])
+def test_gradients_scale_with_their_input(dsa, size):
+    # a power of two moves through every rounding of the pass: P is the same, all else scales exactly
+    q, c, idx, dout = _attention_case(5, 300, 24, 192, "holes", 4)
+    out, lse, dq, dc = _run_attention(dsa, q, c, idx, dout)
+    dq2, dc2 = dsa.dsa_sparse_mla_attn_backward(q.cuda(), c.cuda(), idx.cuda(), out, lse, (dout * size).cuda(), SCALE)
+    assert torch.equal(dq2.double(), dq.double() * size) and torch.equal(dc2.double(), dc.double() * size)
+    qi, qs, kk, ks, w, idx, dsel = _indexer_case(5, 300, 64, 128, 192, "holes", True, 6)
+    dev = [t.cuda() for t in (qi, qs, kk, ks, w, idx)]
+    a = dsa.dsa_indexer_scores_backward(*dev, dsel.cuda())
+    b = dsa.dsa_indexer_scores_backward(*dev, (dsel * size).cuda())
+    # G q_scale and G k_scale are bf16 operands, whose subnormals the tensor cores may take as zero: each is then off by at
+    # most 2^-126, and an element of dq or dk by that times 448 (the largest e4m3) for each of at most 64 x 192 terms.
+    # Only the smallest size meets this: there the rms of G k_scale is 2^-100 x 2^-7.6 (dsel) x 2^-6.9 (k_scale) x 2^-3 (w) =
+    # 2^-117.5, against which 2^-126 is 2^-8.5 in relative L2.
+    for x, y in zip(a, b):
+        assert ((y.double() - x.double() * size).abs() <= 64 * 192 * 448 * 2.0 ** -126).all()
+        assert _rel(y.double() / size, x) <= L2_BF16
+
+
+def test_infinite_gradients_reach_what_they_touch(dsa):
+    q, c, idx, dout = _attention_case(4, 300, 16, 128, "causal", 13)
+    out, lse, dq, dc = _run_attention(dsa, q, c, idx, dout)
+    dout[1, 3, 7] = math.inf
+    dq2, dc2 = dsa.dsa_sparse_mla_attn_backward(q.cuda(), c.cuda(), idx.cuda(), out, lse, dout.cuda(), SCALE)
+    hit = torch.zeros(300, dtype=torch.bool)
+    hit[idx[1].long()] = True
+    assert not torch.isfinite(dc2.cpu()[hit]).all(1).any() and torch.equal(dc2.cpu()[~hit], dc.cpu()[~hit])
+    same = torch.ones(4, 16, dtype=torch.bool)
+    same[1, 3] = False
+    assert torch.equal(dq2.cpu()[same], dq.cpu()[same]) and not torch.isfinite(dq2.cpu()[1, 3]).any()
 
 
 def test_bad_indices_are_recorded_and_skipped(dsa):
