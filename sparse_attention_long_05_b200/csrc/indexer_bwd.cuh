@@ -302,7 +302,9 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
         tc_fence_after();
         uint8_t* gl = cta.smem + OFF_G + 2 * s * G_BYTES + row * 128;
         const float eks = e * ks, eqs = e * qs;
-#pragma unroll
+        // not unrolled (nor are the loops over 64 dims below): the roles' code together has to stay in the instruction cache,
+        // fetches from behind it were a sixth of all stalls (680 us for 2048 tokens, against XXX)
+#pragma unroll 1
         for (int c = 0; c < BLOCKS; ++c) {
           uint32_t v[16];
           tmem_ld16(lane_addr + tmem + TX + 64 * s + 16 * c, v);
@@ -352,7 +354,9 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
           DSA_IXB_HALVE(2)
           DSA_IXB_HALVE(1)
 #undef DSA_IXB_HALVE
-          dw[c] += x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
+          const float sum = x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
+#pragma unroll
+          for (int i = 0; i < BLOCKS; ++i) dw[i] += i == c ? sum : 0.f;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -393,7 +397,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
         const int s = g & 1;
         if (!(ok = warp_wait(cta.bar(B_DK_FULL + s), (g >> 1) & 1, abort_flag))) break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < DI / 64; ++c) {
           // each warp stages and stores its own 32 rows, 64 dims at a time
           uint32_t v[64];

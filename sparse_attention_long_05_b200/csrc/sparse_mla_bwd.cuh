@@ -753,7 +753,7 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
         if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), ((g + j - sp.j0) >> 1) & 1, abort_flag))) break;
         tc_fence_after();
         uint16_t* out = p.contrib + (static_cast<long long>(t) * p.kp + j * NK + quad * 32) * D + 192 * d3;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 3; ++c) {
           uint32_t v[64], w[32];
           tmem_ld32(lane_addr + tmem + 256 * ab + 64 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
