@@ -128,7 +128,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
         if (sp.j0 >= sp.j1) continue;
         const int t = token(item);
         const int ib = n & 1;
-        if (!(ok = mbar_wait(cta.bar(B_IDX_EMPTY + ib), ((n >> 1) & 1) ^ 1, abort_flag))) break;
+        if (!(ok = lean_wait(cta.bar(B_IDX_EMPTY + ib), ((n >> 1) & 1) ^ 1, abort_flag))) break;
         mbar_arrive_expect_tx(cta.bar(B_IDX_FULL + ib), p.k * 4);
         bulk_load(sbase + OFF_IDX + ib * mla::KMAX * 4, p.idx + static_cast<long long>(t) * p.k, p.k * 4,
                   cta.bar(B_IDX_FULL + ib));
@@ -150,7 +150,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
       if (sp.j0 >= sp.j1) continue;
       const int t = token(item);
       const int ib = n & 1;
-      if (!(ok = warp_wait(cta.bar(B_IDX_FULL + ib), (n >> 1) & 1, abort_flag))) break;
+      if (!(ok = lean_warp_wait(cta.bar(B_IDX_FULL + ib), (n >> 1) & 1, abort_flag))) break;
       const int* ids = reinterpret_cast<const int*>(cta.smem + OFF_IDX + ib * mla::KMAX * 4);
       // the rows of the next tile are read while this one waits for its buffer; an empty slot's row is zero
       auto load = [&](int j, uint4 (&v)[STEPS]) {
@@ -164,7 +164,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
       };
       uint4 v[STEPS];
       load(sp.j0, v);
-      if (!(ok = warp_wait(cta.bar(B_Q_EMPTY + ib), ((n >> 1) & 1) ^ 1, abort_flag))) break;
+      if (!(ok = lean_warp_wait(cta.bar(B_Q_EMPTY + ib), ((n >> 1) & 1) ^ 1, abort_flag))) break;
       const uint4* qrow = reinterpret_cast<const uint4*>(p.q_idx + static_cast<long long>(t) * HI * DI);
       for (int i = pw * 32 + lane; i < HI * U; i += PRODUCERS * 32)
         put_e4m3_row16(cta.smem + OFF_Q + ib * Q_BYTES, QCH, i / U, i % U, __ldg(qrow + i));
@@ -175,7 +175,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
         const int kb = g & 1;
         uint4 next[STEPS];
         if (j + 1 < sp.j1) load(j + 1, next);
-        if (!(ok = warp_wait(cta.bar(B_K_EMPTY + kb), ((g >> 1) & 1) ^ 1, abort_flag))) break;
+        if (!(ok = lean_warp_wait(cta.bar(B_K_EMPTY + kb), ((g >> 1) & 1) ^ 1, abort_flag))) break;
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
           put_e4m3_row16(cta.smem + OFF_K + kb * K_BYTES, KCH, pw * (NK / PRODUCERS) + s * ROWS + sub, u, v[s]);
@@ -207,9 +207,9 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
     constexpr uint32_t idq = idesc_bf16_major(128, HP, true, true);
     auto scores = [&]() -> bool {         // x of cursor a's tile
       const int s = a.g & 1, qb = a.n & 1;
-      if (a.j == 0 && !warp_wait(cta.bar(B_Q_FULL + qb), (a.n >> 1) & 1, abort_flag)) return false;
-      if (!warp_wait(cta.bar(B_K_FULL + s), (a.g >> 1) & 1, abort_flag)) return false;
-      if (!warp_wait(cta.bar(B_X_EMPTY + s), ((a.g >> 1) & 1) ^ 1, abort_flag)) return false;
+      if (a.j == 0 && !lean_warp_wait(cta.bar(B_Q_FULL + qb), (a.n >> 1) & 1, abort_flag)) return false;
+      if (!lean_warp_wait(cta.bar(B_K_FULL + s), (a.g >> 1) & 1, abort_flag)) return false;
+      if (!lean_warp_wait(cta.bar(B_X_EMPTY + s), ((a.g >> 1) & 1) ^ 1, abort_flag)) return false;
       tc_fence_after();
       const uint64_t kd = smem_desc(sbase + OFF_K + s * K_BYTES, 16, 1024, kLayoutSW128);
       const uint64_t qd = smem_desc(sbase + OFF_Q + qb * Q_BYTES, 16, 1024, kLayoutSW128);
@@ -228,9 +228,9 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
     while (ok && b.item < items) {
       if (a.item < items && !(ok = scores())) break;
       const int s = b.g & 1, qb = b.n & 1;
-      if (b.j == 0 && !(ok = warp_wait(cta.bar(B_DQ_EMPTY + qb), ((b.n >> 1) & 1) ^ 1, abort_flag))) break;
-      if (!(ok = warp_wait(cta.bar(B_DK_EMPTY + s), ((b.g >> 1) & 1) ^ 1, abort_flag))) break;
-      if (!(ok = warp_wait(cta.bar(B_G_FULL + s), (b.g >> 1) & 1, abort_flag))) break;
+      if (b.j == 0 && !(ok = lean_warp_wait(cta.bar(B_DQ_EMPTY + qb), ((b.n >> 1) & 1) ^ 1, abort_flag))) break;
+      if (!(ok = lean_warp_wait(cta.bar(B_DK_EMPTY + s), ((b.g >> 1) & 1) ^ 1, abort_flag))) break;
+      if (!(ok = lean_warp_wait(cta.bar(B_G_FULL + s), (b.g >> 1) & 1, abort_flag))) break;
       tc_fence_after();
       const uint32_t gb = sbase + OFF_G + 2 * s * G_BYTES;
       const uint64_t gd = smem_desc(gb, 16, 1024, kLayoutSW128);                             // keys x heads, K = heads
@@ -258,7 +258,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
     }
   } else if (warp < 8 || warp >= 18) {
     // ===================================================================== G qs, G ks and dw (one key a thread)
-    // Two groups of four warps take tiles in turn (one group alone: 707 us for 2048 tokens, against XXX).  The entry of
+    // Two groups of four warps take tiles in turn (one group alone: 707 us for 2048 tokens, against 596).  The entry of
     // a thread's next tile but one, and the gradient and key scale of its next tile, are on their way meanwhile.
     const int grp = warp >= 18 ? 1 : 0;
     const int quad = warp & 3, row = quad * 32 + lane;
@@ -296,14 +296,14 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
         const int s = grp, use = (g + j - sp.j0) >> 1;
         const float e_next = grad(j + 2, id_next), ks_next = scale(id_next);
         id_next = entry(j + 4);
-        ok = warp_wait(cta.bar(B_X_FULL + s), use & 1, abort_flag);
-        ok = ok && warp_wait(cta.bar(B_G_EMPTY + s), (use & 1) ^ 1, abort_flag);
+        ok = lean_warp_wait(cta.bar(B_X_FULL + s), use & 1, abort_flag);
+        ok = ok && lean_warp_wait(cta.bar(B_G_EMPTY + s), (use & 1) ^ 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         uint8_t* gl = cta.smem + OFF_G + 2 * s * G_BYTES + row * 128;
         const float eks = e * ks, eqs = e * qs;
         // not unrolled (nor are the loops over 64 dims below): the roles' code together has to stay in the instruction cache,
-        // fetches from behind it were a sixth of all stalls (680 us for 2048 tokens, against XXX)
+        // fetches from behind it were a sixth of all stalls (680 us for 2048 tokens, against 560)
 #pragma unroll 1
         for (int c = 0; c < BLOCKS; ++c) {
           uint32_t v[16];
@@ -395,7 +395,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
       }
       for (int j = sp.j0; j < sp.j1; ++j, ++g) {
         const int s = g & 1;
-        if (!(ok = warp_wait(cta.bar(B_DK_FULL + s), (g >> 1) & 1, abort_flag))) break;
+        if (!(ok = lean_warp_wait(cta.bar(B_DK_FULL + s), (g >> 1) & 1, abort_flag))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < DI / 64; ++c) {
@@ -429,7 +429,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
       if (!ok) break;
       // dq^T: lane = dim, column = head
       const int qb = n & 1;
-      if (!(ok = warp_wait(cta.bar(B_DQ_FULL + qb), (n >> 1) & 1, abort_flag))) break;
+      if (!(ok = lean_warp_wait(cta.bar(B_DQ_FULL + qb), (n >> 1) & 1, abort_flag))) break;
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < (HI + 31) / 32; ++c) {

@@ -112,8 +112,10 @@ __device__ __forceinline__ void tma2_gather4(uint32_t dst, const CUtensorMap* ma
       " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
       :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
 }
+// Relaxed: what it announces (tensor memory read to the end, or nothing at all) is complete when it is issued, and a release
+// would first wait for every store of P and dS the thread has in flight.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
 }
 
 // 32 rows of 8 N bf16 of a warp, one row a lane (packed in v), to rows `stride` bytes apart.  Turned in the warp's own
@@ -141,6 +143,29 @@ struct TileSpan {
 __device__ __forceinline__ TileSpan tile_span(int n_end, int keys, int sp, int splits) {
   const int tiles = (n_end + keys - 1) / keys, per = (tiles + splits - 1) / splits;
   return {min(tiles, sp * per), min(tiles, (sp + 1) * per)};
+}
+
+// Bounded waits as mbar_wait and warp_wait, the part behind a first unsuccessful look in a function of its own: where a
+// kernel's roles together overflow the instruction cache, the copies of that part cost more than the call (dq 96 -> 88 us for
+// 333 tokens, the index scores' pass 534 -> 494 for 2048; the probabilities' kernels fit and keep theirs in line).
+__device__ __noinline__ bool mbar_wait_far(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const long long t0 = clock64();
+  while (!mbar_test(bar, parity)) {
+    if (*abort_flag) return false;
+    if (clock64() - t0 > g_wait_limit) {
+      *abort_flag = 1;
+      raise_status(DSA_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool lean_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_test(bar, parity) || mbar_wait_far(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool lean_warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const bool ok = lean_wait(bar, parity, abort_flag);
+  return __all_sync(0xffffffffu, ok);
 }
 
 namespace mbw {
@@ -818,7 +843,7 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
         const TileSpan sp = part(item, ts, d3);
         const int t = token(ts);
         for (int j = sp.j0; j < sp.j1; ++j, rp.advance(), ++issued) {
-          if (!(ok = mbar_wait(cta.bar(B_RING_EMPTY + rp.stage), rp.phase ^ 1, abort_flag))) break;
+          if (!(ok = lean_wait(cta.bar(B_RING_EMPTY + rp.stage), rp.phase ^ 1, abort_flag))) break;
           const uint32_t full = cta.bar(B_RING_FULL + rp.stage), dst = ring + rp.stage * STAGE;
           mbar_arrive_expect_tx(full, A_BYTES);
           for (int i = 0; i < 2; ++i)      // HP = 64: the second block is P's columns, its products are not stored
@@ -848,7 +873,7 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
       for (int j = j0; j < sp.j1; j += 2) {
         const int at = m + j - sp.j0, st = at % NS;
         const int next = entry(j + 2);
-        if (!(ok = warp_wait(cta.bar(B_RING_EMPTY + st), ((at / NS) & 1) ^ 1, abort_flag))) break;
+        if (!(ok = lean_warp_wait(cta.bar(B_RING_EMPTY + st), ((at / NS) & 1) ^ 1, abort_flag))) break;
         const uint32_t dst = ring + st * STAGE + A_BYTES + (rows + sub) * 128;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -875,10 +900,10 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
       const TileSpan sp = part(item, ts, d3);
       if (sp.j0 >= sp.j1) continue;
       const int ab = n & 1;
-      if (!(ok = warp_wait(cta.bar(B_ACC_EMPTY + ab), ((n >> 1) & 1) ^ 1, abort_flag))) break;
+      if (!(ok = lean_warp_wait(cta.bar(B_ACC_EMPTY + ab), ((n >> 1) & 1) ^ 1, abort_flag))) break;
       tc_fence_after();
       for (int j = sp.j0; j < sp.j1; ++j, rp.advance()) {
-        if (!(ok = warp_wait(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
+        if (!(ok = lean_warp_wait(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
         fence_proxy_async_smem();            // the gathered keys were written through the generic proxy
         tc_fence_after();
         const uint32_t at = ring + rp.stage * STAGE;
@@ -911,7 +936,7 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
         continue;
       }
       const int ab = n & 1;
-      if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), (n >> 1) & 1, abort_flag))) break;
+      if (!(ok = lean_warp_wait(cta.bar(B_ACC_FULL + ab), (n >> 1) & 1, abort_flag))) break;
       tc_fence_after();
       for (int c = 0; c < 6; ++c) {
         uint32_t v[32];
