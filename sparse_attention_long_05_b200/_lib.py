@@ -167,10 +167,11 @@ def _elsewhere(fn: str, device, stream):
     return torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream)
 
 
-def _ws(fn: str, ws, need: int, device):
-    """The workspace (allocated when None) as (tensor, pointer, bytes)."""
+def _ws(fn: str, ws, need: int, like):
+    """The workspace (allocated on the device of `like` when None) as (tensor, pointer, bytes)."""
+    device = like.device
     if ws is None:
-        ws = torch.empty((need,), dtype=torch.uint8, device=device)
+        ws = like.new_empty((need,), dtype=torch.uint8)
     elif ws.device != device or not ws.is_contiguous():
         raise ValueError(f"{fn}: the workspace is a contiguous tensor on {device}")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
@@ -245,16 +246,17 @@ def dsa_sparse_mla_attn_backward(q, c, idx, out, lse, dout, scale: float, dq=Non
         with at:
             return dsa_sparse_mla_attn_backward(q, c, idx, out, lse, dout, scale, dq, dc, ws)
     if dq is None:
-        dq = torch.empty((T, H, 576), dtype=bf16, device=dev)
+        dq = q.new_empty((T, H, 576))
     if dc is None:
-        dc = torch.empty((S, 576), dtype=bf16, device=dev)
+        dc = q.new_empty((S, 576))
     pq, pc, pi, po, pl, pd, pdq, pdc = _want(fn, dev, (
         ("q", q, bf16, (T, H, 576)), ("c", c, bf16, (S, 576)), ("idx", idx, torch.int32, (T, k)),
         ("out", out, bf16, (T, H, 512)), ("lse", lse, torch.float32, (T, H)), ("dout", dout, bf16, (T, H, 512)),
         ("dq", dq, bf16, (T, H, 576)), ("dc", dc, bf16, (S, 576))))
     ws, pw, nw = _ws(fn, ws, 0 if ws is not None else _lib.dsa_sparse_mla_attn_backward_workspace_size(T, S, H, k),
-                     dev)
-    _check(fn, _lib.dsa_sparse_mla_attn_backward(pq, pc, S, pi, po, pl, pd, T, H, k, scale, pdq, pdc, pw, nw, _current_stream(dev.index)))
+                     q)
+    _check(fn, _lib.dsa_sparse_mla_attn_backward(pq, pc, S, pi, po, pl, pd, T, H, k, scale, pdq, pdc, pw,
+                                                 nw, _current_stream(dev.index)))
     return dq, dc
 
 
@@ -288,12 +290,12 @@ def dsa_indexer_kl_backward(q, c, idx, sel_scores, lse, dkl, scale: float, dsel=
         with at:
             return dsa_indexer_kl_backward(q, c, idx, sel_scores, lse, dkl, scale, dsel, ws)
     if dsel is None:
-        dsel = torch.empty((T, k), dtype=f32, device=dev)
+        dsel = lse.new_empty((T, k))
     pq, pc, pi, ps, pl, pk, pd = _want(fn, dev, (
         ("q", q, bf16, (T, H, 576)), ("c", c, bf16, (S, 576)), ("idx", idx, torch.int32, (T, k)),
         ("sel_scores", sel_scores, f32, (T, k)), ("lse", lse, f32, (T, H)), ("dkl", dkl, f32, (T,)),
         ("dsel", dsel, f32, (T, k))))
-    ws, pw, nw = _ws(fn, ws, 0 if ws is not None else _lib.dsa_indexer_kl_backward_workspace_size(T), dev)
+    ws, pw, nw = _ws(fn, ws, 0 if ws is not None else _lib.dsa_indexer_kl_backward_workspace_size(T), q)
     _check(fn, _lib.dsa_indexer_kl_backward(pq, pc, S, pi, ps, pl, pk, T, H, k, scale, pd, pw, nw, _current_stream(dev.index)))
     return dsel
 
@@ -315,18 +317,18 @@ def dsa_indexer_scores_backward(q_idx, q_scale, k_idx, k_scale, w, idx, dsel, dq
         with at:
             return dsa_indexer_scores_backward(q_idx, q_scale, k_idx, k_scale, w, idx, dsel, dq, dk, dw, ws)
     if dq is None:
-        dq = torch.empty((T, H_I, d_I), dtype=bf16, device=dev)
+        dq = q_idx.new_empty((T, H_I, d_I), dtype=bf16)
     if dk is None:
-        dk = torch.empty((S, d_I), dtype=bf16, device=dev)
+        dk = q_idx.new_empty((S, d_I), dtype=bf16)
     if dw is None:
-        dw = torch.empty((T, H_I), dtype=f32, device=dev)
+        dw = w.new_empty((T, H_I))
     pq, pqs, pk, pks, pw_, pi, pe, pdq, pdk, pdw = _want(fn, dev, (
         ("q_idx", q_idx, e4m3, (T, H_I, d_I)), ("q_scale", q_scale, f32, (T,)), ("k_idx", k_idx, e4m3, (S, d_I)),
         ("k_scale", k_scale, f32, (S,)), ("w", w, f32, (T, H_I)), ("idx", idx, torch.int32, (T, k)),
         ("dsel", dsel, f32, (T, k)), ("dq", dq, bf16, (T, H_I, d_I)), ("dk", dk, bf16, (S, d_I)),
         ("dw", dw, f32, (T, H_I))))
     ws, pw, nw = _ws(fn, ws, 0 if ws is not None else
-                     _lib.dsa_indexer_scores_backward_workspace_size(T, S, H_I, d_I, k), dev)
+                     _lib.dsa_indexer_scores_backward_workspace_size(T, S, H_I, d_I, k), q_idx)
     _check(fn, _lib.dsa_indexer_scores_backward(pq, pqs, pk, pks, pw_, pi, pe, T, S, H_I, d_I, k, pdq, pdk, pdw, pw,
                                                 nw, _current_stream(dev.index)))
     return dq, dk, dw
@@ -359,7 +361,7 @@ def _rope(fn: str, x, inv_freq, positions, pos0, rot_off, interleaved, mscale, o
         with at:
             return _rope(fn, x, inv_freq, positions, pos0, rot_off, interleaved, mscale, out, None)
     if out is None:
-        out = torch.empty((T, H, D), dtype=dtype, device=dev)
+        out = x.new_empty((T, H, D))
     elif out.shape != x.shape or out.dtype is not dtype or out.device != dev:
         raise ValueError(f"{fn}: input and result are of one shape, type and device")
     xt, xh, x1 = x.stride()

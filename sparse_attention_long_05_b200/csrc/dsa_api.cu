@@ -252,6 +252,27 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// launch_pdl of a kernel with more dynamic shared memory than the default: the attribute that allows it is set at the
+// kernel's first launch on a device (`seen`: one bit a device), and once more where a launch is refused without it (after
+// a cudaDeviceReset); setting it on every call costs about as much as a third of a launch.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_large(std::atomic<unsigned long long>& seen, void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                             size_t smem, cudaStream_t st, Args... args) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  const bool known = dev < 64 && (seen.load(std::memory_order_relaxed) & bit);
+  if (known) {
+    e = launch_pdl(kernel, grid, block, smem, st, args...);
+    if (e != cudaErrorInvalidValue) return e;
+    cudaGetLastError();
+  }
+  if ((e = set_smem(kernel, static_cast<int>(smem))) != cudaSuccess) return e;
+  if (dev < 64) seen.fetch_or(bit, std::memory_order_relaxed);
+  return launch_pdl(kernel, grid, block, smem, st, args...);
+}
+
 dsa_status_t last_launch_status() {
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
@@ -786,10 +807,7 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
       !make_rows_map(&tc, c, S, mbw::D, 1) || !make_rows_map(&tp128, w.pds, rows, 2 * w.HP, 128) ||
       !make_rows_map(&tp64, w.pds, rows, 2 * w.HP, 64))
     return DSA_ERR_CUDA;
-  if (set_smem(mla_bwd_p_kernel<false>, mbw::p::Map<false>::SMEM) != cudaSuccess ||
-      set_smem(mla_bwd_dc_kernel, mbw::dc::SMEM) != cudaSuccess ||
-      set_smem(mla_bwd_dq_kernel, mbw::dq::SMEM) != cudaSuccess)
-    return DSA_ERR_CUDA;
+  static std::atomic<unsigned long long> seen[3];
   const int sms = num_sms();
   for (int t0 = 0; t0 < T; t0 += w.Tc) {
     const int n = std::min(w.Tc, T - t0);
@@ -821,18 +839,18 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
     if (e != DSA_OK) return e;
     if ((e = scatter_build(w.sc, p.idx, n, S, k, st)) != DSA_OK) return e;
     p.splits = choose_splits(n, sms / 2, (k + 255) / 256, 0.8);
-    if (launch_pdl(mla_bwd_p_kernel<false>, dim3(2 * std::min(sms / 2, n * p.splits)), dim3(mbw::p::THREADS),
+    if (launch_pdl_large(seen[0], mla_bwd_p_kernel<false>, dim3(2 * std::min(sms / 2, n * p.splits)), dim3(mbw::p::THREADS),
                    mbw::p::Map<false>::SMEM, st, tq, tdo, tc, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
     p.splits = choose_splits(3ll * n, sms, w.kp / 128, 1.5);
-    if (launch_pdl(mla_bwd_dc_kernel, dim3(std::min(sms, 3 * n * p.splits)), dim3(mbw::dc::THREADS), mbw::dc::SMEM, st,
+    if (launch_pdl_large(seen[1], mla_bwd_dc_kernel, dim3(std::min(sms, 3 * n * p.splits)), dim3(mbw::dc::THREADS), mbw::dc::SMEM, st,
                    tp128, tq, tdo, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
     p.splits = w.dq_splits;
     p.dq_part = w.dq_part;
-    if (launch_pdl(mla_bwd_dq_kernel, dim3(std::min(sms, 3 * n * p.splits)), dim3(mbw::dq::THREADS), mbw::dq::SMEM, st,
+    if (launch_pdl_large(seen[2], mla_bwd_dq_kernel, dim3(std::min(sms, 3 * n * p.splits)), dim3(mbw::dq::THREADS), mbw::dq::SMEM, st,
                    tp64, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
@@ -875,8 +893,8 @@ dsa_status_t run_kl_bwd(const uint16_t* q, const uint16_t* c, int S, const int32
     return DSA_ERR_CUDA;
   const dsa_status_t e = last_launch_status();
   if (e != DSA_OK) return e;
-  if (set_smem(mla_bwd_p_kernel<true>, mbw::p::Map<true>::SMEM) != cudaSuccess) return DSA_ERR_CUDA;
-  if (launch_pdl(mla_bwd_p_kernel<true>, dim3(2 * std::min(num_sms() / 2, T)), dim3(mbw::p::THREADS),
+  static std::atomic<unsigned long long> seen;
+  if (launch_pdl_large(seen, mla_bwd_p_kernel<true>, dim3(2 * std::min(num_sms() / 2, T)), dim3(mbw::p::THREADS),
                  mbw::p::Map<true>::SMEM, st, tq, tq, tc, p) != cudaSuccess)
     return DSA_ERR_CUDA;
   return last_launch_status();
@@ -905,7 +923,7 @@ template <int HI, int DI>
 dsa_status_t run_index_bwd(IndexerBwdParams p, int T, uint16_t* dk, const IndexBwdWs& w, cudaStream_t st) {
   CUtensorMap tout;
   if (!make_rows_map(&tout, w.sc.contrib, static_cast<long long>(w.Tc) * w.kp, DI, 32)) return DSA_ERR_CUDA;
-  if (set_smem(indexer_bwd_kernel<HI, DI>, ixb::SMEM) != cudaSuccess) return DSA_ERR_CUDA;
+  static std::atomic<unsigned long long> seen;
   p.n_end = w.sc.n_end;
   p.kp = w.kp;
   p.splits = w.splits;
@@ -927,7 +945,7 @@ dsa_status_t run_index_bwd(IndexerBwdParams p, int T, uint16_t* dk, const IndexB
     dsa_status_t e = last_launch_status();
     if (e != DSA_OK) return e;
     if ((e = scatter_build(w.sc, p.idx, p.T, p.S, p.k, st)) != DSA_OK) return e;
-    if (launch_pdl(indexer_bwd_kernel<HI, DI>, dim3(std::min(num_sms(), p.T * p.splits)), dim3(ixb::THREADS), ixb::SMEM, st, tout,
+    if (launch_pdl_large(seen, indexer_bwd_kernel<HI, DI>, dim3(std::min(num_sms(), p.T * p.splits)), dim3(ixb::THREADS), ixb::SMEM, st, tout,
                    p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
