@@ -843,8 +843,8 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
                    mbw::p::Map<false>::SMEM, st, tq, tdo, tc, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
-    p.splits = choose_splits(3ll * n, sms, w.kp / 128, 1.5);
-    if (launch_pdl_large(seen[1], mla_bwd_dc_kernel, dim3(std::min(sms, 3 * n * p.splits)), dim3(mbw::dc::THREADS), mbw::dc::SMEM, st,
+    p.splits = choose_splits(3ll * n, sms / 2, (k + 255) / 256, 1.0);
+    if (launch_pdl_large(seen[1], mla_bwd_dc_kernel, dim3(2 * std::min(sms / 2, 3 * n * p.splits)), dim3(mbw::dc::THREADS), mbw::dc::SMEM, st,
                    tp128, tq, tdo, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;

@@ -13,7 +13,7 @@
 // with a resident operand that fits, and P and dS (bf16, 1 MB a token) between them:
 //   mla_bwd_p_kernel   (token, 64 heads): keys are the M dimension; q and dout rows of the 64 heads, stacked to
 //                      N = 128, stay in shared memory; every gathered chunk of 128 keys x 64 dims meets both at once;
-//   mla_bwd_dc_kernel  (token, 192 dims): [dS | P] (128 keys x heads) times [q ; dout] (heads x 192 dims), resident;
+//   mla_bwd_dc_kernel  (token, 256 dims): [dS | P] (256 keys x heads) times [q ; dout] (heads x 256 dims), resident;
 //                      writes each entry's own contribution to dc (16 bits a value, see scatter.cuh);
 //   mla_bwd_dq_kernel  (token, 192 dims): dS^T (heads x keys) times the gathered keys (keys x 192 dims), accumulated
 //                      over the token's keys in tensor memory.
@@ -104,6 +104,12 @@ __device__ __forceinline__ void tma2_load_3d(uint32_t dst, const CUtensorMap* ma
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
       " [%0], [%1, {%3, %4, %5}], [%2];"
       :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void tma2_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4}], [%2];"
+      :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
 }
 __device__ __forceinline__ void tma2_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
                                              int r0, int r1, int r2, int r3) {
@@ -209,8 +215,8 @@ static_assert(OFF_RES % 1024 == 0 && OFF_SUMS + 32 <= BAR_BYTES && Map<true>::NS
 // ---- mla_bwd_dc_kernel
 namespace dc {
 constexpr int THREADS = 384;            // w0 resident rows, w1 MMA, w2 dS and P, w4..7 w8..11 contributions
-constexpr int NS = 3;                   // ring stages: dS or P of 128 keys x all heads (two 64-head blocks, 32 KB)
-constexpr int UNIT = 3 * HCHUNK;        // resident operand of 64 heads: 64 heads x 192 dims (24 KB)
+constexpr int NS = 4;                   // ring stages: dS or P of 128 keys x all heads (two 64-head blocks, 32 KB)
+constexpr int UNIT = 2 * HCHUNK;        // resident operand of 64 heads: 64 heads x 128 dims (16 KB)
 constexpr int NU = 4;                   // units: q of heads 0..63, 64..127, dout of the same
 constexpr int B_RES_FULL = 0, B_RES_EMPTY = B_RES_FULL + NU, B_RING_FULL = B_RES_EMPTY + NU;
 constexpr int B_RING_EMPTY = B_RING_FULL + NS, B_ACC_FULL = B_RING_EMPTY + NS, B_ACC_EMPTY = B_ACC_FULL + 2;
@@ -653,8 +659,13 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   bwd_end<true>(cta);
 }
 
-// Contributions to dc: out[t kp + slot][d] = sum_h dS q[t][h][d] + P dout[t][h][d] for 192 dims d per item.
-__global__ void __launch_bounds__(mbw::dc::THREADS, 1)
+// Contributions to dc: contrib[t kp + slot][d] = sum_h dS q[t][h][d] + P dout[t][h][d], one (token, 256 dims) per CTA pair and
+// item, the 64 position dims (dS q alone) as a third item.
+//
+// M = 256 keys (128 in each CTA), N = 256 dims (128 of q and dout in each CTA, resident), K = heads of dS, then of P.  As
+// single CTAs with N = 192 each MMA read 10 KB of shared memory in 96 cycles, and a token's dS and P three times: 1426 us
+// for 2048 tokens, against XXX.  HBM: the contributions (2.3 MB a token) written, P and dS (1 MB) read.
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mbw::dc::THREADS, 1)
 mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_do, const MlaBwdParams p) {
   using namespace mbw;
@@ -664,104 +675,129 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
   const uint32_t sbase = cta.sbase;
   volatile int* abort_flag = cta.abort_flag;
   const int warp = warp_id(), lane = lane_id();
+  const int rank = static_cast<int>(cluster_rank());
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NU; ++i) { mbar_init(cta.bar(B_RES_FULL + i), 1); mbar_init(cta.bar(B_RES_EMPTY + i), 1); }
-    for (int i = 0; i < NS; ++i) { mbar_init(cta.bar(B_RING_FULL + i), 1); mbar_init(cta.bar(B_RING_EMPTY + i), 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(cta.bar(B_ACC_FULL + i), 1); mbar_init(cta.bar(B_ACC_EMPTY + i), 4); }
+    for (int i = 0; i < NU; ++i) { mbar_init(cta.bar(B_RES_FULL + i), 2); mbar_init(cta.bar(B_RES_EMPTY + i), 1); }
+    for (int i = 0; i < NS; ++i) { mbar_init(cta.bar(B_RING_FULL + i), 2); mbar_init(cta.bar(B_RING_EMPTY + i), 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(cta.bar(B_ACC_FULL + i), 1); mbar_init(cta.bar(B_ACC_EMPTY + i), 8); }
   }
-  bwd_begin(cta);
+  bwd_begin<true>(cta);
   const uint32_t tmem = cta.tmem;
   const uint32_t res = sbase + OFF_RES, ring = sbase + OFF_RING;
-  const int hb = p.HP / 64, units = 2 * hb;        // 64-head blocks of dS, then of P
+  const uint32_t lead = map_cluster(sbase, 0);     // CTA 0's barriers, where every load of the pair completes
+  const int first = static_cast<int>(blockIdx.x >> 1), stride = static_cast<int>(gridDim.x >> 1);
+  const int hb = p.HP / 64;                        // 64-head blocks
   const int items = 3 * p.T * p.splits;
-  auto part = [&](int item, int& t, int& d3) {         // item: (token, split, 192 dims)
+  auto part = [&](int item, int& t, int& d3) {     // item: (token, split, 256 or 64 dims)
     d3 = item % 3;
     const int ts = item / 3;
     t = p.splits == 1 ? ts : ts / p.splits;
-    return tile_span(p.n_end[t], NK, p.splits == 1 ? 0 : ts % p.splits, p.splits);
+    return tile_span(p.n_end[t], 2 * NK, p.splits == 1 ? 0 : ts % p.splits, p.splits);
   };
   bool ok = true;
   int n = 0;
 
   if (warp == 0) {
     // ===================================================================== resident q and dout
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    for (int item = first; item < items && ok; item += stride) {
       int t, d3;
       const TileSpan sp = part(item, t, d3);
       if (sp.j0 >= sp.j1) continue;
-      for (int u = 0; u < units; ++u) {                  // a box of 64 dims a lane
-        const int boxes = (u >= hb && d3 == 2) ? 2 : 3;  // dout ends at dim 512
-        const uint32_t full = cta.bar(B_RES_FULL + u);
+      const int units = d3 == 2 ? hb : 2 * hb, boxes = d3 == 2 ? 1 : 2;
+      // (CTA 1's columns of the third item lie behind dim 576: zeros)
+      const int d0 = d3 == 2 ? 512 + 64 * rank : 256 * d3 + 128 * rank;
+      for (int u = 0; u < units; ++u) {            // a box of 64 dims a lane
+        const uint32_t full = lead + 8 * (B_RES_FULL + u);
         if (!(ok = warp_wait(cta.bar(B_RES_EMPTY + u), (n & 1) ^ 1, abort_flag))) break;
-        if (lane == 0) mbar_arrive_expect_tx(full, boxes * HCHUNK);
+        if (lane == 0) mbar_arrive_expect_tx_remote(full, boxes * HCHUNK);
         __syncwarp();
         if (lane < boxes)
-          tma_load_3d(res + u * UNIT + lane * HCHUNK, u < hb ? &tm_q : &tm_do, full, 192 * d3 + 64 * lane,
-                      64 * (u % hb), p.t0 + t);
+          tma2_load_3d(res + u * UNIT + lane * HCHUNK, u < hb ? &tm_q : &tm_do, full, d0 + 64 * lane, 64 * (u % hb),
+                       p.t0 + t);
       }
+      // the third item leaves dout's units alone: their phase goes on without a load
+      if (d3 == 2)
+        for (int u = units; u < 2 * hb && ok; ++u) {
+          ok = warp_wait(cta.bar(B_RES_EMPTY + u), (n & 1) ^ 1, abort_flag);
+          if (ok && lane == 0) mbar_arrive_remote(lead + 8 * (B_RES_FULL + u));
+        }
       ++n;
     }
-    if (lane == 0 && *abort_flag && n > 0)
-      for (int u = 0; u < units; ++u) mbar_wait_drain(cta.bar(B_RES_FULL + u), (n - 1) & 1);
   } else if (warp == 2) {
     // ===================================================================== dS and P tiles
     if (lane == 0) {
       Pipe<NS> rp;
-      int issued = 0;
-      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      for (int item = first; item < items && ok; item += stride) {
         int t, d3;
         const TileSpan sp = part(item, t, d3);
-        for (int j = sp.j0; j < sp.j1 && ok; ++j)
-          for (int u = 0; u < 2; ++u, rp.advance(), ++issued) {        // dS, then P
+        const int n_end = p.n_end[t];
+        for (int j = sp.j0; j < sp.j1 && ok; ++j) {
+          const bool any = (2 * j + rank) * NK < n_end;            // this CTA has keys in the tile
+          for (int u = 0; u < (d3 == 2 ? 1 : 2); ++u, rp.advance()) {
             if (!(ok = mbar_wait(cta.bar(B_RING_EMPTY + rp.stage), rp.phase ^ 1, abort_flag))) break;
-            const uint32_t full = cta.bar(B_RING_FULL + rp.stage);
-            mbar_arrive_expect_tx(full, hb * CHUNK);
+            const uint32_t full = lead + 8 * (B_RING_FULL + rp.stage);
+            if (!any) {
+              mbar_arrive_remote(full);
+              continue;
+            }
+            mbar_arrive_expect_tx_remote(full, hb * CHUNK);
             for (int i = 0; i < hb; ++i)
-              tma_load_2d(ring + (2 * rp.stage + i) * CHUNK, &tm_pds, full, 64 * (u * hb + i), t * p.kp + j * NK);
+              tma2_load_2d(ring + (2 * rp.stage + i) * CHUNK, &tm_pds, full, 64 * (u * hb + i),
+                           t * p.kp + (2 * j + rank) * NK);
           }
+        }
       }
-      if (*abort_flag)
-        for (int i = max(0, issued - NS); i < issued; ++i)
-          mbar_wait_drain(cta.bar(B_RING_FULL + i % NS), (i / NS) & 1);
     }
   } else if (warp == 1) {
-    // ===================================================================== MMA issue
-    Pipe<NS> rp;
-    int g = 0;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      int t, d3;
-      const TileSpan sp = part(item, t, d3);
-      if (sp.j0 >= sp.j1) continue;
-      for (int j = sp.j0; j < sp.j1 && ok; ++j, ++g) {
-        const int ab = g & 1;
-        if (!(ok = warp_wait(cta.bar(B_ACC_EMPTY + ab), ((g >> 1) & 1) ^ 1, abort_flag))) break;
-        tc_fence_after();
-        for (int half = 0; half < 2; ++half, rp.advance()) {   // dS . q, then P . dout
-          if (j == sp.j0)
-            for (int i = 0; i < hb && ok; ++i) ok = warp_wait(cta.bar(B_RES_FULL + half * hb + i), n & 1, abort_flag);
-          if (!(ok = ok && warp_wait(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
+    // ===================================================================== MMA issue (CTA 0 for the pair)
+    if (rank == 0) {
+      Pipe<NS> rp;
+      int g = 0;
+      for (int item = first; item < items && ok; item += stride) {
+        int t, d3;
+        const TileSpan sp = part(item, t, d3);
+        if (sp.j0 >= sp.j1) continue;
+        const uint32_t idesc = idesc_bf16(256, d3 == 2 ? 128 : 256, true);
+        for (int j = sp.j0; j < sp.j1 && ok; ++j, ++g) {
+          const int ab = g & 1;
+          const bool last = j == sp.j1 - 1;
+          if (!(ok = warp_wait<true>(cta.bar(B_ACC_EMPTY + ab), ((g >> 1) & 1) ^ 1, abort_flag))) break;
           tc_fence_after();
-          const uint64_t ad = smem_desc(ring + 2 * rp.stage * CHUNK, 16, 1024, kLayoutSW128);
-          // heads x dims, dims contiguous (MN-major): 64-dim atoms 8 KB apart, 8-head groups 1 KB apart
-          const uint64_t bd = smem_desc(res + half * hb * UNIT, HCHUNK, 1024, kLayoutSW128);
-          const uint32_t idesc = idesc_bf16(128, (half && d3 == 2) ? 128 : 192, true);
-          if (elect_one()) {
-            for (int i = 0; i < hb; ++i) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_bf16_ss(tmem + 256 * ab, ad + ((i * CHUNK) >> 4) + 2 * k, bd + ((i * UNIT + k * 2048) >> 4), idesc,
-                            (half | i | k) ? 1u : 0u);
-              if (j == sp.j1 - 1) mma_commit(cta.bar(B_RES_EMPTY + half * hb + i));
+          for (int half = 0; half < 2; ++half) {   // dS . q, then P . dout
+            if (j == sp.j0)
+              for (int i = 0; i < hb && ok; ++i)
+                ok = warp_wait<true>(cta.bar(B_RES_FULL + half * hb + i), n & 1, abort_flag);
+            if (!ok) break;
+            if (half && d3 == 2) {
+              if (last && elect_one())
+                for (int i = 0; i < hb; ++i) mma2_commit(cta.bar(B_RES_EMPTY + hb + i));
+              __syncwarp();
+              continue;
             }
-            mma_commit(cta.bar(B_RING_EMPTY + rp.stage));
+            if (!(ok = warp_wait<true>(cta.bar(B_RING_FULL + rp.stage), rp.phase, abort_flag))) break;
+            tc_fence_after();
+            const uint64_t ad = smem_desc(ring + 2 * rp.stage * CHUNK, 16, 1024, kLayoutSW128);
+            // heads x dims, dims contiguous (MN-major): 64-dim atoms 8 KB apart, 8-head groups 1 KB apart
+            const uint64_t bd = smem_desc(res + half * hb * UNIT, HCHUNK, 1024, kLayoutSW128);
+            if (elect_one()) {
+              for (int i = 0; i < hb; ++i) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma2_bf16_ss(tmem + 256 * ab, ad + ((i * CHUNK) >> 4) + 2 * k, bd + ((i * UNIT + k * 2048) >> 4), idesc,
+                               (half | i | k) ? 1u : 0u);
+                if (last) mma2_commit(cta.bar(B_RES_EMPTY + half * hb + i));
+              }
+              mma2_commit(cta.bar(B_RING_EMPTY + rp.stage));
+            }
+            __syncwarp();
+            rp.advance();
           }
+          if (!ok) break;
+          if (elect_one()) mma2_commit(cta.bar(B_ACC_FULL + ab));
           __syncwarp();
         }
-        if (!ok) break;
-        if (elect_one()) mma_commit(cta.bar(B_ACC_FULL + ab));
-        __syncwarp();
+        ++n;
       }
-      ++n;
     }
   } else if (warp >= 4) {
     // ===================================================================== contributions out (one key a thread)
@@ -770,25 +806,29 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
     const int quad = warp & 3;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     int g = 0;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    for (int item = first; item < items && ok; item += stride) {
       int t, d3;
       const TileSpan sp = part(item, t, d3);
+      const int n_end = p.n_end[t], blocks = d3 == 2 ? 1 : 4;
       for (int j = sp.j0 + ((g ^ grp) & 1); j < sp.j1; j += 2) {
         const int ab = grp;                // tile j is the CTA's tile g + j - j0, of this group's parity
+        const int slot0 = (2 * j + rank) * NK + quad * 32;
         if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), ((g + j - sp.j0) >> 1) & 1, abort_flag))) break;
         tc_fence_after();
-        uint16_t* out = p.contrib + (static_cast<long long>(t) * p.kp + j * NK + quad * 32) * D + 192 * d3;
+        uint16_t* out = p.contrib + (static_cast<long long>(t) * p.kp + slot0) * D + 256 * d3;
+        const bool any = slot0 < n_end;    // the warp's keys are not all behind the token's last entry
 #pragma unroll 1
-        for (int c = 0; c < 3; ++c) {
+        for (int c = 0; c < blocks; ++c) {
           uint32_t v[64], w[32];
           tmem_ld32(lane_addr + tmem + 256 * ab + 64 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
           tmem_ld32(lane_addr + tmem + 256 * ab + 64 * c + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
           tmem_wait_ld();
-          if (c == 2) {
+          if (c == blocks - 1) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(cta.bar(B_ACC_EMPTY + ab));
+            if (lane == 0) mbar_arrive_remote(lead + 8 * (B_ACC_EMPTY + ab));
           }
+          if (!any) continue;
           scatter_pack64(v, w);
           store_rows<8>(cta.smem + OFF_TURN + (4 * grp + quad) * 4096, w, out + 64 * c, 2 * D);
         }
@@ -796,7 +836,7 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
       g += sp.j1 - sp.j0;
     }
   }
-  bwd_end(cta);
+  bwd_end<true>(cta);
 }
 
 // dq[t][:, 192 dims] = dS^T . C per item, accumulated over the token's keys (or, with splits, over the split's) in tensor
