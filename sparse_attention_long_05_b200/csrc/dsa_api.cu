@@ -801,11 +801,12 @@ AttnBwdWs attn_bwd_ws(void* ws, int T, int64_t S, int H, int k) {
 dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx, const uint16_t* out,
                           const float* lse, const uint16_t* dout, int T, int H, int k, float scale, uint16_t* dq,
                           uint16_t* dc, const AttnBwdWs& w, cudaStream_t st) {
-  CUtensorMap tq, tdo, tc, tp128, tp64;
+  CUtensorMap tq, tdo, tc, tp128, tp64, tout;
   const size_t rows = size_t(w.Tc) * w.kp;
   if (!make_heads_map(&tq, q, T, H, mbw::D) || !make_heads_map(&tdo, dout, T, H, mbw::DV) ||
       !make_rows_map(&tc, c, S, mbw::D, 1) || !make_rows_map(&tp128, w.pds, rows, 2 * w.HP, 128) ||
-      !make_rows_map(&tp64, w.pds, rows, 2 * w.HP, 64))
+      !make_rows_map(&tp64, w.pds, rows, 2 * w.HP, 64) ||
+      !make_rows_map(&tout, w.sc.contrib, rows, mbw::D, 32))
     return DSA_ERR_CUDA;
   static std::atomic<unsigned long long> seen[3];
   const int sms = num_sms();
@@ -845,7 +846,7 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
     if ((e = last_launch_status()) != DSA_OK) return e;
     p.splits = choose_splits(3ll * n, sms / 2, (k + 255) / 256, 1.0);
     if (launch_pdl_large(seen[1], mla_bwd_dc_kernel, dim3(2 * std::min(sms / 2, 3 * n * p.splits)), dim3(mbw::dc::THREADS), mbw::dc::SMEM, st,
-                   tp128, tq, tdo, p) != cudaSuccess)
+                   tp128, tq, tdo, tout, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
     p.splits = w.dq_splits;

@@ -215,14 +215,14 @@ static_assert(OFF_RES % 1024 == 0 && OFF_SUMS + 32 <= BAR_BYTES && Map<true>::NS
 // ---- mla_bwd_dc_kernel
 namespace dc {
 constexpr int THREADS = 384;            // w0 resident rows, w1 MMA, w2 dS and P, w4..7 w8..11 contributions
-constexpr int NS = 4;                   // ring stages: dS or P of 128 keys x all heads (two 64-head blocks, 32 KB)
+constexpr int NS = 3;                   // ring stages: dS or P of 128 keys x all heads (two 64-head blocks, 32 KB)
 constexpr int UNIT = 2 * HCHUNK;        // resident operand of 64 heads: 64 heads x 128 dims (16 KB)
 constexpr int NU = 4;                   // units: q of heads 0..63, 64..127, dout of the same
 constexpr int B_RES_FULL = 0, B_RES_EMPTY = B_RES_FULL + NU, B_RING_FULL = B_RES_EMPTY + NU;
 constexpr int B_RING_EMPTY = B_RING_FULL + NS, B_ACC_FULL = B_RING_EMPTY + NS, B_ACC_EMPTY = B_ACC_FULL + 2;
 static_assert((B_ACC_EMPTY + 2) * 8 <= OFF_TMEM, "barrier area");
-constexpr int OFF_RES = BAR_BYTES, OFF_RING = OFF_RES + NU * UNIT, OFF_TURN = OFF_RING + NS * 2 * CHUNK;
-constexpr int SMEM = OFF_TURN + 8 * 4096 + 1024;
+constexpr int OFF_RES = BAR_BYTES, OFF_RING = OFF_RES + NU * UNIT, OFF_OUT = OFF_RING + NS * 2 * CHUNK;
+constexpr int SMEM = OFF_OUT + 8 * 2 * 4096 + 1024;   // two staging areas (32 keys x 64 dims) of each of eight warps
 static_assert(SMEM <= 232448, "shared memory per CTA");
 }  // namespace dc
 
@@ -667,7 +667,8 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 // for 2048 tokens, against XXX.  HBM: the contributions (2.3 MB a token) written, P and dS (1 MB) read.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mbw::dc::THREADS, 1)
 mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_constant__ CUtensorMap tm_q,
-                  const __grid_constant__ CUtensorMap tm_do, const MlaBwdParams p) {
+                  const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_out,
+                  const MlaBwdParams p) {
   using namespace mbw;
   using namespace mbw::dc;
   extern __shared__ uint8_t smem_raw[];
@@ -805,7 +806,7 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
     const int grp = (warp - 4) >> 2;
     const int quad = warp & 3;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
-    int g = 0;
+    int g = 0, put = 0;
     for (int item = first; item < items && ok; item += stride) {
       int t, d3;
       const TileSpan sp = part(item, t, d3);
@@ -815,7 +816,6 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
         const int slot0 = (2 * j + rank) * NK + quad * 32;
         if (!(ok = warp_wait(cta.bar(B_ACC_FULL + ab), ((g + j - sp.j0) >> 1) & 1, abort_flag))) break;
         tc_fence_after();
-        uint16_t* out = p.contrib + (static_cast<long long>(t) * p.kp + slot0) * D + 256 * d3;
         const bool any = slot0 < n_end;    // the warp's keys are not all behind the token's last entry
 #pragma unroll 1
         for (int c = 0; c < blocks; ++c) {
@@ -830,11 +830,27 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
           }
           if (!any) continue;
           scatter_pack64(v, w);
-          store_rows<8>(cta.smem + OFF_TURN + (4 * grp + quad) * 4096, w, out + 64 * c, 2 * D);
+          // the warp's 32 rows of 64 dims (128-byte swizzled: 16-byte unit u of row r at unit u ^ (r % 8)) go out by TMA, the
+          // previous piece's area being read meanwhile
+          const int area = OFF_OUT + ((2 * (4 * grp + quad)) + (put & 1)) * 4096;
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(cta.smem + area + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tm_out, sbase + area, 256 * d3 + 64 * c, t * p.kp + slot0);
+            bulk_commit();
+          }
+          ++put;
         }
       }
       g += sp.j1 - sp.j0;
     }
+    if (lane == 0) bulk_wait_all();
   }
   bwd_end<true>(cta);
 }
