@@ -179,6 +179,59 @@ def test_attention_backward_in_chunks_and_repeated(dsa):
     assert _rel(dq, want_q) <= L2_BF16 and _rel(dc, want_c) <= L2_BF16
 
 
+def test_more_tokens_than_a_chunk(dsa):
+    # a chunk holds at most 2048 tokens; the last one is shorter, and rows get entries from both
+    T, S, k = 2100, 700, 128
+    g = _gen(15)
+    idx = torch.stack([torch.randperm(S, generator=g)[:k] for _ in range(T)]).int()
+    idx[:, 100:] = -1
+    idx[2090:, 0] = 7
+    q, c = torch.randn(T, 3, D, generator=g).bfloat16().cuda(), torch.randn(S, D, generator=g).bfloat16().cuda()
+    dout, idx = torch.randn(T, 3, DV, generator=g).bfloat16().cuda(), idx.cuda()
+    out, lse = dsa.dsa_sparse_mla_attn(q, c, idx, SCALE)
+    dq, dc = dsa.dsa_sparse_mla_attn_backward(q, c, idx, out, lse, dout, SCALE)
+    want_q, want_c = _formula(q, c, idx, out, lse, dout)
+    assert _rel(dq, want_q) <= L2_BF16 and _rel(dc, want_c) <= L2_BF16
+    qi = torch.randn(T, 4, 64, generator=g).to(torch.float8_e4m3fn).cuda()
+    ki = torch.randn(S, 64, generator=g).to(torch.float8_e4m3fn).cuda()
+    w, dsel = torch.randn(T, 4, generator=g).cuda(), torch.randn(T, k, generator=g).cuda()
+    got = dsa.dsa_indexer_scores_backward(qi, None, ki, None, w, idx, dsel)
+    assert dsa.dsa_get_device_status() == 0
+    qf, kf, wf = (t.float().double().requires_grad_() for t in (qi, ki, w))
+    (_indexer_scores(qf, kf, wf, idx) * torch.where(idx >= 0, dsel.double(), 0.0)).sum().backward()
+    assert _rel(got[0], qf.grad) <= L2_BF16 and _rel(got[1], kf.grad) <= L2_BF16 and _rel(got[2], wf.grad) <= L2_FP32
+
+
+def test_rows_behind_32_bit_offsets(dsa):
+    # 4.0 million rows: c and dc hold 2.3e9 elements each, k_idx and dk 5.1e8 (bytes: 4.6e9, 1.0e9)
+    T, S, k, H = 2, 4_000_000, 128, 4
+    g = _gen(16)
+    near = torch.randint(0, 1000, (T, 64), generator=g)
+    idx = torch.cat([near.sort(1).values.unique(dim=1)[:, :32], S - 1 - torch.arange(96).expand(T, 96)], 1).int().cuda()
+    assert idx.shape == (T, k)
+    rows = idx.long().unique()
+    c = torch.zeros(S, D, dtype=torch.bfloat16, device="cuda")
+    c[rows] = torch.randn(len(rows), D, generator=g).bfloat16().cuda()
+    q, dout = (torch.randn(T, H, n, generator=g).bfloat16().cuda() for n in (D, DV))
+    out, lse = dsa.dsa_sparse_mla_attn(q, c, idx, SCALE)
+    dq, dc = dsa.dsa_sparse_mla_attn_backward(q, c, idx, out, lse, dout, SCALE)
+    assert dsa.dsa_get_device_status() == 0
+    where = torch.searchsorted(rows, idx.long()).int()
+    want_q, want_c = _formula(q, c[rows], where, out, lse, dout)
+    assert _rel(dq, want_q) <= L2_BF16 and _rel(dc[rows], want_c) <= L2_BF16
+    dc[rows] = 0
+    assert not dc.any()
+    del c, dc
+    ki = torch.zeros(S, 128, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    ki.view(torch.uint8)[rows] = torch.randn(len(rows), 128, generator=g).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+    qi = torch.randn(T, 64, 128, generator=g).to(torch.float8_e4m3fn).cuda()
+    w, dsel = torch.randn(T, 64, generator=g).cuda(), torch.randn(T, k, generator=g).cuda()
+    got = dsa.dsa_indexer_scores_backward(qi, None, ki, None, w, idx, dsel)
+    qf, kf, wf = (t.float().double().requires_grad_() for t in (qi, ki.view(torch.uint8)[rows].view(torch.float8_e4m3fn), w))
+    (_indexer_scores(qf, kf, wf, where) * dsel.double()).sum().backward()
+    assert _rel(got[0], qf.grad) <= L2_BF16 and _rel(got[1][rows], kf.grad) <= L2_BF16 and _rel(got[2], wf.grad) <= L2_FP32
+
+
 def test_attention_backward_nan_rows_nobody_selects(dsa):
     q, c, idx, dout = _attention_case(6, 400, 20, 192, "holes", 9)
     used = torch.zeros(400, dtype=torch.bool)
@@ -390,6 +443,10 @@ def test_rope_strides_offsets_and_positions(dsa):
     dsa.dsa_rope(q, f, pos0=90, out=q)
     assert torch.equal(wide[..., :512], before[..., :512])
     _rope_close(q, want, before.cpu(), 1.0)
+    # positions before the first, and both ends of their range
+    ends = torch.tensor([-1, -1000, -2 ** 31, 2 ** 31 - 1, 0], dtype=torch.int32)
+    x = torch.randn(5, 2, 64, generator=g)
+    _rope_close(dsa.dsa_rope(x.cuda(), f, ends.cuda()), _rope_reference(x, f.cpu(), ends, 0, True, 1.0, False), x, 1.0)
     # into the gaps of the same buffer
     both = torch.randn(6, 1, 128, generator=g).cuda()
     x, out = both[..., :64], both[..., 64:]
