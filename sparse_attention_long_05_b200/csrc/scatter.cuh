@@ -169,7 +169,7 @@ struct ScatterCfg {
 };
 
 template <int W>
-__global__ void __launch_bounds__(ScatterCfg<W>::THREADS, 6) scatter_sum_kernel(const ScatterParams p) {
+__global__ void __launch_bounds__(ScatterCfg<W>::THREADS, W == 576 ? 7 : 8) scatter_sum_kernel(const ScatterParams p) {
   using C = ScatterCfg<W>;
   __shared__ uint32_t list[sct::MAX_T];
   __shared__ int warp_n[C::WARPS];

@@ -398,6 +398,9 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // one L2 line for the whole GPU: 30 us against 18 for 96 short tokens); a CTA whose keys of a tile are all behind the
     // token's last entry reads nothing.
     constexpr int PER = SC * 32 / M::WPS, GROUPS = 8 / M::WPS;
+    // a group that comes to a stage again has seen the chunk before last of it consumed (its own last stage could not be
+    // filled before): the barrier's parity tells the two last phases apart
+    static_assert(GROUPS <= NS, "stages");
     const int gw = (warp < 8) ? warp - 2 : warp - 6;
     const int grp = gw / M::WPS, gi = (gw % M::WPS) * PER + lane, cc = gi / 32, rg = gi % 32;
     const bool active = lane < PER;
@@ -924,6 +927,7 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
     // An empty slot's row is filled with zeros: a NaN in a row that no token selects must not meet its dS = 0.
     const int gw = (warp < 8) ? warp - 2 : warp - 6;
     const int grp = gw >> 2, rows = (gw & 3) * 16, sub = lane >> 3, unit = lane & 7;
+    static_assert(2 <= NS, "stages (as in mla_bwd_p_kernel)");
     int m = 0;                             // stages of the items before this one
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       int ts, d3;
