@@ -655,12 +655,13 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           a_all = other.z + a_all;
         }
         const float up = p.dkl ? p.dkl[t] : 1.f;
-        const float iz = z_all > 0.f ? 1.f / z_all : 0.f, ia = a_all > 0.f ? 1.f / a_all : 0.f;
+        // (divisions, not products with reciprocals: a token with one entry has both exactly 1, and a gradient of 0)
+        const float z_div = z_all > 0.f ? z_all : INFINITY, a_div = a_all > 0.f ? a_all : INFINITY;
         for (int i = (2 * grp + rank) * NK + row; i < min(sp.j1 * 2 * NK, p.k); i += 4 * NK) {
           const int e = __ldg(p.idx + base + i);
           const float x = p.sel[base + i];
-          const float soft = x > -INFINITY ? ex2_approx((x - m_all) * kLog2e) * iz : 0.f;
-          p.dsel[base + i] = (e >= 0 && e < p.S) ? up * (soft - __ldcg(p.dsel + base + i) * ia) : 0.f;
+          const float soft = x > -INFINITY ? ex2_approx((x - m_all) * kLog2e) / z_div : 0.f;
+          p.dsel[base + i] = (e >= 0 && e < p.S) ? up * (soft - __ldcg(p.dsel + base + i) / a_div) : 0.f;
         }
       }
       ++n;

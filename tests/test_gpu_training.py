@@ -293,7 +293,7 @@ def test_bad_indices_are_recorded_and_skipped(dsa):
 
 
 # ------------------------------------------------------------------------------------------------ indexer objective
-@pytest.mark.parametrize("T,S,H,k,kind", [c for c in CASES if c[4] != "one" and c[1] > 1] + [(4, 50, 128, 256, "one")])
+@pytest.mark.parametrize("T,S,H,k,kind", CASES)
 def test_objective_backward(dsa, T, S, H, k, kind):
     q, c, idx, _ = _attention_case(T, S, H, k, kind, 5 * T + S)
     g = _gen(T)
@@ -311,8 +311,8 @@ def test_objective_backward(dsa, T, S, H, k, kind):
     kl = torch.where(on & (target > 0), target * (target.clamp(min=1e-300).log() - logq), 0.0).sum(1)
     kl.backward(dkl.double())
     want = torch.where(on, x.grad, 0.0)
-    if kind == "one":
-        assert (got.double().cpu() - want).abs().max() <= 1e-6 * float(dkl.abs().max())
+    if kind == "one" or S == 1:
+        assert (got == 0).all()                          # both distributions are the one entry, exactly
     else:
         assert _rel(got, want) <= L2_FP32
     assert (got.cpu()[~on] == 0).all()
