@@ -130,22 +130,11 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
 }
 
-// 32 rows of 8 N bf16 of a warp, one row a lane (packed in v), to rows `stride` bytes apart.  Turned in the warp's own
-// 512 N bytes of shared memory, so that N adjacent lanes write a row's piece (N = 8: whole 128-byte lines).
-template <int N>
-__device__ __forceinline__ void store_rows(uint8_t* buf, const uint32_t (&v)[4 * N], void* dst, long long stride) {
-  const int lane = lane_id();
-  // unit i of row r at unit i ^ x(r): eight lanes on end meet all 32 banks in both directions
-  auto at = [&](int r, int i) { return reinterpret_cast<uint4*>(buf + r * (16 * N) + ((i ^ (N == 8 ? r & 7 : (r >> 1) & 3)) << 4)); };
-#pragma unroll
-  for (int i = 0; i < N; ++i) *at(lane, i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  __syncwarp();
-  const int sub = lane / N, unit = lane % N;
-  char* to = static_cast<char*>(dst) + sub * stride + 16 * unit;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    __stwt(reinterpret_cast<uint4*>(to + (32 / N) * i * stride), *at((32 / N) * i + sub, unit));
-  __syncwarp();
+// one 32-byte store (32-byte aligned): a whole sector of the lane's own row
+__device__ __forceinline__ void st_global_32(void* at, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // Tiles [j0, j1) of a token with n_end slots that split `sp` of `splits` works on (`keys` a tile).
@@ -193,7 +182,7 @@ constexpr int OFF_TMEM = 512, OFF_ABORT = 516;
 // ---- mla_bwd_p_kernel
 namespace p {
 constexpr int THREADS = 576;            // w0 resident rows, w1 MMA, w2 w3 w8..13 gathers, w4..7 w14..17 probabilities
-constexpr int NS_MAX = 4;
+constexpr int NS_MAX = 5;
 constexpr int B_RES_FULL = 0, B_RES_EMPTY = B_RES_FULL + DCH, B_RING_FULL = B_RES_EMPTY + DCH;
 constexpr int B_RING_EMPTY = B_RING_FULL + NS_MAX, B_ACC_FULL = B_RING_EMPTY + NS_MAX, B_ACC_EMPTY = B_ACC_FULL + 4;
 constexpr int B_SUMS = B_ACC_EMPTY + 4;                       // objective: the other CTA's sums of a token (2 buffers)
@@ -206,12 +195,11 @@ template <bool KL> struct Map {
   static constexpr int RES_CHUNK = KL ? HCHUNK : CHUNK;       // a 64-dim chunk of the resident rows (the last: 64 rows)
   static constexpr int RES = 8 * RES_CHUNK + HCHUNK;          // 72 KB, 136 KB
   static constexpr int SC = KL ? 3 : 1;                       // gathered chunks (16 KB) of a ring stage
-  static constexpr int NS = KL ? 3 : 4;                       // ring stages
+  static constexpr int NS = KL ? 3 : 5;                       // ring stages
   static constexpr int WPS = KL ? 8 : 2;                      // warps that fill a stage
   static constexpr int NACC = KL ? 4 : 2;                     // accumulators of 128, 256 columns
   static constexpr int OFF_RING = OFF_RES + RES;
-  static constexpr int OFF_TURN = OFF_RING + NS * SC * CHUNK;  // store_rows: 2 KB of each of eight warps
-  static constexpr int SMEM = OFF_TURN + (KL ? 0 : 8 * 2048) + 1024;
+  static constexpr int SMEM = OFF_RING + NS * SC * CHUNK + 1024;
   static_assert(DCH % SC == 0 && SC * 32 % WPS == 0 && SC * 32 / WPS <= 32, "stage split");
 };
 static_assert(Map<false>::SMEM <= 232448 && Map<true>::SMEM <= 232448, "shared memory per CTA");
@@ -540,15 +528,15 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         };
         if constexpr (KL) {
           float a0 = 0.f, a1 = 0.f;
-          for (int c = 0; c < p.HP / 64; ++c) {
-            uint32_t v[64];
-            tmem_ld32(acc + 64 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-            tmem_ld32(acc + 64 * c + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+#pragma unroll 1
+          for (int c = 0; c < p.HP / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld32(acc + 32 * c, v);
             tmem_wait_ld();
-            if (c == p.HP / 64 - 1) release();
+            if (c == p.HP / 32 - 1) release();
 #pragma unroll
-            for (int i = 0; i < 64; i += 4) {
-              const float4 l = *reinterpret_cast<const float4*>(hs + 64 * c + i);
+            for (int i = 0; i < 32; i += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(hs + 32 * c + i);
               a0 += ex2_approx(fmaf(__uint_as_float(v[i]), p.scale_log2, l.x));
               a1 += ex2_approx(fmaf(__uint_as_float(v[i + 1]), p.scale_log2, l.y));
               a0 += ex2_approx(fmaf(__uint_as_float(v[i + 2]), p.scale_log2, l.z));
@@ -570,9 +558,8 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
         } else {
           // the warp's 32 keys; kp is a multiple of 128: they lie on one side of it
-          uint8_t* turn = cta.smem + M::OFF_TURN + (4 * grp + quad) * 2048;
           const int slot0 = slot - lane;
-          uint16_t* out = p.pds + (static_cast<long long>(t) * p.kp + slot0) * (2 * p.HP);
+          uint16_t* out = p.pds + (static_cast<long long>(t) * p.kp + slot) * (2 * p.HP);
           const uint32_t keep = valid ? 0xffffffffu : 0u;     // an empty slot's S or dP may be NaN: its bits go
 #pragma unroll 1
           for (int c = 0; c < p.HP / 32; ++c) {
@@ -596,9 +583,15 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               ds[i / 2 + 1] = pack_bf16(p2 * fmaf(__uint_as_float(d[i + 2]), p.scale, m.z),
                                         p3 * fmaf(__uint_as_float(d[i + 3]), p.scale, m.w)) & keep;
             }
+            // Straight from the lanes' own rows, a sector a store.  Turned in shared memory to 64-byte pieces the stores are
+            // as fast, but the 16 KB that takes are a ring stage (1274 us for 2048 tokens, against 1159 so); staged for TMA
+            // they were slower, and 16 bytes a store took 1466 in an earlier form against 1252.
             if (slot0 < p.kp) {
-              store_rows<4>(turn, ds, out + 32 * c, 4 * p.HP);
-              store_rows<4>(turn, ps, out + p.HP + 32 * c, 4 * p.HP);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                st_global_32(out + 32 * c + 16 * i, ds + 8 * i);
+                st_global_32(out + p.HP + 32 * c + 16 * i, ps + 8 * i);
+              }
             }
           }
         }
