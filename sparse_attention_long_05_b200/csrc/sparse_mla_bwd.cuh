@@ -196,7 +196,7 @@ template <bool KL> struct Map {
   static constexpr int RES = 8 * RES_CHUNK + HCHUNK;          // 72 KB, 136 KB
   static constexpr int SC = KL ? 3 : 1;                       // gathered chunks (16 KB) of a ring stage
   static constexpr int NS = KL ? 3 : 5;                       // ring stages
-  static constexpr int WPS = KL ? 8 : 2;                      // warps that fill a stage
+  static constexpr int WPS = KL ? 4 : 2;                      // warps that fill a stage
   static constexpr int NACC = KL ? 4 : 2;                     // accumulators of 128, 256 columns
   static constexpr int OFF_RING = OFF_RES + RES;
   static constexpr int SMEM = OFF_RING + NS * SC * CHUNK + 1024;
