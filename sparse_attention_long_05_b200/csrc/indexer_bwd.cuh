@@ -12,7 +12,7 @@
 // held in fp32.  G qs and G ks are rounded to bf16 once (2^-9).  dw is summed from the fp32 x.  Per token: 16 tiles of
 // 128 keys, each x -> G -> (dk, dq); x of the next tile is issued before G of this one is waited for.
 // HBM sees each entry's contribution to dk twice (written here, summed by scatter.cuh).
-// Measured on 2048 tokens of a 32K sequence, k = 2048, 64 heads: 522 us here, 231 for the sums, 91 for the table; bound by the
+// Measured on 2048 tokens of a 32K sequence, k = 2048, 64 heads: 523 us here, 231 for the sums, 116 for the table; bound by the
 // latency of G's chain (x from tensor memory -> G to shared memory) and by the issue slots its warps share.
 // The small indexer (4 heads, 64 dims) runs in the same layout, its missing heads and dims zero.
 #pragma once

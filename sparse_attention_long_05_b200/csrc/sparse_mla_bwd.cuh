@@ -23,9 +23,9 @@
 // P and dS are rounded to bf16, by at most 2^-9 of their value, as the operands of the second products have to be.  All
 // sums are fp32.
 //
-// Measured on 2048 tokens of a 32K sequence, k = 2048, 128 heads (launches one by one): P and dS 1152 us, contributions
-// 1407, dq 616, their sum 888, delta and the table 173; 4.5 to 4.9 ms in a row (2.95 TFLOP: 0.44 to 0.47 of the sustained
-// bf16 rate).  The objective's gradient takes 555 us (1.1 PFLOP/s).  The two pair kernels are bound by shared memory: operand fetches of the tensor cores and the warps' own
+// Measured on 2048 tokens of a 32K sequence, k = 2048, 128 heads (launches one by one): P and dS 1141 us, contributions
+// 1403, dq 622, their sum 887, delta and the table 170; 4.5 to 4.9 ms in a row (2.95 TFLOP: 0.43 to 0.47 of the sustained
+// bf16 rate).  The objective's gradient takes 591 us (1.05 PFLOP/s).  The two pair kernels are bound by shared memory: operand fetches of the tensor cores and the warps' own
 // traffic (turned rows, staged pieces) take about 45 % of its cycles each.  dq reads 40 KB a stage at 77 GB/s an SM, what
 // gathers and tiles together reach here; the sum runs at 0.85 of HBM.
 #pragma once
