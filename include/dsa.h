@@ -155,6 +155,8 @@ DSA_API size_t dsa_sparse_mla_attn_backward_workspace_size(int T, int S, int H, 
  * A row of c selected twice by a token counts twice, as in the forward.  A token without entries (lse = -INFINITY)
  * has dq = 0.  An entry outside [-1, S) is treated as -1 and recorded as DSA_ERR_BAD_INDEX.
  * P and dS are rounded to bf16 once, each entry's contribution to dc to about 11 bits; every sum is fp32.
+ * 16-bit arrays and idx are 16-byte aligned, fp32 arrays to their type; results share no memory with inputs (here and in
+ * the two backward passes below).
  *   ws: dsa_sparse_mla_attn_backward_workspace_size() bytes, 16-byte aligned.  Long T are worked through in chunks of
  *     tokens (about 4 GiB of workspace and, with more than one, an fp32 copy of dc).
  */

@@ -25,8 +25,9 @@
 //
 // Measured on 2048 tokens of a 32K sequence, k = 2048, 128 heads (launches one by one): P and dS 1141 us, contributions
 // 1403, dq 622, their sum 887, delta and the table 170; 4.5 to 4.9 ms in a row (2.95 TFLOP: 0.43 to 0.47 of the sustained
-// bf16 rate).  The objective's gradient takes 591 us (1.05 PFLOP/s).  The two pair kernels are bound by shared memory: operand fetches of the tensor cores and the warps' own
-// traffic (turned rows, staged pieces) take about 45 % of its cycles each.  dq reads 40 KB a stage at 77 GB/s an SM, what
+// bf16 rate).  The objective's gradient takes 591 us (1.05 PFLOP/s).  The two pair kernels are bound by
+// shared memory: in the contributions' the operand fetches of the tensor cores and the warps' own traffic (staged pieces)
+// take about 45 % of its cycles each.  dq reads 40 KB a stage at 77 GB/s an SM, what
 // gathers and tiles together reach here; the sum runs at 0.85 of HBM.
 #pragma once
 #include "common.cuh"
@@ -1044,8 +1045,10 @@ __global__ void __launch_bounds__(256) join_splits_kernel(const float* part, con
   }
   if (i < width)
     *reinterpret_cast<uint2*>(out + static_cast<long long>(t) * width + i) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
-  else
-    *reinterpret_cast<float4*>(out_tail + static_cast<long long>(t) * tail + i - width) = s;
+  else {
+    float* to = out_tail + static_cast<long long>(t) * tail + i - width;   // a caller's array: aligned to its type only
+    to[0] = s.x; to[1] = s.y; to[2] = s.z; to[3] = s.w;
+  }
 }
 
 // What the other kernels of a chunk start from: delta[t][h] = dout . out over the 512 value dims (one warp a row, eight rows

@@ -369,6 +369,38 @@ def test_index_scores_backward(dsa, heads, dim, T, S, k, kind, scaled):
     assert all(torch.equal(a, b) for a, b in zip((dq, dk, dw), again))
 
 
+def _shifted(t):
+    """The same fp32 values in memory that is aligned to 4 bytes only."""
+    at = torch.empty(t.numel() + 1, device="cuda")[1:].view(t.shape)
+    assert at.data_ptr() % 16 == 4
+    return at.copy_(t)
+
+
+def test_fp32_arrays_at_any_address(dsa):
+    """fp32 arguments need the alignment of their type, no more: few tokens (whose items are split and joined) and many
+    give the same bits from arrays that start 4 bytes behind a 16-byte boundary."""
+    for heads, dim in ((64, 128), (4, 64)):
+        for T in (3, 400):
+            case = _indexer_case(T, 700, heads, dim, 640, "causal", True, 11 + T)
+            q, qs, kk, ks, w, idx, dsel = (t.cuda() for t in case)
+            want = dsa.dsa_indexer_scores_backward(q, qs, kk, ks, w, idx, dsel)
+            dw = _shifted(torch.zeros_like(w))
+            got = dsa.dsa_indexer_scores_backward(q, _shifted(qs), kk, _shifted(ks), _shifted(w), idx, _shifted(dsel),
+                                                  dw=dw)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for T in (3, 200):
+        q, c, idx, dout = (t.cuda() for t in _attention_case(T, 700, 128, 640, "causal", 13 + T))
+        out, lse = dsa.dsa_sparse_mla_attn(q, c, idx, SCALE)[:2]
+        want = dsa.dsa_sparse_mla_attn_backward(q, c, idx, out, lse, dout, SCALE)
+        got = dsa.dsa_sparse_mla_attn_backward(q, c, idx, out, _shifted(lse), dout, SCALE)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        sel, dkl = torch.randn(T, 640, device="cuda"), torch.randn(T, device="cuda")
+        want = dsa.dsa_indexer_kl_backward(q, c, idx, sel, lse, dkl, SCALE)
+        got = dsa.dsa_indexer_kl_backward(q, c, idx, _shifted(sel), _shifted(lse), _shifted(dkl), SCALE,
+                                          dsel=_shifted(torch.zeros_like(sel)))
+        assert torch.equal(got, want)
+
+
 def test_index_scores_backward_is_the_slope_of_the_forward(dsa):
     # dw against the forward kernel itself: the scores are linear in w
     q, qs, kk, ks, w, idx, dsel = _indexer_case(6, 500, 64, 128, 192, "causal", True, 4)
