@@ -24,7 +24,7 @@
 // sums are fp32.
 //
 // Measured on 2048 tokens of a 32K sequence, k = 2048, 128 heads (launches one by one): P and dS 1141 us, contributions
-// 1403, dq 622, their sum 887, delta and the table 170; 4.5 to 4.9 ms in a row (2.95 TFLOP: 0.43 to 0.47 of the sustained
+// 1403, dq 622, their sum 887, delta and the table 170; 4.5 to 5.0 ms in a row (2.95 TFLOP: 0.42 to 0.47 of the sustained
 // bf16 rate).  The objective's gradient takes 591 us (1.05 PFLOP/s).  The two pair kernels are bound by
 // shared memory: in the contributions' the operand fetches of the tensor cores and the warps' own traffic (staged pieces)
 // take about 45 % of its cycles each.  dq reads 40 KB a stage at 77 GB/s an SM, what
