@@ -662,10 +662,15 @@ dsa_status_t run_decode(int B, const DecodeLayout& lay, const int32_t* ctx_len, 
 }
 
 // ------------------------------------------------------------------------------------------ backward passes
-// Hands out 256-byte aligned pieces of a workspace (null base: only counts).
+// Hands out 256-byte aligned pieces of a workspace that starts on 16 bytes (null base: only counts).  The 32-byte stores of
+// P and dS need more than the 16 bytes a caller's workspace is asked for, so the first piece starts at its first 256-byte
+// boundary; bytes() counts the most that skips, whatever the address.
 struct Carve {
   char* base;
   size_t at = 0;
+  explicit Carve(void* ws)
+      : base(reinterpret_cast<char*>(align_up(reinterpret_cast<uintptr_t>(ws), 256))) {}
+  size_t bytes() const { return at + 256 - 16; }
   template <typename X>
   X* take(size_t n) {
     X* r = base ? reinterpret_cast<X*>(base + at) : nullptr;
@@ -787,14 +792,14 @@ AttnBwdWs attn_bwd_ws(void* ws, int T, int64_t S, int H, int k) {
   a.HP = round_up(H, 64);
   a.kp = round_up(k, 128);
   a.Tc = bwd_chunk(T, S, a.kp, mbw::D * 2 + 4 * size_t(a.HP));
-  Carve w{static_cast<char*>(ws)};
+  Carve w(ws);
   a.sc = carve_scatter(w, a.Tc, S, a.kp, mbw::D, a.Tc < T);
   a.delta = w.take<float>(size_t(a.Tc) * H);
   a.pds = w.take<uint16_t>(size_t(a.Tc) * a.kp * 2 * a.HP);
   // 3 stages of 64 keys are about what an item's start and end take
   a.dq_splits = a.Tc < T ? 1 : choose_joined_splits(3ll * T, num_sms(), a.kp / mbw::dq::KT, 6.0);
   a.dq_part = a.dq_splits > 1 ? w.take<float>(size_t(T) * a.dq_splits * H * mbw::D) : nullptr;
-  a.bytes = w.at;
+  a.bytes = w.bytes();
   return a;
 }
 
@@ -864,14 +869,18 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
   return DSA_OK;
 }
 
-size_t kl_bwd_ws_bytes(int T) { return align_up(size_t(T) * 4, 256); }
+size_t kl_bwd_ws_bytes(int T) {
+  Carve w(nullptr);
+  w.take<int>(T);
+  return w.bytes();
+}
 
 dsa_status_t run_kl_bwd(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx, const float* sel,
                         const float* lse, const float* dkl, int T, int H, int k, float scale, float* dsel, void* ws,
                         cudaStream_t st) {
   CUtensorMap tq, tc;
   if (!make_heads_map(&tq, q, T, H, mbw::D) || !make_rows_map(&tc, c, S, mbw::D, 1)) return DSA_ERR_CUDA;
-  Carve w{static_cast<char*>(ws)};
+  Carve w(ws);
   MlaBwdParams p{};
   int* n_end = w.take<int>(T);
   p.idx = idx;
@@ -912,11 +921,11 @@ IndexBwdWs index_bwd_ws(void* ws, int T, int64_t S, int H_I, int d_I, int k) {
   IndexBwdWs a{};
   a.kp = round_up(k, 128);
   a.Tc = bwd_chunk(T, S, a.kp, size_t(d_I) * 2);
-  Carve w{static_cast<char*>(ws)};
+  Carve w(ws);
   a.sc = carve_scatter(w, a.Tc, S, a.kp, d_I, a.Tc < T);
   a.splits = a.Tc < T ? 1 : choose_joined_splits(T, num_sms(), a.kp / ixb::NK, 2.0);
   a.part = a.splits > 1 ? w.take<float>(size_t(T) * a.splits * (size_t(H_I) * d_I + H_I)) : nullptr;
-  a.bytes = w.at;
+  a.bytes = w.bytes();
   return a;
 }
 

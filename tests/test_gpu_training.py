@@ -401,6 +401,42 @@ def test_fp32_arrays_at_any_address(dsa):
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("off", [16, 48, 240])
+def test_workspaces_at_any_16_bytes(dsa, off):
+    """A workspace of just the stated size, `off` bytes behind a 256-byte boundary: the same bits as one on it, and
+    nothing written before or behind it."""
+    def workspace(need):
+        buf = torch.full((need + 512,), 0xab, dtype=torch.uint8, device="cuda")
+        assert buf.data_ptr() % 256 == 0
+        return buf, buf[off:off + need]
+
+    def untouched(buf, need):
+        return bool((buf[:off] == 0xab).all()) and bool((buf[off + need:] == 0xab).all())
+
+    for T, S, H, k in ((3, 500, 128, 320), (40, 700, 24, 192), (200, 700, 128, 640)):
+        q, c, idx, dout = (t.cuda() for t in _attention_case(T, S, H, k, "causal", 3 * T))
+        out, lse = dsa.dsa_sparse_mla_attn(q, c, idx, SCALE)
+        need = dsa.dsa_sparse_mla_attn_backward_workspace_size(T, S, H, k)
+        buf, ws = workspace(need)
+        want = dsa.dsa_sparse_mla_attn_backward(q, c, idx, out, lse, dout, SCALE)
+        got = dsa.dsa_sparse_mla_attn_backward(q, c, idx, out, lse, dout, SCALE, ws=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and untouched(buf, need)
+        sel = torch.randn(T, k, generator=_gen(T)).cuda()
+        need = dsa.dsa_indexer_kl_backward_workspace_size(T)
+        buf, ws = workspace(need)
+        want = dsa.dsa_indexer_kl_backward(q, c, idx, sel, lse, None, SCALE)
+        assert torch.equal(dsa.dsa_indexer_kl_backward(q, c, idx, sel, lse, None, SCALE, ws=ws), want)
+        assert untouched(buf, need)
+        for heads, dim in ((64, 128), (4, 64)):
+            case = [t.cuda() for t in _indexer_case(T, S, heads, dim, k, "causal", True, T)]
+            need = dsa.dsa_indexer_scores_backward_workspace_size(T, S, heads, dim, k)
+            buf, ws = workspace(need)
+            want = dsa.dsa_indexer_scores_backward(*case)
+            got = dsa.dsa_indexer_scores_backward(*case, ws=ws)
+            assert all(torch.equal(a, b) for a, b in zip(got, want)) and untouched(buf, need)
+    assert dsa.dsa_get_device_status() == 0
+
+
 def test_index_scores_backward_is_the_slope_of_the_forward(dsa):
     # dw against the forward kernel itself: the scores are linear in w
     q, qs, kk, ks, w, idx, dsel = _indexer_case(6, 500, 64, 128, 192, "causal", True, 4)

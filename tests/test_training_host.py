@@ -93,6 +93,18 @@ def test_index_scores_backward_workspace(lib):
     assert size(50000, 32768, 64, 128, 2048) <= (4 << 30) + (1 << 27) + 32768 * 128 * 4
 
 
+def test_workspaces_leave_room_to_align_their_pieces(lib):
+    """Every piece of a workspace takes a multiple of 256 bytes, from the workspace's first 256-byte boundary on; a
+    workspace may start at any multiple of 16, so up to 240 bytes in front of that boundary come on top."""
+    for T, S, H, k in ((1, 8, 1, 128), (4, 100, 8, 192), (300, 70001, 16, 2048)):
+        assert lib.dsa_sparse_mla_attn_backward_workspace_size(T, S, H, k) % 256 == 240
+        assert lib.dsa_indexer_kl_backward_workspace_size(T) % 256 == 240
+        assert lib.dsa_indexer_scores_backward_workspace_size(T, S, 64, 128, k) % 256 == 240
+        assert lib.dsa_indexer_scores_backward_workspace_size(T, S, 4, 64, k) % 256 == 240
+    need = lib.dsa_indexer_kl_backward_workspace_size(4)
+    assert lib.dsa_indexer_kl_backward(*dict(KL, ws=P(32), ws_bytes=need - 1).values()) == WS
+
+
 # ------------------------------------------------------------------------------------------- rotary positions
 ROPE = dict(x=ONE, xt=128, xh=64, out=P(1 << 30), ot=128, oh=64, pos=None, pos0=0, f=ONE, T=4, H=2, D=64, off=0, R=64, inter=1,
             m=1.0, dtype=0, stream=None)
