@@ -426,6 +426,7 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
             tma_store_2d(&tm_out, sbase + OFF_OUT + c * KCH + quad * 32 * 128, 64 * c, t * p.kp + j * NK + quad * 32);
             bulk_commit();
           }
+          __syncwarp();                      // the warp's next load of tensor memory wants all its lanes
         }
       }
       if (!ok) break;

@@ -850,6 +850,7 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
             tma_store_2d(&tm_out, sbase + area, 256 * d3 + 64 * c, t * p.kp + slot0);
             bulk_commit();
           }
+          __syncwarp();                      // the warp's next load of tensor memory wants all its lanes
           ++put;
         }
       }
@@ -1004,8 +1005,9 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
         uint32_t v[32];
         tmem_ld32(lane_addr + tmem + 256 * ab + 32 * c, v);
         tmem_wait_ld();
-        if (h >= p.H) continue;
-        if (p.splits == 1) {
+        if (h >= p.H) {
+          // a head that only fills up the tile: nothing to store
+        } else if (p.splits == 1) {
           uint4* dst = reinterpret_cast<uint4*>(p.dq + at + 32 * c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -1017,6 +1019,7 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
 #pragma unroll
           for (int i = 0; i < 8; ++i) dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
+        __syncwarp();                        // the warp's next load of tensor memory wants all its lanes
       }
       tc_fence_before();
       __syncwarp();
