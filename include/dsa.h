@@ -230,7 +230,9 @@ enum { DSA_BF16 = 0, DSA_FP32 = 1 };
  * i < rot_dim / 2 (HOST array).  factor > 1 scales them for contexts `factor` times as long as the orig_len positions
  * a model was trained on: pairs that turn less than turns_slow times over orig_len positions are slowed by factor,
  * pairs that turn more than turns_fast times are kept, those between are blended linearly in i (usual values: 32 and
- * 1).  *mscale (may be NULL) receives 0.1 ln(factor) + 1, the usual factor on rotated values, or 1 when factor is 1.
+ * 1): inv_freq[i] (1 - r + r / factor), r = (i - low) / (high - low) within [0, 1], where with
+ * pair(n) = rot_dim ln(orig_len / (2 pi n)) / (2 ln base), the index at which a pair turns n times over orig_len positions,
+ * low = floor(pair(turns_fast)) and high = ceil(pair(turns_slow)), whether pairs of these indices exist or not.  *mscale (may be NULL) receives 0.1 ln(factor) + 1, the usual factor on rotated values, or 1 when factor is 1.
  */
 DSA_API dsa_status_t dsa_rope_frequencies(int rot_dim, double base, double factor, int orig_len, double turns_fast,
                                           double turns_slow, double* inv_freq, float* mscale);

@@ -1794,19 +1794,20 @@ dsa_status_t dsa_rope_frequencies(int rot_dim, double base, double factor, int o
   if (factor > 1.0 && (orig_len <= 0 || !(turns_slow > 0.0) || !(turns_fast > turns_slow) || !std::isfinite(turns_fast)))
     return DSA_ERR_INVALID_ARG;
   const int n = rot_dim / 2;
-  double low = 0.0, high = 0.0;
+  double low = 0.0, high = 1.0;
   if (factor > 1.0) {
-    // pair index whose wavelength makes `turns` turns over orig_len positions
+    // pair index whose wavelength makes `turns` turns over orig_len positions.  Either end of the blend may lie
+    // outside the pairs that there are: it is then cut off, not squeezed into them.
     auto pair_of = [&](double turns) {
       return rot_dim * std::log(orig_len / (turns * 6.283185307179586)) / (2.0 * std::log(base));
     };
-    low = std::max(0.0, std::floor(pair_of(turns_fast)));
-    high = std::min(n - 1.0, std::ceil(pair_of(turns_slow)));
+    low = std::floor(pair_of(turns_fast));
+    high = std::ceil(pair_of(turns_slow));
   }
   for (int i = 0; i < n; ++i) {
     const double f = std::pow(base, -2.0 * i / rot_dim);
     double slow = 0.0;
-    if (factor > 1.0) slow = std::min(1.0, std::max(0.0, (i - low) / std::max(high - low, 1e-3)));
+    if (factor > 1.0) slow = std::min(1.0, std::max(0.0, (i - low) / std::max(high - low, 1.0)));
     inv_freq[i] = f / factor * slow + f * (1.0 - slow);
   }
   if (mscale) *mscale = factor > 1.0 ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;

@@ -151,6 +151,29 @@ def test_rope_frequencies():
         assert (ratio[1:] <= ratio[:-1] + 1e-12).all()
 
 
+@pytest.mark.parametrize("R,base,factor,orig,fast,slow", [
+    (64, 1e4, 40.0, 65536, 32.0, 1.0), (64, 1e4, 40.0, 163840, 32.0, 1.0), (16, 1e4, 8.0, 32768, 32.0, 1.0),
+    (64, 1e4, 4.0, 1_300_000, 32.0, 1.0), (64, 1e4, 40.0, 4096, 32.0, 1.0), (128, 1e6, 16.0, 8192, 32.0, 1.0),
+    (2, 5e5, 16.0, 8192, 32.0, 1.0), (2, 5e5, 16.0, 64, 32.0, 1.0), (64, 1e4, 8.0, 2_000_000_000, 32.0, 1.0),
+    (64, 1e4, 8.0, 100, 32.0, 1.0), (64, 1e4, 8.0, 4, 32.0, 1.0), (32, 150000.0, 2.0, 4096, 8.0, 0.5)])
+def test_rope_frequencies_blend(R, base, factor, orig, fast, slow):
+    """The blend written out pair by pair, also where its ends lie outside the pairs that there are: with orig_len 65536 the
+    slowest of 32 pairs still turns 1.39 times and must not be slowed by the whole factor."""
+    import sparse_attention_long_05_b200 as dsa
+    got, _ = dsa.dsa_rope_frequencies(R, base, factor, orig, fast, slow)
+    low = math.floor(R * math.log(orig / (2 * math.pi * fast)) / (2 * math.log(base)))
+    high = math.ceil(R * math.log(orig / (2 * math.pi * slow)) / (2 * math.log(base)))
+    for i in range(R // 2):
+        f = base ** (-2 * i / R)
+        r = min(1.0, max(0.0, (i - low) / (high - low)))
+        # log, pow and the blend in fp64 on both sides: a few units of 2^-53 each
+        assert float(got[i]) == pytest.approx(f * (1 - r + r / factor), rel=1e-13)
+        turns = orig * f / (2 * math.pi)
+        assert turns <= fast or r == 0.0                          # kept
+        assert turns >= slow or r == 1.0                          # slowed by the whole factor
+        assert turns <= slow * base ** (2 / R) or r < 1.0         # and no pair a whole index away from those
+
+
 def test_python_checks_name_the_argument():
     # CPU tensors never reach the library; shapes and types are checked before any pointer is taken
     import sparse_attention_long_05_b200 as dsa
