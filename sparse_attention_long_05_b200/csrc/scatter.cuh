@@ -32,19 +32,16 @@ __device__ __forceinline__ void scatter_clear(uint4* table, long long n) {
 }
 // 64 values as pieces of eight: fp16 of x 2^(141 - E), E the exponent of the largest magnitude of the 64 (kept where
 // 2^(141 - E) and its inverse are normal), bit i of E in the lowest bit of a piece's value 2 i, bit i + 4 in that of value
-// 2 i + 1.  E = 0: 64 values with infinities among them, unscaled.
+// 2 i + 1.  Infinities and NaN pass through the scale.  An infinity beside finite values is a sum that left fp32's range
+// (an infinite operand leaves nothing finite in the row): it counts as 2^127 to 2^128, and so scaled it is still infinite.
 __device__ __forceinline__ void scatter_pack64(const uint32_t (&v)[64], uint32_t (&w)[32]) {
   float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 64; i += 2)
     top[(i >> 1) & 3] = fmaxf(fmaxf(top[(i >> 1) & 3], fabsf(__uint_as_float(v[i]))), fabsf(__uint_as_float(v[i + 1])));
-  const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-  uint32_t e = max(15u, __float_as_uint(most) >> 23);
-  float f = __uint_as_float((268u - e) << 23);
-  if (e > 254u) {
-    e = 0;
-    f = 1.f;
-  }
+  const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));      // (NaN are not looked at)
+  const uint32_t e = min(254u, max(15u, __float_as_uint(most) >> 23));
+  const float f = __uint_as_float((268u - e) << 23);
   const uint32_t bits = e | (e << 12);
   const uint32_t b4[4] = {bits & 0x00010001u, (bits >> 1) & 0x00010001u, (bits >> 2) & 0x00010001u,
                           (bits >> 3) & 0x00010001u};
@@ -63,7 +60,7 @@ __device__ __forceinline__ void scatter_add(uint4 v, float (&sum)[8]) {
   const uint32_t t = (w[0] & 0x00010001u) | ((w[1] & 0x00010001u) << 1) | ((w[2] & 0x00010001u) << 2) |
                      ((w[3] & 0x00010001u) << 3);
   const uint32_t e = (t | (t >> 12)) & 0xffu;
-  const float f = e ? __uint_as_float((e - 14u) << 23) : 1.f;
+  const float f = __uint_as_float((e - 14u) << 23);      // (e = 0 in the zeros that stand for no entry: -2^115, 0 f = 0)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t x = w[i] & 0xfffefffeu;

@@ -281,6 +281,40 @@ def test_infinite_gradients_reach_what_they_touch(dsa):
     assert torch.equal(dq2.cpu()[same], dq.cpu()[same]) and not torch.isfinite(dq2.cpu()[1, 3]).any()
 
 
+@pytest.mark.parametrize("S", [2, 200])                  # the sums of long and of short lists
+def test_values_beside_an_infinity_are_kept(dsa, S):
+    """A contribution that overflows fp32 in one dim is finite, and exact, in the dims beside it: powers of two, with two
+    keys of equal weight."""
+    q, c, dout = torch.zeros(1, 1, D), torch.zeros(S, D), torch.zeros(1, 1, DV)
+    q[0, 0, 5], q[0, 0, 7] = 2.0 ** 13, 1.0              # the keys are 0 there: both logits are 0, P = 1/2
+    c[0, 0], c[1, 0] = 1.0, -1.0
+    dout[0, 0, 0] = 2.0 ** 118                           # dP = 2^118 and its negative, delta = 0, dS = scale / 2 of that
+    idx = torch.full((1, 128), -1, dtype=torch.int32)
+    idx[0, :2] = torch.tensor([0, 1])
+    want = torch.zeros(S, D)
+    want[0, 0], want[0, 7], want[0, 5] = 2.0 ** 117, 2.0 ** 116, math.inf
+    want[1, 0], want[1, 7], want[1, 5] = 2.0 ** 117, -2.0 ** 116, -math.inf
+    qd, cd, dd = (t.bfloat16().cuda() for t in (q, c, dout))
+    out, lse = dsa.dsa_sparse_mla_attn(qd, cd, idx.cuda(), 0.5)
+    _, dc = dsa.dsa_sparse_mla_attn_backward(qd, cd, idx.cuda(), out, lse, dd, 0.5)
+    # P, dS and the result are rounded to bf16: 2^-8 of a value at most, each
+    fin = want.isfinite()
+    assert ((dc.float().cpu() - want)[fin].abs() <= want[fin].abs() * 3 * 2.0 ** -8).all()
+    assert torch.equal(dc.float().cpu()[~fin], want[~fin])
+    # index scores: one live head, whose query has one large dim
+    qi, ki, w = torch.zeros(1, 4, 64), torch.zeros(S, 64), torch.zeros(1, 4)
+    qi[0, 0], qi[0, 0, 5], ki[0], w[0, 0] = 1.0, 448.0, 1.0, 1.0
+    sel = torch.zeros(1, 128)
+    sel[0, 0] = 2.0 ** 120
+    idx[0, 1] = -1
+    dq, dk, _ = dsa.dsa_indexer_scores_backward(qi.to(torch.float8_e4m3fn).cuda(), None, ki.to(torch.float8_e4m3fn).cuda(),
+                                                None, w.cuda(), idx.cuda(), sel.cuda())
+    want = torch.zeros(S, 64)
+    want[0], want[0, 5] = 2.0 ** 120, math.inf
+    assert torch.equal(dk.float().cpu(), want) and (dq[0, 0].float() == 2.0 ** 120).all()
+    assert dsa.dsa_get_device_status() == 0
+
+
 def test_bad_indices_are_recorded_and_skipped(dsa):
     q, c, idx, dout = _attention_case(4, 300, 16, 128, "causal", 12)
     _, _, dq, dc = _run_attention(dsa, q, c, idx, dout)
