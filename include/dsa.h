@@ -154,7 +154,7 @@ DSA_API size_t dsa_sparse_mla_attn_backward_workspace_size(int T, int S, int H, 
  *     a caller that accumulates adds them itself.  The selection and lse pass no gradient on.
  * A row of c selected twice by a token counts twice, as in the forward.  A token without entries (lse = -INFINITY)
  * has dq = 0.  An entry outside [-1, S) is treated as -1 and recorded as DSA_ERR_BAD_INDEX.
- * P and dS are rounded to bf16 once, each entry's contribution to dc to about 11 bits; every sum is fp32.
+ * P and dS are rounded to bf16 once, each entry's contribution to dc to 10 bits; every sum is fp32.
  * 16-bit arrays and idx are 16-byte aligned, fp32 arrays to their type; results share no memory with inputs (here and in
  * the two backward passes below).
  *   ws: dsa_sparse_mla_attn_backward_workspace_size() bytes, 16-byte aligned.  Long T are worked through in chunks of
@@ -212,7 +212,7 @@ DSA_API size_t dsa_indexer_scores_backward_workspace_size(int T, int S, int H_I,
  *     where idx is -1), as dsa_indexer_kl_backward writes it;
  *   dq [T, H_I, d_I] bf16, dk [S, d_I] bf16, dw [T, H_I] fp32 (out); every row is written.
  * k as in dsa_sparse_mla_attn; entries outside [-1, S) count as -1 and are recorded as DSA_ERR_BAD_INDEX.  The weights
- * dsel w_j q_scale and dsel w_j k_scale are rounded to bf16 once, each entry's contribution to dk to about 11 bits; sums
+ * dsel w_j q_scale and dsel w_j k_scale are rounded to bf16 once, each entry's contribution to dk to 10 bits; sums
  * are fp32, and dw is computed in fp32 throughout.
  *   ws: dsa_indexer_scores_backward_workspace_size() bytes, 16-byte aligned.
  */

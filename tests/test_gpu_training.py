@@ -281,6 +281,29 @@ def test_infinite_gradients_reach_what_they_touch(dsa):
     assert torch.equal(dq2.cpu()[same], dq.cpu()[same]) and not torch.isfinite(dq2.cpu()[1, 3]).any()
 
 
+@pytest.mark.parametrize("T,S,H,k", [(64, 600, 16, 320), (24, 24000, 16, 320)])    # long lists, short lists
+def test_gradients_are_not_biased(dsa, T, S, H, k):
+    """sum(got want) / sum(want^2) - 1: roundings that go up as often as down leave 2^-8 / sqrt(n) of it, n = T k H or more
+    independent ones (1.2e-5 at most here); cutting each contribution off at ten bits leaves -3.5e-4."""
+    def shift(got, want):
+        got, want = got.double().cpu(), want.double().cpu()
+        return float((got * want).sum() / (want * want).sum()) - 1
+
+    q, c, idx, dout = _attention_case(T, S, H, k, "causal", 2 * T)
+    out, lse, dq, dc = _run_attention(dsa, q, c, idx, dout)
+    want_q, want_c = _formula(q, c, idx, out.cpu(), lse.cpu(), dout)
+    assert abs(shift(dq, want_q)) <= 1e-4 and abs(shift(dc, want_c)) <= 1e-4
+    for scaled in (True, False):
+        qi, qs, kk, ks, w, idx, dsel = _indexer_case(T, S, 64, 128, k, "causal", scaled, 3 * T)
+        dq, dk, dw = dsa.dsa_indexer_scores_backward(*[None if t is None else t.cuda() for t in (qi, qs, kk, ks, w, idx, dsel)])
+        qf, kf = qi.float().double(), kk.float().double()
+        if scaled:
+            qf, kf = qf * qs.double()[:, None, None], kf * ks.double()[:, None]
+        qf, kf, wf = qf.requires_grad_(), kf.requires_grad_(), w.double().requires_grad_()
+        (_indexer_scores(qf, kf, wf, idx) * torch.where(idx >= 0, dsel.double(), 0.0)).sum().backward()
+        assert max(abs(shift(dq, qf.grad)), abs(shift(dk, kf.grad)), abs(shift(dw, wf.grad))) <= 1e-4
+
+
 @pytest.mark.parametrize("S", [2, 200])                  # the sums of long and of short lists
 def test_values_beside_an_infinity_are_kept(dsa, S):
     """A contribution that overflows fp32 in one dim is finite, and exact, in the dims beside it: powers of two, with two
