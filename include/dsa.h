@@ -245,8 +245,9 @@ DSA_API dsa_status_t dsa_rope_frequencies(int rot_dim, double base, double facto
  * dsa_rope_backward is the transpose: dx from the gradient dout, with the same mscale.
  *   x, out: T tokens x H heads x D dims of `dtype` (DSA_BF16, DSA_FP32); the dims of a head are adjacent, tokens and
  *     heads at the given strides in elements (x may repeat rows with stride 0; rows of out must not meet).  out may be
- *     x itself (same strides: only the rotated dims are touched) and may otherwise share no element with it
- *     (DSA_ERR_INVALID_ARG).
+ *     x itself (same strides: only the rotated dims are touched).  Otherwise it lies apart from x in memory, or, with the
+ *     same strides, between x's rows (two parts of one [T, parts, H, D] array, say) without an element in common; anything
+ *     else is DSA_ERR_INVALID_ARG.
  *   positions [T] int32 (device), or NULL: token t is at position pos0 + t.  inv_freq [rot_dim / 2] fp64 (DEVICE).
  * Angles are exact to 2^-32 turns at any position.  At most 2^30 tokens and 2^18 heads a call.  Pieces of 16 bytes are moved where pointers, strides and offsets allow, single elements
  * otherwise.  Needs no workspace.

@@ -1001,6 +1001,23 @@ bool rope_rows_apart(int T, int H, int D, int64_t st, int64_t sh) {
   return (sh >= D && st >= (H - 1) * sh + D) || (st >= D && sh >= (T - 1) * st + D);
 }
 
+// T x H rows of D elements at these strides, which lie apart (rope_rows_apart), meet the same rows moved by `delta`.  The
+// larger stride is longer than all rows along the smaller one together, so that only the two multiples of it next to delta
+// can leave a difference that those bridge, and for each of them two multiples of the smaller.
+bool rope_moved_rows_meet(int64_t delta, int T, int H, int D, int64_t st, int64_t sh) {
+  const bool heads_inside = st >= sh;
+  const int64_t so = heads_inside ? st : sh, si = heads_inside ? sh : st;
+  const int64_t no = heads_inside ? T : H, ni = heads_inside ? H : T;
+  auto floor_div = [](int64_t a, int64_t b) { return b ? a / b - (a % b < 0 ? 1 : 0) : 0; };
+  for (int64_t q = floor_div(delta, so), q1 = q + 1; q <= q1; ++q) {
+    if (q <= -no || q >= no) continue;
+    const int64_t r = delta - q * so;
+    for (int64_t p = floor_div(r, si), p1 = p + 1; p <= p1; ++p)
+      if (p > -ni && p < ni && std::abs(r - p * si) < D) return true;
+  }
+  return false;
+}
+
 dsa_status_t run_rope(const void* x, int64_t x_st, int64_t x_sh, void* out, int64_t o_st, int64_t o_sh,
                       const int32_t* positions, int pos0, const double* inv_freq, int T, int H, int D, int rot_off,
                       int rot_dim, int interleaved, float mscale, int dtype, bool backward, void* stream) {
@@ -1019,19 +1036,15 @@ dsa_status_t run_rope(const void* x, int64_t x_st, int64_t x_sh, void* out, int6
   if (H == 1) x_sh = o_sh = 0;
   if (!rope_rows_apart(T, H, D, o_st, o_sh)) return DSA_ERR_INVALID_ARG;
   // the result replaces its input exactly, or shares no element with it: apart in memory, or (equal strides) lying
-  // in the gaps between the other's rows
+  // between the other's rows
   if (x == out) {
     if (x_st != o_st || x_sh != o_sh) return DSA_ERR_INVALID_ARG;
   } else {
     const char *xb = static_cast<const char*>(x), *ob = static_cast<const char*>(out);
     const int64_t xe = ((T - 1) * x_st + (H - 1) * x_sh + D) * es, oe = ((T - 1) * o_st + (H - 1) * o_sh + D) * es;
-    if (xb < ob + oe && ob < xb + xe) {
-      const int64_t unit = H > 1 ? (T > 1 ? std::min(x_st, x_sh) : x_sh) : x_st, delta = (ob - xb) / es;
-      const bool lattice = x_st == o_st && x_sh == o_sh && unit > 0 && x_st % unit == 0 && x_sh % unit == 0 &&
-                           (ob - xb) % es == 0;
-      const int64_t r = lattice ? ((delta % unit) + unit) % unit : 0;
-      if (!lattice || r < D || r > unit - D) return DSA_ERR_INVALID_ARG;
-    }
+    if (xb < ob + oe && ob < xb + xe &&
+        (x_st != o_st || x_sh != o_sh || rope_moved_rows_meet((ob - xb) / es, T, H, D, o_st, o_sh)))
+      return DSA_ERR_INVALID_ARG;
   }
   RopeParams p{};
   p.x = x;

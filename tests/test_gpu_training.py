@@ -585,6 +585,35 @@ def test_rope_strides_offsets_and_positions(dsa):
     assert dsa.dsa_rope(both[:0], f).shape == (0, 1, 128)
 
 
+@pytest.mark.parametrize("shape,at", [((5, 3, 4, 64), 1), ((5, 4, 3, 64), 2), ((4, 5, 3, 64), 2), ((3, 4, 5, 64), 0)])
+@pytest.mark.parametrize("swap", [False, True])
+def test_rope_between_parts_of_one_array(dsa, shape, at, swap):
+    # x and the result are two parts of one array: [tokens, part, heads, dims] and the other orders of those
+    g = _gen(sum(shape) + at)
+    buf = torch.randn(*shape, generator=g).bfloat16().cuda()
+    before = buf.clone()
+    parts = [buf.select(at, i) for i in range(shape[at])]
+    parts = [t.transpose(0, 1) for t in parts] if swap else parts
+    x, out = parts[2], parts[1]                          # in front of x
+    f = dsa.dsa_rope_frequencies(32)[0].cuda()
+    want = _rope_reference(x.cpu(), f.cpu(), torch.arange(len(x)) + 7, 16, True, 1.0, False)
+    assert dsa.dsa_rope(x, f, pos0=7, rot_off=16, out=out).data_ptr() == out.data_ptr()
+    _rope_close(out, want, x.cpu(), 1.0)
+    back = parts[0]
+    dsa.dsa_rope_backward(x, f, pos0=7, rot_off=16, dx=back)
+    _rope_close(back, _rope_reference(x.cpu(), f.cpu(), torch.arange(len(x)) + 7, 16, True, 1.0, True), x.cpu(), 1.0)
+    keep = torch.ones(shape[at], dtype=torch.bool, device="cuda")
+    keep[:2] = False
+    assert torch.equal(buf.movedim(at, 0)[keep], before.movedim(at, 0)[keep])
+    # parts that have rows in common are refused, before anything is launched
+    wide = torch.randn(5, 6, 64, generator=g).bfloat16().cuda()
+    for a, b in ((wide[:, :4], wide[:, 1:5]), (wide[:4], wide[1:]), (wide[:, :4, :32], wide[:, 1:5, 16:48])):
+        with pytest.raises(dsa.DsaError) as e:
+            dsa.dsa_rope(a, f, out=b)
+        assert e.value.code == 1                         # DSA_ERR_INVALID_ARG
+    assert dsa.dsa_get_device_status() == 0
+
+
 # ------------------------------------------------------------------------------------------------ together
 def _training_step(dsa, s, stream=None):
     """One step of a layer: positions, attention, its backward pass, the objective's gradient, the indexer's."""
