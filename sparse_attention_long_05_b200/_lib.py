@@ -334,6 +334,12 @@ def dsa_indexer_scores_backward(q_idx, q_scale, k_idx, k_scale, w, idx, dsel, dq
     return dq, dk, dw
 
 
+def _int32(fn: str, name: str, v: int):
+    """ctypes cuts an int argument to its lowest 32 bits: a number that they do not hold is refused here."""
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{fn}: {name} {v} is outside the 32-bit integers")
+
+
 _ROPE_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
@@ -341,6 +347,8 @@ def dsa_rope_frequencies(rot_dim: int, base: float = 10000.0, factor: float = 1.
                          turns_fast: float = 32.0, turns_slow: float = 1.0):
     """(inv_freq [rot_dim / 2] fp64 on the host, mscale) of a rotary embedding, scaled for long contexts when
     factor > 1.  dsa_rope takes inv_freq on the device."""
+    _int32("dsa_rope_frequencies", "rot_dim", rot_dim)
+    _int32("dsa_rope_frequencies", "orig_len", orig_len)
     f = torch.empty((max(rot_dim, 0) // 2,), dtype=torch.float64)
     m = ctypes.c_float(0.0)
     _check("dsa_rope_frequencies", _lib.dsa_rope_frequencies(
@@ -354,6 +362,8 @@ def _rope(fn: str, x, inv_freq, positions, pos0, rot_off, interleaved, mscale, o
         raise ValueError(f"{fn}: takes bf16 or fp32 tensors")
     if x.dim() != 3:
         raise ValueError(f"{fn}: takes [T, H, D] tensors")
+    _int32(fn, "pos0", pos0)
+    _int32(fn, "rot_off", rot_off)
     T, H, D = x.shape
     R = 2 * inv_freq.numel()
     at = _elsewhere(fn, dev, stream)

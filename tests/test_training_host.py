@@ -197,3 +197,16 @@ def test_python_checks_name_the_argument():
     with pytest.raises(ValueError, match="contiguous"):
         _lib._want("fn", cpu, (("q", z(4, 4).t(), torch.bfloat16, (4, 4)),))
     assert _lib._want("fn", cpu, (("a", None, torch.int32, (2,)),)) == [None]
+
+
+def test_integers_beyond_32_bits_are_refused():
+    # ctypes would pass their lowest 32 bits on: position 2^32 + 5 as 5, dim 2^32 as 0
+    import sparse_attention_long_05_b200 as dsa
+    x, f = torch.zeros(2, 1, 64), torch.zeros(32, dtype=torch.float64)
+    for call in (dsa.dsa_rope, dsa.dsa_rope_backward):
+        for kw in (dict(pos0=2 ** 32 + 5), dict(pos0=2 ** 31), dict(pos0=-2 ** 31 - 1), dict(rot_off=2 ** 32)):
+            with pytest.raises(ValueError, match="outside the 32-bit integers"):
+                call(x, f, **kw)
+    for a, kw in ((2 ** 32 + 64, {}), (64, dict(factor=4.0, orig_len=2 ** 32 + 4096))):
+        with pytest.raises(ValueError, match="outside the 32-bit integers"):
+            dsa.dsa_rope_frequencies(a, **kw)
