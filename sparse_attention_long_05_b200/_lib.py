@@ -395,7 +395,10 @@ def dsa_rope(x, inv_freq, positions=None, pos0: int = 0, rot_off: int = 0, inter
 
 def dsa_rope_backward(dout, inv_freq, positions=None, pos0: int = 0, rot_off: int = 0, interleaved: bool = True,
                       mscale: float = 1.0, dx=None, out=None, stream=None):
-    """Gradient of dsa_rope's x from the gradient dout of its result -> dx (may be dout; `out` is another name of it)."""
+    """Gradient of dsa_rope's x from the gradient dout of its result -> dx (may be dout; `out` is another name of it, and
+    only one of the two is given)."""
+    if dx is not None and out is not None:
+        raise ValueError("dsa_rope_backward: dx and out name the same result, give one of them")
     return _rope("dsa_rope_backward", dout, inv_freq, positions, pos0, rot_off, interleaved, mscale,
                  out if dx is None else dx, stream)
 

@@ -210,3 +210,10 @@ def test_integers_beyond_32_bits_are_refused():
     for a, kw in ((2 ** 32 + 64, {}), (64, dict(factor=4.0, orig_len=2 ** 32 + 4096))):
         with pytest.raises(ValueError, match="outside the 32-bit integers"):
             dsa.dsa_rope_frequencies(a, **kw)
+
+
+def test_rope_backward_takes_one_result():
+    import sparse_attention_long_05_b200 as dsa
+    x, f = torch.zeros(2, 1, 64), torch.zeros(32, dtype=torch.float64)
+    with pytest.raises(ValueError, match="give one of them"):
+        dsa.dsa_rope_backward(x, f, dx=torch.zeros(2, 1, 64), out=torch.zeros(2, 1, 64))
