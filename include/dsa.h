@@ -214,6 +214,8 @@ DSA_API size_t dsa_indexer_scores_backward_workspace_size(int T, int S, int H_I,
  * k as in dsa_sparse_mla_attn; entries outside [-1, S) count as -1 and are recorded as DSA_ERR_BAD_INDEX.  The weights
  * dsel w_j q_scale and dsel w_j k_scale are rounded to bf16 once, each entry's contribution to dk to 10 bits; sums
  * are fp32, and dw is computed in fp32 throughout.
+ * q_j . k_s is summed in fp32, as in the forward: where it is within 2^-15 of the sum of its terms' magnitudes of 0, its sign
+ * may not be the exact sum's, and the entry may then count as live or not for that head.
  *   ws: dsa_indexer_scores_backward_workspace_size() bytes, 16-byte aligned.
  */
 DSA_API dsa_status_t dsa_indexer_scores_backward(const uint8_t* q_idx, const float* q_scale, const uint8_t* k_idx,

@@ -426,6 +426,37 @@ def test_index_scores_backward(dsa, heads, dim, T, S, k, kind, scaled):
     assert all(torch.equal(a, b) for a, b in zip((dq, dk, dw), again))
 
 
+@pytest.mark.parametrize("heads,dim", [(64, 128), (4, 64)])
+def test_index_scores_backward_of_sums_that_cancel(dsa, heads, dim):
+    """The largest products cancel in pairs, one product of 2^-15 of their sum or more decides the sign, and small ones have
+    bits below fp32's: the live heads are those of the exact sum."""
+    T, S, k = 12, 300, 192
+    g = _gen(dim)
+    big = dim // 2 - 4
+    q, kk = torch.zeros(T, heads, dim), torch.zeros(S, dim)
+    q[..., :big] = 224 + 224 * torch.rand(T, heads, big, generator=g)
+    kk[:, :big] = (224 + 224 * torch.rand(S, big, generator=g)) * torch.randn(S, big, generator=g).sign()
+    q[..., big:2 * big], kk[:, big:2 * big] = q[..., :big], -kk[:, :big]
+    for t in (q, kk):
+        t[..., 2 * big] = (32 + 416 * torch.rand(t.shape[:-1], generator=g)) * torch.randn(t.shape[:-1], generator=g).sign()
+        t[..., 2 * big + 1:] = 2.0 ** -5 * torch.randn(*t.shape[:-1], dim - 2 * big - 1, generator=g)
+    q, kk = q.to(torch.float8_e4m3fn), kk.to(torch.float8_e4m3fn)
+    qf, kf = q.float().double(), kk.float().double()
+    size = torch.einsum("thd,sd->ths", qf.abs(), kf.abs())
+    assert (torch.einsum("thd,sd->ths", qf, kf).abs() >= 2.0 ** -15 * size).all() and size.max() > 2.0 ** 20
+    w, idx = torch.randn(T, heads, generator=g), _selection(T, S, k, g, "holes")
+    dsel = torch.randn(T, k, generator=g)
+    dq, dk, dw = dsa.dsa_indexer_scores_backward(q.cuda(), None, kk.cuda(), None, w.cuda(), idx.cuda(), dsel.cuda())
+    assert dsa.dsa_get_device_status() == 0
+    qf, kf, wf = qf.requires_grad_(), kf.requires_grad_(), w.double().requires_grad_()
+    (_indexer_scores(qf, kf, wf, idx) * torch.where(idx >= 0, dsel.double(), 0.0)).sum().backward()
+    assert _rel(dq, qf.grad) <= L2_BF16 and _rel(dk, kf.grad) <= L2_BF16
+    # dw takes x itself, which is off by 2^-15 of sum |q k| at most; each live entry's error adds up
+    bound = 2.0 ** -15 * torch.einsum("tk,thk->th", torch.where(idx >= 0, dsel.abs().double(), 0.0),
+                                      size.gather(2, idx.clamp(min=0).long()[:, None].expand(-1, heads, -1)))
+    assert ((dw.double().cpu() - wf.grad).abs() <= bound).all()
+
+
 def _shifted(t):
     """The same fp32 values in memory that is aligned to 4 bytes only."""
     at = torch.empty(t.numel() + 1, device="cuda")[1:].view(t.shape)
