@@ -187,6 +187,7 @@ DSA_API size_t dsa_indexer_kl_backward_workspace_size(int T);
 /*
  * Gradient of dsa_indexer_kl with respect to the index scores of the selected entries:
  *   dsel[t][i] = dkl[t] * (Softmax(I_t)_i - p_t,i) over the token's selected entries, 0 where idx is -1.
+ * A score of -INFINITY has a softmax of 0; a NaN among a token's selected scores makes all its gradients NaN.
  * The target p_t is a constant of the objective: no gradient reaches q, c or lse.
  *   q, c, S, idx, sel_scores, lse, T, H, k, scale: as in dsa_indexer_kl;
  *   dkl [T] fp32 or NULL (1 for every token): the gradient of kl;

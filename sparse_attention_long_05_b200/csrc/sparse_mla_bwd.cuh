@@ -552,7 +552,7 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               if (x > m_i) {
                 z_i = z_i * ex2_approx((m_i - x) * kLog2e) + 1.f;
                 m_i = x;
-              } else if (x > -INFINITY) {
+              } else if (x != -INFINITY) {     // (a NaN stays in the sum, and with it in the token's gradient)
                 z_i += ex2_approx((x - m_i) * kLog2e);
               }
             }
@@ -605,7 +605,7 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
         float* rs = hs + 128;              // [8 warps][max, sum of exp, sum of a]
-        float z = m_i == -INFINITY ? 0.f : z_i * ex2_approx((m_i - mm) * kLog2e);
+        float z = m_i == -INFINITY ? z_i : z_i * ex2_approx((m_i - mm) * kLog2e);      // (then 0 or NaN)
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
           z += __shfl_xor_sync(0xffffffffu, z, d);
@@ -650,11 +650,11 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         const float up = p.dkl ? p.dkl[t] : 1.f;
         // (divisions, not products with reciprocals: a token with one entry has both exactly 1, and a gradient of 0)
-        const float z_div = z_all > 0.f ? z_all : INFINITY, a_div = a_all > 0.f ? a_all : INFINITY;
+        const float z_div = z_all == 0.f ? INFINITY : z_all, a_div = a_all > 0.f ? a_all : INFINITY;
         for (int i = (2 * grp + rank) * NK + row; i < min(sp.j1 * 2 * NK, p.k); i += 4 * NK) {
           const int e = __ldg(p.idx + base + i);
           const float x = p.sel[base + i];
-          const float soft = x > -INFINITY ? ex2_approx((x - m_all) * kLog2e) / z_div : 0.f;
+          const float soft = (x == -INFINITY ? 0.f : ex2_approx((x - m_all) * kLog2e)) / z_div;
           p.dsel[base + i] = (e >= 0 && e < p.S) ? up * (soft - __ldcg(p.dsel + base + i) / a_div) : 0.f;
         }
       }

@@ -378,6 +378,38 @@ def test_objective_backward(dsa, T, S, H, k, kind):
     assert torch.equal(ones, dsa.dsa_indexer_kl_backward(qd, cd, idxd, sel.cuda(), lse, torch.ones(T, device="cuda"), SCALE))
 
 
+def test_objective_backward_with_nan_and_infinite_scores(dsa):
+    """Softmax(I) - p of a token with a NaN among its selected scores is NaN, whichever slot (and so whichever lane, warp or
+    CTA of the pair) holds it; a NaN in an empty slot is not looked at; a score of -inf has a softmax of 0."""
+    T, S, H, k = 9, 900, 24, 640
+    q, c, idx, _ = _attention_case(T, S, H, k, "causal", 17)
+    idx[2, 100:], idx[6, 1:], idx[8] = -1, -1, -1
+    g = _gen(18)
+    sel, dkl = torch.randn(T, k, generator=g), torch.randn(T, generator=g)
+    qd, cd, idxd = q.cuda(), c.cuda(), idx.cuda()
+    _, lse = dsa.dsa_sparse_mla_attn(qd, cd, idxd, SCALE)
+    run = lambda x: dsa.dsa_indexer_kl_backward(qd, cd, idxd, x.cuda(), lse, dkl.cuda(), SCALE)
+    clean = run(sel)
+    bad = sel.clone()
+    bad[2, 100:], bad[8] = math.nan, math.nan            # empty slots only
+    bad[1, 0], bad[3, 130], bad[4, 639], bad[5], bad[6, 0] = math.nan, math.nan, math.nan, math.nan, math.nan
+    bad[7, 5:300] = -math.inf
+    got, on = run(bad).cpu(), idx >= 0
+    hit = torch.zeros(T, dtype=torch.bool)
+    hit[[1, 3, 4, 5, 6]] = True
+    assert torch.isnan(got[hit][on[hit]]).all() and (got[~on] == 0).all()
+    same = ~hit
+    same[7] = False
+    assert torch.equal(got[same], clean.cpu()[same])
+    _, _, p, _ = _attention(q.double(), c.double(), idx)
+    want = dkl.double()[7] * (torch.softmax(bad[7].double(), 0) - p[7].sum(0) / p[7].sum())
+    assert _rel(got[7], want) <= L2_FP32
+    # every score -inf: no softmax at all, minus the target is left
+    bad[7] = -math.inf
+    assert _rel(run(bad)[7], -dkl.double()[7] * p[7].sum(0) / p[7].sum()) <= L2_FP32
+    assert dsa.dsa_get_device_status() == 0
+
+
 # ------------------------------------------------------------------------------------------------ index scores
 def _indexer_case(T, S, heads, dim, k, kind, scaled, seed):
     g = _gen(seed)
