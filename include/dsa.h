@@ -174,7 +174,8 @@ DSA_API dsa_status_t dsa_sparse_mla_attn_backward(const uint16_t* q, const uint1
  *   sel_scores [T, k] fp32: the index score I[t, idx[t][i]] of each selected entry (ignored where idx is -1);
  *   lse [T, H] fp32: the attention's natural-log log-sum-exp per head over the same entries (dsa_sparse_mla_attn's
  *     lse output), from which the probabilities are formed;
- *   kl [T] fp32 (out): the divergence in nats (0 for a token without entries).
+ *   kl [T] fp32 (out): the divergence in nats (0 for a token without entries, NaN for one with a NaN among its selected
+ *     scores).
  * The logits are recomputed on the tensor cores as in the attention.  Needs no workspace.
  */
 DSA_API dsa_status_t dsa_indexer_kl(const uint16_t* q, const uint16_t* c, int S, const int32_t* idx,

@@ -739,7 +739,7 @@ sparse_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         if (lane == 0) {
           float kl = 0.f;
-          if (s_a > 0.f && z > 0.f) {
+          if (s_a > 0.f && (z > 0.f || isnan(s_ai))) {     // (a NaN score is in s_ai whatever became of z)
             const float lse_i = mm + lg2_approx(z) * kLn2;
             kl = (s_alog - s_a * lg2_approx(s_a) * kLn2 - s_ai) / s_a + lse_i;
           }

@@ -108,3 +108,26 @@ def test_indexer_kl_on_given_selections(dsa):
         m = idx[r] >= 0
         ref = O.indexer_kl_row(sel[r][m].astype(np.float64), q[r], c[idx[r][m]], cfg.scale)
         assert abs(kl[r] - ref) <= _tol(ref, float(np.abs(sel[r][m]).max())), f"row {r}"
+
+
+def test_kl_of_nan_scores_is_nan(dsa):
+    """A NaN among a token's selected scores makes its divergence NaN, whichever slot holds it and whatever the others are;
+    one in an empty slot is not looked at."""
+    T, S, H, k = 9, 900, 24, 640
+    g = torch.Generator().manual_seed(19)
+    q, c = torch.randn(T, H, 576, generator=g).bfloat16().cuda(), torch.randn(S, 576, generator=g).bfloat16().cuda()
+    idx = torch.stack([torch.randperm(S, generator=g)[:k].sort().values for _ in range(T)]).int()
+    idx[2, 100:], idx[6, 1:], idx[8] = -1, -1, -1
+    sel = torch.randn(T, k, generator=g)
+    _, lse = dsa.dsa_sparse_mla_attn(q, c, idx.cuda(), 576 ** -0.5)
+    run = lambda x: dsa.dsa_indexer_kl(q, c, idx.cuda(), x.cuda(), lse, 576 ** -0.5).cpu()
+    clean = run(sel)
+    assert torch.isfinite(clean).all() and clean[8] == 0
+    bad = sel.clone()
+    bad[2, 100:], bad[8] = float("nan"), float("nan")    # empty slots only
+    for t, i in ((0, 77), (1, 0), (3, 130), (4, 639), (5, slice(None)), (6, 0)):
+        bad[t, i] = float("nan")
+    got = run(bad)
+    assert torch.isnan(got[[0, 1, 3, 4, 5, 6]]).all()
+    assert torch.equal(got[[2, 7, 8]], clean[[2, 7, 8]])
+    assert dsa.dsa_get_device_status() == 0
