@@ -253,7 +253,9 @@ DSA_API dsa_status_t dsa_rope_frequencies(int rot_dim, double base, double facto
  *     same strides, between x's rows (two parts of one [T, parts, H, D] array, say) without an element in common; anything
  *     else is DSA_ERR_INVALID_ARG.
  *   positions [T] int32 (device), or NULL: token t is at position pos0 + t.  inv_freq [rot_dim / 2] fp64 (DEVICE).
- * Angles are exact to 2^-32 turns at any position.  At most 2^30 tokens and 2^18 heads a call.  Pieces of 16 bytes are moved where pointers, strides and offsets allow, single elements
+ * An angle is position * inv_freq[i] to 2^-24 turns (it reaches sine and cosine as fp32) plus |position| * inv_freq[i] * 2^-54
+ * turns (1 / 2 pi times inv_freq[i] is formed in fp64), which is as much from positions of 2^30 on.  At most 2^30
+ * tokens and 2^18 heads a call.  Pieces of 16 bytes are moved where pointers, strides and offsets allow, single elements
  * otherwise.  Needs no workspace.
  */
 DSA_API dsa_status_t dsa_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, void* out, int64_t out_stride_t,

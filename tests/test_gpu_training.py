@@ -648,6 +648,25 @@ def test_rope_strides_offsets_and_positions(dsa):
     assert dsa.dsa_rope(both[:0], f).shape == (0, 1, 128)
 
 
+def test_rope_angles_at_any_position(dsa):
+    """Pairs (1, 0) turn to (cos, sin): angles against exact arithmetic.  Bound: 2^-24 turns, |position| f 2^-54 turns, and
+    2^-22 for sine, cosine and the result in fp32 (a few units of 2^-24 each)."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+    pos = [0, 1, -1, 4095, 131071, 10 ** 6 + 1, 2 ** 24 + 1, -(2 ** 24) - 3, 10 ** 8 + 7, 2 ** 31 - 1, -2 ** 31]
+    f = torch.cat([dsa.dsa_rope_frequencies(32)[0], torch.tensor([2.5, 0.5, 1e-9, 3.0], dtype=torch.float64)])
+    x = torch.tensor([1.0, 0.0]).repeat(len(f)).expand(len(pos), 1, -1).contiguous().cuda()
+    y = dsa.dsa_rope(x, f.cuda(), torch.tensor(pos, dtype=torch.int64).int().cuda()).cpu().double()
+    for t, p in enumerate(pos):
+        for i, w in enumerate(f.tolist()):
+            turns = p * Decimal(w) / (2 * pi)
+            angle = float((turns - turns.to_integral_value()) * 2 * pi)
+            bound = 2 * math.pi * (2.0 ** -24 + abs(p) * w * 2.0 ** -54) + 2.0 ** -22
+            assert abs(float(y[t, 0, 2 * i]) - math.cos(angle)) <= bound, (p, w)
+            assert abs(float(y[t, 0, 2 * i + 1]) - math.sin(angle)) <= bound, (p, w)
+
+
 @pytest.mark.parametrize("shape,at", [((5, 3, 4, 64), 1), ((5, 4, 3, 64), 2), ((4, 5, 3, 64), 2), ((3, 4, 5, 64), 0)])
 @pytest.mark.parametrize("swap", [False, True])
 def test_rope_between_parts_of_one_array(dsa, shape, at, swap):
