@@ -727,7 +727,7 @@ constexpr long long kShortList = 16;
 template <int W>
 dsa_status_t scatter_end(const ScatterWs& w, const int* idx, int T, int64_t S, int k, int kp, bool first, bool last, uint16_t* out,
                          cudaStream_t st) {
-  const ScatterParams p{w.contrib, w.table, idx, T, w.ld, k, kp, w.acc, first ? 1 : 0, last ? 1 : 0, out};
+  const ScatterParams p{w.contrib, w.table, idx, w.ld, k, kp, w.acc, first ? 1 : 0, last ? 1 : 0, out};
   // by the mean length of a row's list (T k / S at most): short ones a warp each
   const bool brief = static_cast<long long>(T) * k < kShortList * static_cast<long long>(S);
   const cudaError_t err =
@@ -825,7 +825,6 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
     p.lse = lse + o * H;
     p.delta = w.delta;
     p.pds = w.pds;
-    p.contrib = w.sc.contrib;
     p.dq = dq + o * H * mbw::D;
     p.T = n;
     p.t0 = t0;

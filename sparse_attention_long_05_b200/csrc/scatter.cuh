@@ -160,7 +160,7 @@ struct ScatterParams {
   const uint16_t* contrib;    // [T * kp, W] in pieces of eight (scatter_pack64)
   const uint16_t* table;      // [S, ld]
   const int* idx;             // [T, k]
-  int T, ld, k, kp;
+  int ld, k, kp;
   float* acc;                 // [S, W] sums of the chunks so far, or null (one chunk)
   int first, last;            // first / last chunk
   uint16_t* out;              // [S, W] bf16, written with the last chunk

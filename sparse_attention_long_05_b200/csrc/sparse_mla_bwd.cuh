@@ -43,7 +43,6 @@ struct MlaBwdParams {
   const float* lse;            // [T, H]
   const float* delta;          // [T, H]
   uint16_t* pds;               // [T * kp, 2 HP] bf16: dS of HP heads, then P of HP heads, for every slot
-  uint16_t* contrib;           // [T * kp, 576]: each entry's contribution to dc (scatter_pack64)
   uint16_t* dq;                // [T, H, 576]
   float* dq_part;              // splits > 1: [T * splits, H, 576] sums of each split
   int T, t0;                   // tokens of the chunk; the first one's index in q and dout
