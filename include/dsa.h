@@ -155,8 +155,8 @@ DSA_API size_t dsa_sparse_mla_attn_backward_workspace_size(int T, int S, int H, 
  * A row of c selected twice by a token counts twice, as in the forward.  A token without entries (lse = -INFINITY)
  * has dq = 0.  An entry outside [-1, S) is treated as -1 and recorded as DSA_ERR_BAD_INDEX.
  * P and dS are rounded to bf16 once, each entry's contribution to dc to 10 bits; every sum is fp32.
- * 16-bit arrays and idx are 16-byte aligned, fp32 arrays to their type; results share no memory with inputs (here and in
- * the two backward passes below).
+ * 16-bit arrays and idx are 16-byte aligned, fp32 arrays to their type; results share no memory with inputs (here and
+ * in the two backward passes below).
  *   ws: dsa_sparse_mla_attn_backward_workspace_size() bytes, 16-byte aligned.  Long T are worked through in chunks of
  *     tokens (about 4 GiB of workspace and, with more than one, an fp32 copy of dc).
  */
@@ -216,8 +216,8 @@ DSA_API size_t dsa_indexer_scores_backward_workspace_size(int T, int S, int H_I,
  * k as in dsa_sparse_mla_attn; entries outside [-1, S) count as -1 and are recorded as DSA_ERR_BAD_INDEX.  The weights
  * dsel w_j q_scale and dsel w_j k_scale are rounded to bf16 once, each entry's contribution to dk to 10 bits; sums
  * are fp32, and dw is computed in fp32 throughout.
- * q_j . k_s is summed in fp32, as in the forward: where it is within 2^-15 of the sum of its terms' magnitudes of 0, its sign
- * may not be the exact sum's, and the entry may then count as live or not for that head.
+ * q_j . k_s is summed in fp32, as in the forward: where it is within 2^-15 of the sum of its terms' magnitudes of 0,
+ * its sign may not be the exact sum's, and the entry may then count as live or not for that head.
  *   ws: dsa_indexer_scores_backward_workspace_size() bytes, 16-byte aligned.
  */
 DSA_API dsa_status_t dsa_indexer_scores_backward(const uint8_t* q_idx, const float* q_scale, const uint8_t* k_idx,
@@ -234,9 +234,10 @@ enum { DSA_BF16 = 0, DSA_FP32 = 1 };
  * i < rot_dim / 2 (HOST array).  factor > 1 scales them for contexts `factor` times as long as the orig_len positions
  * a model was trained on: pairs that turn less than turns_slow times over orig_len positions are slowed by factor,
  * pairs that turn more than turns_fast times are kept, those between are blended linearly in i (usual values: 32 and
- * 1): inv_freq[i] (1 - r + r / factor), r = (i - low) / (high - low) within [0, 1], where with
- * pair(n) = rot_dim ln(orig_len / (2 pi n)) / (2 ln base), the index at which a pair turns n times over orig_len positions,
- * low = floor(pair(turns_fast)) and high = ceil(pair(turns_slow)), whether pairs of these indices exist or not.  *mscale (may be NULL) receives 0.1 ln(factor) + 1, the usual factor on rotated values, or 1 when factor is 1.
+ * 1): inv_freq[i] (1 - r + r / factor), r = (i - low) / (high - low) within [0, 1], low = floor(pair(turns_fast)) and
+ * high = ceil(pair(turns_slow)), whether pairs of these indices exist or not, with pair(n) = rot_dim
+ * ln(orig_len / (2 pi n)) / (2 ln base), the index at which a pair turns n times over orig_len positions.  *mscale (may
+ * be NULL) receives 0.1 ln(factor) + 1, the usual factor on rotated values, or 1 when factor is 1.
  */
 DSA_API dsa_status_t dsa_rope_frequencies(int rot_dim, double base, double factor, int orig_len, double turns_fast,
                                           double turns_slow, double* inv_freq, float* mscale);
@@ -249,14 +250,14 @@ DSA_API dsa_status_t dsa_rope_frequencies(int rot_dim, double base, double facto
  * dsa_rope_backward is the transpose: dx from the gradient dout, with the same mscale.
  *   x, out: T tokens x H heads x D dims of `dtype` (DSA_BF16, DSA_FP32); the dims of a head are adjacent, tokens and
  *     heads at the given strides in elements (x may repeat rows with stride 0; rows of out must not meet).  out may be
- *     x itself (same strides: only the rotated dims are touched).  Otherwise it lies apart from x in memory, or, with the
- *     same strides, between x's rows (two parts of one [T, parts, H, D] array, say) without an element in common; anything
- *     else is DSA_ERR_INVALID_ARG.
+ *     x itself (same strides: only the rotated dims are touched).  Otherwise it lies apart from x in memory, or, with
+ *     the same strides, between x's rows (two parts of one [T, parts, H, D] array, say) without an element in common;
+ *     anything else is DSA_ERR_INVALID_ARG.
  *   positions [T] int32 (device), or NULL: token t is at position pos0 + t.  inv_freq [rot_dim / 2] fp64 (DEVICE).
- * An angle is position * inv_freq[i] to 2^-24 turns (it reaches sine and cosine as fp32) plus |position| * inv_freq[i] * 2^-54
- * turns (1 / 2 pi times inv_freq[i] is formed in fp64), which is as much from positions of 2^30 on.  At most 2^30
- * tokens and 2^18 heads a call.  Pieces of 16 bytes are moved where pointers, strides and offsets allow, single elements
- * otherwise.  Needs no workspace.
+ * An angle is position * inv_freq[i], off by 2^-24 turns at most (it reaches sine and cosine as fp32) and 2^-54 turns
+ * for each |position| * inv_freq[i] (1 / 2 pi times inv_freq[i] is formed in fp64), as much again at position 2^30.  At
+ * most 2^30 tokens and 2^18 heads a call.  Pieces of 16 bytes are moved where pointers, strides and offsets allow,
+ * single elements otherwise.  Needs no workspace.
  */
 DSA_API dsa_status_t dsa_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, void* out, int64_t out_stride_t,
                               int64_t out_stride_h, const int32_t* positions, int pos0, const double* inv_freq, int T,

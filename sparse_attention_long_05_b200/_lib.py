@@ -296,7 +296,8 @@ def dsa_indexer_kl_backward(q, c, idx, sel_scores, lse, dkl, scale: float, dsel=
         ("sel_scores", sel_scores, f32, (T, k)), ("lse", lse, f32, (T, H)), ("dkl", dkl, f32, (T,)),
         ("dsel", dsel, f32, (T, k))))
     ws, pw, nw = _ws(fn, ws, 0 if ws is not None else _lib.dsa_indexer_kl_backward_workspace_size(T), q)
-    _check(fn, _lib.dsa_indexer_kl_backward(pq, pc, S, pi, ps, pl, pk, T, H, k, scale, pd, pw, nw, _current_stream(dev.index)))
+    _check(fn, _lib.dsa_indexer_kl_backward(pq, pc, S, pi, ps, pl, pk, T, H, k, scale, pd, pw, nw,
+                                            _current_stream(dev.index)))
     return dsel
 
 
@@ -395,8 +396,8 @@ def dsa_rope(x, inv_freq, positions=None, pos0: int = 0, rot_off: int = 0, inter
 
 def dsa_rope_backward(dout, inv_freq, positions=None, pos0: int = 0, rot_off: int = 0, interleaved: bool = True,
                       mscale: float = 1.0, dx=None, out=None, stream=None):
-    """Gradient of dsa_rope's x from the gradient dout of its result -> dx (may be dout; `out` is another name of it, and
-    only one of the two is given)."""
+    """Gradient of dsa_rope's x from the gradient dout of its result -> dx (may be dout; `out` is another name of it,
+    and only one of the two is given)."""
     if dx is not None and out is not None:
         raise ValueError("dsa_rope_backward: dx and out name the same result, give one of them")
     return _rope("dsa_rope_backward", dout, inv_freq, positions, pos0, rot_off, interleaved, mscale,

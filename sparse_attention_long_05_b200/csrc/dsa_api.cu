@@ -253,8 +253,8 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 }
 
 // launch_pdl of a kernel with more dynamic shared memory than the default: the attribute that allows it is set at the
-// kernel's first launch on a device (`seen`: one bit a device), and once more where a launch is refused without it (after
-// a cudaDeviceReset); setting it on every call costs about as much as a third of a launch.
+// kernel's first launch on a device (`seen`: one bit a device), and once more where a launch is refused without it
+// (after a cudaDeviceReset); setting it on every call costs about as much as a third of a launch.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl_large(std::atomic<unsigned long long>& seen, void (*kernel)(KArgs...), dim3 grid, dim3 block,
                              size_t smem, cudaStream_t st, Args... args) {
@@ -662,9 +662,9 @@ dsa_status_t run_decode(int B, const DecodeLayout& lay, const int32_t* ctx_len, 
 }
 
 // ------------------------------------------------------------------------------------------ backward passes
-// Hands out 256-byte aligned pieces of a workspace that starts on 16 bytes (null base: only counts).  The 32-byte stores of
-// P and dS need more than the 16 bytes a caller's workspace is asked for, so the first piece starts at its first 256-byte
-// boundary; bytes() counts the most that skips, whatever the address.
+// Hands out 256-byte aligned pieces of a workspace that starts on 16 bytes (null base: only counts).  The 32-byte
+// stores of P and dS need more than the 16 bytes a caller's workspace is asked for, so the first piece starts at its
+// first 256-byte boundary; bytes() counts the most that skips, whatever the address.
 struct Carve {
   char* base;
   size_t at = 0;
@@ -725,8 +725,8 @@ dsa_status_t scatter_build(const ScatterWs& w, const int* idx, int T, int64_t S,
 constexpr long long kShortList = 16;
 
 template <int W>
-dsa_status_t scatter_end(const ScatterWs& w, const int* idx, int T, int64_t S, int k, int kp, bool first, bool last, uint16_t* out,
-                         cudaStream_t st) {
+dsa_status_t scatter_end(const ScatterWs& w, const int* idx, int T, int64_t S, int k, int kp, bool first, bool last,
+                         uint16_t* out, cudaStream_t st) {
   const ScatterParams p{w.contrib, w.table, idx, w.ld, k, kp, w.acc, first ? 1 : 0, last ? 1 : 0, out};
   // by the mean length of a row's list (T k / S at most): short ones a warp each
   const bool brief = static_cast<long long>(T) * k < kShortList * static_cast<long long>(S);
@@ -753,8 +753,8 @@ bool make_rows_map(CUtensorMap* m, const uint16_t* base, long long rows, int wid
   return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Splits of each of n items' `tiles` tiles over `workers` CTAs (or pairs) that minimise the rounds' length: cost = rounds x
-// (tiles of a split + `setup`, what an item costs beside its tiles, in tiles).
+// Splits of each of n items' `tiles` tiles over `workers` CTAs (or pairs) that minimise the rounds' length: cost =
+// rounds x (tiles of a split + `setup`, what an item costs beside its tiles, in tiles).
 int choose_splits(long long n, int workers, int tiles, double setup) {
   int best = 1;
   double best_cost = 1e300;
@@ -764,7 +764,8 @@ int choose_splits(long long n, int workers, int tiles, double setup) {
   }
   return best;
 }
-// The same where the splits' sums have to be joined: only for at most two rounds of items, so that the parts stay small.
+// The same where the splits' sums have to be joined: only for at most two rounds of items, so that the parts stay
+// small.
 int choose_joined_splits(long long n, int workers, int tiles, double setup) {
   return n > 2 * workers ? 1 : choose_splits(n, workers, tiles, setup);
 }
@@ -844,19 +845,19 @@ dsa_status_t run_attn_bwd(const uint16_t* q, const uint16_t* c, int S, const int
     if (e != DSA_OK) return e;
     if ((e = scatter_build(w.sc, p.idx, n, S, k, st)) != DSA_OK) return e;
     p.splits = choose_splits(n, sms / 2, (k + 255) / 256, 0.8);
-    if (launch_pdl_large(seen[0], mla_bwd_p_kernel<false>, dim3(2 * std::min(sms / 2, n * p.splits)), dim3(mbw::p::THREADS),
-                   mbw::p::Map<false>::SMEM, st, tq, tdo, tc, p) != cudaSuccess)
+    if (launch_pdl_large(seen[0], mla_bwd_p_kernel<false>, dim3(2 * std::min(sms / 2, n * p.splits)),
+                         dim3(mbw::p::THREADS), mbw::p::Map<false>::SMEM, st, tq, tdo, tc, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
     p.splits = choose_splits(3ll * n, sms / 2, (k + 255) / 256, 1.0);
-    if (launch_pdl_large(seen[1], mla_bwd_dc_kernel, dim3(2 * std::min(sms / 2, 3 * n * p.splits)), dim3(mbw::dc::THREADS), mbw::dc::SMEM, st,
-                   tp128, tq, tdo, tout, p) != cudaSuccess)
+    if (launch_pdl_large(seen[1], mla_bwd_dc_kernel, dim3(2 * std::min(sms / 2, 3 * n * p.splits)),
+                         dim3(mbw::dc::THREADS), mbw::dc::SMEM, st, tp128, tq, tdo, tout, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
     p.splits = w.dq_splits;
     p.dq_part = w.dq_part;
-    if (launch_pdl_large(seen[2], mla_bwd_dq_kernel, dim3(std::min(sms, 3 * n * p.splits)), dim3(mbw::dq::THREADS), mbw::dq::SMEM, st,
-                   tp64, p) != cudaSuccess)
+    if (launch_pdl_large(seen[2], mla_bwd_dq_kernel, dim3(std::min(sms, 3 * n * p.splits)), dim3(mbw::dq::THREADS),
+                         mbw::dq::SMEM, st, tp64, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
     if (p.splits > 1 && (e = join_splits(w.dq_part, w.sc.n_end, mbw::dq::KT, p.splits, n, H * mbw::D, 0, p.dq, nullptr,
@@ -954,11 +955,12 @@ dsa_status_t run_index_bwd(IndexerBwdParams p, int T, uint16_t* dk, const IndexB
     dsa_status_t e = last_launch_status();
     if (e != DSA_OK) return e;
     if ((e = scatter_build(w.sc, p.idx, p.T, p.S, p.k, st)) != DSA_OK) return e;
-    if (launch_pdl_large(seen, indexer_bwd_kernel<HI, DI>, dim3(std::min(num_sms(), p.T * p.splits)), dim3(ixb::THREADS), ixb::SMEM, st, tout,
-                   p) != cudaSuccess)
+    if (launch_pdl_large(seen, indexer_bwd_kernel<HI, DI>, dim3(std::min(num_sms(), p.T * p.splits)),
+                         dim3(ixb::THREADS), ixb::SMEM, st, tout, p) != cudaSuccess)
       return DSA_ERR_CUDA;
     if ((e = last_launch_status()) != DSA_OK) return e;
-    if (p.splits > 1 && (e = join_splits(w.part, w.sc.n_end, ixb::NK, p.splits, p.T, HI * DI, HI, p.dq, p.dw, st)) != DSA_OK)
+    if (p.splits > 1 &&
+        (e = join_splits(w.part, w.sc.n_end, ixb::NK, p.splits, p.T, HI * DI, HI, p.dq, p.dw, st)) != DSA_OK)
       return e;
     e = scatter_end<DI>(w.sc, p.idx, p.T, p.S, p.k, w.kp, t0 == 0, t0 + p.T >= T, dk, st);
     if (e != DSA_OK) return e;
@@ -1000,9 +1002,9 @@ bool rope_rows_apart(int T, int H, int D, int64_t st, int64_t sh) {
   return (sh >= D && st >= (H - 1) * sh + D) || (st >= D && sh >= (T - 1) * st + D);
 }
 
-// T x H rows of D elements at these strides, which lie apart (rope_rows_apart), meet the same rows moved by `delta`.  The
-// larger stride is longer than all rows along the smaller one together, so that only the two multiples of it next to delta
-// can leave a difference that those bridge, and for each of them two multiples of the smaller.
+// T x H rows of D elements at these strides, which lie apart (rope_rows_apart), meet the same rows moved by `delta`.
+// The larger stride is longer than all rows along the smaller one together, so that only the two multiples of it next
+// to delta can leave a difference that those bridge, and for each of them two multiples of the smaller.
 bool rope_moved_rows_meet(int64_t delta, int T, int H, int D, int64_t st, int64_t sh) {
   const bool heads_inside = st >= sh;
   const int64_t so = heads_inside ? st : sh, si = heads_inside ? sh : st;
@@ -1803,7 +1805,8 @@ dsa_status_t dsa_rope_frequencies(int rot_dim, double base, double factor, int o
   if (rot_dim <= 0 || rot_dim % 2 || !(base > 1.0) || !(factor >= 1.0) || !inv_freq || !std::isfinite(base) ||
       !std::isfinite(factor))
     return DSA_ERR_INVALID_ARG;
-  if (factor > 1.0 && (orig_len <= 0 || !(turns_slow > 0.0) || !(turns_fast > turns_slow) || !std::isfinite(turns_fast)))
+  if (factor > 1.0 &&
+      (orig_len <= 0 || !(turns_slow > 0.0) || !(turns_fast > turns_slow) || !std::isfinite(turns_fast)))
     return DSA_ERR_INVALID_ARG;
   const int n = rot_dim / 2;
   double low = 0.0, high = 1.0;

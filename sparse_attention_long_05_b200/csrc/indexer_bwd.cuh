@@ -2,22 +2,23 @@
 //
 // I[t,i] = sum_j w_j relu(q_j . k_s), s = idx[t][i], q_j = qs_t q_idx[t][j] and k_s = ks_s k_idx[s] the dequantised
 // operands.  With the gradient e = dsel[t][i], x = q_idx[t][j] . k_idx[s] and the live pairs 1[x > 0]:
-//   dw_j = qs sum_i e ks relu(x)       dq_j = sum_i (e w_j 1[x > 0] ks) k_idx[s]       dk_s = sum_(t,i) sum_j (G qs) q_idx[j]
-// with G = e w_j 1[x > 0]: three products of 2 x 64 heads x 128 dims per entry (G qs and G ks are what is stored).  dq and dk are gradients of the
-// dequantised values (what a straight-through quantiser passes on).
+//   dw_j = qs sum_i e ks relu(x)     dq_j = sum_i (G ks) k_idx[s]     dk_s = sum_(t,i) sum_j (G qs) q_idx[j]
+// with G = e w_j 1[x > 0]: three products of 2 x 64 heads x 128 dims per entry (G qs and G ks are what is stored).  dq
+// and dk are gradients of the dequantised values (what a straight-through quantiser passes on).
 //
-// One CTA per token (or per split of a token's tiles, where tokens are few), keys are the M dimension.  e4m3 rows are gathered with plain 16-byte loads and written as bf16
-// (exact) in the swizzled form the tensor core reads, so the one copy serves x (K-major), dq (transposed, MN-major)
-// and, for q, dk; kind::f16 needs both operands bf16 and G is.  Products of e4m3 are exact and their sum is held in fp32: it is
-// exact for small integers, else off by less than 2^-15 of sum |q k| (eight instructions that each add 17 terms, aligned to
-// the largest and cut at 24 bits or more: 8 x 17 x 2^-23).  Closer to 0 than that the sign, which decides what is live, may
-// be another than the exact one, as in the forward's sum; the jump of the gradient at x = 0 is as large on either side.
-// G qs and G ks are rounded to bf16 once (2^-9).  dw is summed from the fp32 x.  Per token: 16 tiles of
-// 128 keys, each x -> G -> (dk, dq); x of the next tile is issued before G of this one is waited for.
+// One CTA per token (or per split of a token's tiles, where tokens are few), keys are the M dimension.  e4m3 rows are
+// gathered with plain 16-byte loads and written as bf16 (exact) in the swizzled form the tensor core reads, so the one
+// copy serves x (K-major), dq (transposed, MN-major) and, for q, dk; kind::f16 needs both operands bf16 and G is.
+// Products of e4m3 are exact and their sum is held in fp32: it is exact for small integers, else off by less than 2^-15
+// of sum |q k| (eight instructions that each add 17 terms, aligned to the largest and cut at 24 bits or more: 8 x 17 x
+// 2^-23).  Closer to 0 than that the sign, which decides what is live, may be another than the exact one, as in the
+// forward's sum; the jump of the gradient at x = 0 is as large on either side.  G qs and G ks are rounded to bf16 once
+// (by 2^-8 at most).  dw is summed from the fp32 x.  Per token: 16 tiles of 128 keys, each x -> G -> (dk, dq); x of the
+// next tile is issued before G of this one is waited for.
 // HBM sees each entry's contribution to dk twice (written here, summed by scatter.cuh).
-// Measured on 2048 tokens of a 32K sequence, k = 2048, 64 heads: 523 us here, 231 for the sums, 116 for the table; bound by the
-// latency of G's chain (x from tensor memory -> G to shared memory) and by the issue slots its warps share.
-// The small indexer (4 heads, 64 dims) runs in the same layout, its missing heads and dims zero.
+// Measured on 2048 tokens of a 32K sequence, k = 2048, 64 heads: 533 us here, 219 for the sums, 115 for the table;
+// bound by the latency of G's chain (x from tensor memory -> G to shared memory) and by the issue slots its warps
+// share.  The small indexer (4 heads, 64 dims) runs in the same layout, its missing heads and dims zero.
 #pragma once
 #include "common.cuh"
 #include "sparse_mla_bwd.cuh"
@@ -164,7 +165,8 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
           const int slot = j * NK + pw * (NK / PRODUCERS) + s * ROWS + sub;
           const int e = slot < p.k ? ids[slot] : -1;
           v[s] = make_uint4(0, 0, 0, 0);
-          if (e >= 0 && e < p.S) v[s] = __ldg(reinterpret_cast<const uint4*>(p.k_idx + static_cast<long long>(e) * DI) + u);
+          if (e >= 0 && e < p.S)
+            v[s] = __ldg(reinterpret_cast<const uint4*>(p.k_idx + static_cast<long long>(e) * DI) + u);
         }
       };
       uint4 v[STEPS];
@@ -307,8 +309,8 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
         tc_fence_after();
         uint8_t* gl = cta.smem + OFF_G + 2 * s * G_BYTES + row * 128;
         const float eks = e * ks, eqs = e * qs;
-        // not unrolled (nor are the loops over 64 dims below): the roles' code together has to stay in the instruction cache,
-        // fetches from behind it were a sixth of all stalls (680 us for 2048 tokens, against 560)
+        // not unrolled (nor are the loops over 64 dims below): the roles' code together has to stay in the instruction
+        // cache, fetches from behind it were a sixth of all stalls (680 us for 2048 tokens, against 560)
 #pragma unroll 1
         for (int c = 0; c < BLOCKS; ++c) {
           uint32_t v[16];
@@ -342,9 +344,10 @@ indexer_bwd_kernel(const __grid_constant__ CUtensorMap tm_out, const IndexerBwdP
           for (int i = 0; i < 2; ++i) {
             const int unit = ((2 * c + i) ^ (row & 7)) << 4;
             *reinterpret_cast<uint4*>(gl + unit) = make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
-            *reinterpret_cast<uint4*>(gl + G_BYTES + unit) = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
+            *reinterpret_cast<uint4*>(gl + G_BYTES + unit) =
+                make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
           }
-          // sums over the warp's 32 keys: four halving steps, then the two half-warps; lane l ends with head 16 c + l % 16
+          // sums over the warp's 32 keys: four halving steps, then the two half-warps; lane l has head 16 c + l % 16
 #define DSA_IXB_HALVE(O)                                                                \
   {                                                                                     \
     const bool up = (lane & (O)) != 0;                                                  \

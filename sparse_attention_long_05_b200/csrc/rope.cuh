@@ -3,16 +3,17 @@
 // with (a, b) = (2 i, 2 i + 1) (interleaved) or (i, i + R/2) (halves); the backward pass is the transpose (-theta).
 // The other dims are copied, or left alone when the result replaces its input.
 //
-// Bound by HBM: each value is read and written once.  A thread owns one 16-byte piece of a head (halves: the two pieces of
-// its pairs) and walks over tokens and, for each, over some of the token's heads, so that the turn per position of its
-// pairs is formed once and the angles, which the heads share, once a token.  f / 2 pi is taken as a fraction of a turn in
-// units of 2^-64, so that position times it wraps to the fraction of a turn by itself (a position of 10^6 leaves no digit of
-// an fp32 angle); what f / 2 pi itself is off by, f 2^-54.8 (its constant and its product in fp64), grows with the position,
-// to 2^-23.8 turns at 2^31.  The fraction reaches sine and cosine as fp32 (2^-26 turns near half a turn, and as much again for
-// each of the two roundings of its product with 2 pi / 2^32, bf16 only), and bf16 results take the hardware's functions
-// (absolute error 2^-20, against 2^-9 of the rounding).
-// Measured: 53 us for fp32 [5000, 64, 128] (328 MB, 0.95 of HBM), 10.4 us for the 64 position dims of 131072 rows of 576
-// (33.5 MB: 128 bytes of every 1152; what bounds it has not been profiled), 2.4 us for 64 x 128 heads of a decode step.
+// Bound by HBM: each value is read and written once.  A thread owns one 16-byte piece of a head (halves: the two pieces
+// of its pairs) and walks over tokens and, for each, over some of the token's heads, so that the turn per position of
+// its pairs is formed once and the angles, which the heads share, once a token.  f / 2 pi is taken as a fraction of a
+// turn in units of 2^-64, so that position times it wraps to the fraction of a turn by itself (a position of 10^6
+// leaves no digit of an fp32 angle); what f / 2 pi itself is off by, f 2^-54.8 (its constant and its product in fp64),
+// grows with the position, to 2^-23.8 turns at 2^31.  The fraction reaches sine and cosine as fp32 (2^-26 turns near
+// half a turn, and as much again for each of the two roundings of its product with 2 pi / 2^32, bf16 only), and bf16
+// results take the hardware's functions (absolute error 2^-20, against 2^-8 of the rounding).
+// Measured: 53 us for fp32 [5000, 64, 128] (328 MB, 0.95 of HBM), 10.4 us for the 64 position dims of 131072 rows of
+// 576 (33.5 MB: 128 bytes of every 1152; what bounds it has not been profiled), 2.4 us for 64 x 128 heads of a decode
+// step.
 #pragma once
 #include "common.cuh"
 

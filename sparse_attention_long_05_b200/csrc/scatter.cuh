@@ -2,17 +2,16 @@
 // idx[t][i] = s of contrib[t][i], in a fixed order.
 //
 // The backward passes write one row of 16-bit values per selected entry (a chunk of tokens at a time): fp16 with a
-// power-of-two scale for each 64, whose exponent sits in the lowest bits of every eight.  Ten significant bits are left, to
-// which a value is rounded to nearest: it is off by 2^-10 of itself at most and by 2^-11.5 on average (by 2^-37 of the
-// largest of its 64, where it is smaller than 2^-28 of that), over the whole range of fp32, and up as often as down, so that
-// long lists and sums over many calls do not drift (cut off at ten bits, dc and dk came out 3.5e-4 too small; both ways in
-// turn, the rounding takes 879 us instead of 852 for the index scores' pass of 2048 tokens, the attention's 5007 and 5007).
-// bf16 rows, no longer,
-// would round four times as much: as much as the operands that made them, and gradients would be 1.7 steps of their own
-// rounding off instead of 1.4.  A table of the chunk,
-// slot[s][t] = the slot in which token t selected row s (16 bits, empty: 0xffff), turns the scatter into a gather:
-// one CTA per row s lists the row's entries in token order and adds them up.  Every sum has one order whatever the
-// kernels' timing, so results repeat bit for bit; with atomics they would not.  Bound by HBM: each contribution is
+// power-of-two scale for each 64, whose exponent sits in the lowest bits of every eight.  Ten significant bits are
+// left, to which a value is rounded to nearest: it is off by 2^-10 of itself at most and by 2^-11.5 on average (by
+// 2^-37 of the largest of its 64, where it is smaller than 2^-28 of that), over the whole range of fp32, and up as
+// often as down, so that long lists and sums over many calls do not drift (cut off at ten bits, dc and dk came out
+// 3.5e-4 too small; both ways in turn, the rounding takes 879 us instead of 852 for the index scores' pass of 2048
+// tokens, the attention's 5007 and 5007).  bf16 rows, no longer, would round four times as much: as much as the
+// operands that made them, and gradients would be 1.7 steps of their own rounding off instead of 1.4.  A table of the
+// chunk, slot[s][t] = the slot in which token t selected row s (16 bits, empty: 0xffff), turns the scatter into a
+// gather: one CTA per row s lists the row's entries in token order and adds them up.  Every sum has one order whatever
+// the kernels' timing, so results repeat bit for bit; with atomics they would not.  Bound by HBM: each contribution is
 // read once (2 W bytes), the table once (2 bytes per row and token).
 #pragma once
 #include <cuda_fp16.h>
@@ -34,16 +33,16 @@ __device__ __forceinline__ void scatter_clear(uint4* table, long long n) {
   for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step)
     table[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
 }
-// 64 values as pieces of eight: fp16 of x 2^(141 - E), E the exponent of the largest magnitude of the 64 (29 at least, where
-// any fp32 value that is not itself denormal keeps its digits), bit i of E in the lowest bit of a piece's value 2 i, bit i + 4
-// in that of value 2 i + 1.
+// 64 values as pieces of eight: fp16 of x 2^(141 - E), E the exponent of the largest magnitude of the 64 (29 at least,
+// where any fp32 value that is not itself denormal keeps its digits), bit i of E in the lowest bit of a piece's value 2
+// i, bit i + 4 in that of value 2 i + 1.
 //
-// Rounding to ten bits: with y = x 2^(141 - E), t = y (1 + 2^14) in fp32 holds y in steps of 2^14 times y's own, and t - 2^14 y
-// is y to nearest in such steps, ties to even, exactly.
+// Rounding to ten bits: with y = x 2^(141 - E), t = y (1 + 2^14) in fp32 holds y in steps of 2^14 times y's own, and t
+// - 2^14 y is y to nearest in such steps, ties to even, exactly.
 //
-// Infinities and NaN pass through the scale.  An infinity beside finite values is a sum that left fp32's range (an infinite
-// operand leaves nothing finite in the row): it counts as 2^127 to 2^128.  There y = x f / 2 + x f / 2, which keeps the
-// infinity, and the lowest bit is cut off.
+// Infinities and NaN pass through the scale.  An infinity beside finite values is a sum that left fp32's range (an
+// infinite operand leaves nothing finite in the row): it counts as 2^127 to 2^128.  There y = x f / 2 + x f / 2, which
+// keeps the infinity, and the lowest bit is cut off.
 __device__ __forceinline__ void scatter_pack64(const uint32_t (&v)[64], uint32_t (&w)[32]) {
   float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -72,7 +71,7 @@ __device__ __forceinline__ void scatter_add(uint4 v, float (&sum)[8]) {
   const uint32_t t = (w[0] & 0x00010001u) | ((w[1] & 0x00010001u) << 1) | ((w[2] & 0x00010001u) << 2) |
                      ((w[3] & 0x00010001u) << 3);
   const uint32_t e = (t | (t >> 12)) & 0xffu;
-  const float f = __uint_as_float((e - 14u) << 23);      // (e = 0 in the zeros that stand for no entry: -2^115, 0 f = 0)
+  const float f = __uint_as_float((e - 14u) << 23);    // (e = 0 in the zeros that stand for no entry: -2^115, 0 f = 0)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t x = w[i] & 0xfffefffeu;
@@ -88,8 +87,9 @@ __global__ void __launch_bounds__(256) scatter_clear_kernel(uint4* table, long l
   scatter_clear(table, n);
 }
 
-// One CTA per token: n_end (slots up to the last valid entry), and with a table its entries.  A row selected more than once by a token is entered with its lowest slot and
-// flagged.  An entry outside [-1, S) counts as empty and is recorded as DSA_ERR_BAD_INDEX.
+// One CTA per token: n_end (slots up to the last valid entry), and with a table its entries.  A row selected more than
+// once by a token is entered with its lowest slot and flagged.  An entry outside [-1, S) counts as empty and is
+// recorded as DSA_ERR_BAD_INDEX.
 __global__ void __launch_bounds__(256) scatter_build_kernel(const int* idx, int k, long long S, int* n_end,
                                                             uint16_t* table, int ld) {
   __shared__ int last;
@@ -277,10 +277,10 @@ __global__ void __launch_bounds__(ScatterCfg<W>::THREADS, W == 576 ? 7 : 8) scat
   }
 }
 
-// The same for short lists: one warp per row, nothing shared between warps.  W >= 256: the warp reads an entry's pieces in
-// W / 256 rounds of loads, four entries in flight; less: 256 / W entries at once, one to each part of the warp, whose sums
-// are joined at the end.  With few entries a row the time is the chain table -> entries -> result, which eight rows a CTA
-// walk at once here (20 tokens over 20020 rows, W = 576: 16 us against 58).
+// The same for short lists: one warp per row, nothing shared between warps.  W >= 256: the warp reads an entry's pieces
+// in W / 256 rounds of loads, four entries in flight; less: 256 / W entries at once, one to each part of the warp,
+// whose sums are joined at the end.  With few entries a row the time is the chain table -> entries -> result, which
+// eight rows a CTA walk at once here (20 tokens over 20020 rows, W = 576: 16 us against 58).
 constexpr int kSumWarps = 8;
 template <int W>
 __global__ void __launch_bounds__(32 * kSumWarps) scatter_sum_short_kernel(const ScatterParams p, long long S) {
@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(32 * kSumWarps) scatter_sum_short_kernel(const
     for (int u = 0; u < 8; ++u) {
       const uint32_t v = (w[u >> 1] >> (16 * (u & 1))) & 0xffffu;
       if (v != sct::EMPTY)
-        list[to++] = (static_cast<uint32_t>(8 * (q0 + lane) + u) << 11) | (v & (sct::TWICE - 1)) | ((v & sct::TWICE) << 20);
+        list[to++] = (static_cast<uint32_t>(8 * (q0 + lane) + u) << 11) | (v & (sct::TWICE - 1)) |
+                     ((v & sct::TWICE) << 20);
     }
     __syncwarp();
     for (int i = part; i < n; i += 4 * PARTS) {

@@ -20,15 +20,15 @@
 // A last kernel (scatter.cuh) sums the contributions of each row of c in token order: the result does not depend on
 // the order of execution, which atomics would not give.
 //
-// P and dS are rounded to bf16, by at most 2^-9 of their value, as the operands of the second products have to be.  All
+// P and dS are rounded to bf16, by at most 2^-8 of their value, as the operands of the second products have to be.  All
 // sums are fp32.
 //
-// Measured on 2048 tokens of a 32K sequence, k = 2048, 128 heads (launches one by one): P and dS 1141 us, contributions
-// 1403, dq 622, their sum 887, delta and the table 170; 4.5 to 5.0 ms in a row (2.95 TFLOP: 0.42 to 0.47 of the sustained
-// bf16 rate).  The objective's gradient takes 591 us (1.05 PFLOP/s).  The two pair kernels are bound by
-// shared memory: in the contributions' the operand fetches of the tensor cores and the warps' own traffic (staged pieces)
-// take about 45 % of its cycles each.  dq reads 40 KB a stage at 77 GB/s an SM, what
-// gathers and tiles together reach here; the sum runs at 0.85 of HBM.
+// Measured on 2048 tokens of a 32K sequence, k = 2048, 128 heads (launches one by one): P and dS 1137 us, contributions
+// 1416, dq 590, their sum 831, delta and the table 176; 4.8 to 5.0 ms in a row (2.95 TFLOP: 0.42 to 0.44 of the
+// sustained bf16 rate).  The objective's gradient takes 564 us (1.10 PFLOP/s).  The two pair kernels are bound by
+// shared memory: in the contributions' the operand fetches of the tensor cores and the warps' own traffic (staged pieces) take
+// about 45 % of its cycles each.  dq reads 40 KB a stage at 81 GB/s an SM, what gathers and tiles together reach here;
+// the sum runs at 0.88 of HBM.
 #pragma once
 #include "common.cuh"
 #include "scatter.cuh"
@@ -68,7 +68,9 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // all but the last N committed stores have read their shared memory / all have been written
 template <int N = 0>
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" :: "n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" :: "n"(N) : "memory");
+}
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -124,8 +126,8 @@ __device__ __forceinline__ void tma2_gather4(uint32_t dst, const CUtensorMap* ma
       " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
       :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
 }
-// Relaxed: what it announces (tensor memory read to the end, or nothing at all) is complete when it is issued, and a release
-// would first wait for every store of P and dS the thread has in flight.
+// Relaxed: what it announces (tensor memory read to the end, or nothing at all) is complete when it is issued, and a
+// release would first wait for every store of P and dS the thread has in flight.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
 }
@@ -147,8 +149,9 @@ __device__ __forceinline__ TileSpan tile_span(int n_end, int keys, int sp, int s
 }
 
 // Bounded waits as mbar_wait and warp_wait, the part behind a first unsuccessful look in a function of its own: where a
-// kernel's roles together overflow the instruction cache, the copies of that part cost more than the call (dq 96 -> 88 us for
-// 333 tokens, the index scores' pass 534 -> 494 for 2048; the probabilities' kernels fit and keep theirs in line).
+// kernel's roles together overflow the instruction cache, the copies of that part cost more than the call (dq 96 -> 88
+// us for 333 tokens, the index scores' pass 534 -> 494 for 2048; the probabilities' kernels fit and keep theirs in
+// line).
 __device__ __noinline__ bool mbar_wait_far(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   const long long t0 = clock64();
   while (!mbar_test(bar, parity)) {
@@ -292,7 +295,8 @@ __device__ __forceinline__ void bwd_end(BwdCta& c) {
   if (warp_id() == 1) {
     tc_fence_after();
     if constexpr (PAIR)
-      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(c.tmem), "r"(mbw::TMEM_COLS) : "memory");
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;"
+                   :: "r"(c.tmem), "r"(mbw::TMEM_COLS) : "memory");
     else
       tmem_dealloc(c.tmem, mbw::TMEM_COLS);
   }
@@ -312,10 +316,10 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 //
 // M = 256 keys (128 in each CTA, which gathers only its own), N = 2 HP: CTA 0 holds q's rows and CTA 1 dout's, so that
 // one MMA gives S^T (columns 0 .. HP - 1) and dP^T (HP .. 2 HP - 1) of all heads; the position dims, which dout lacks,
-// are an N = HP product with half of q's rows in each CTA.  KL: N = HP, half of q's rows in each CTA.  With both CTAs of
-// a token sharing their halves, each key is gathered once per token: gathers land after 1.5 to 2 us under load, and
-// (80 KB are in flight a CTA, KL 144 KB).  The resident rows are released chunk by chunk during the
-// token's last tile, so the next token's loads overlap it.
+// are an N = HP product with half of q's rows in each CTA.  KL: N = HP, half of q's rows in each CTA.  With both CTAs
+// of a token sharing their halves, each key is gathered once per token: gathers land after 1.5 to 2 us under load
+// (80 KB are in flight a CTA, KL 144 KB).  The resident rows are released chunk by chunk during the token's last tile,
+// so the next token's loads overlap it.
 template <bool KL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mbw::p::THREADS, 1)
 mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -332,7 +336,10 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const int rank = static_cast<int>(cluster_rank());
   if (threadIdx.x == 0) {
     for (int i = 0; i < DCH; ++i) { mbar_init(cta.bar(B_RES_FULL + i), 2); mbar_init(cta.bar(B_RES_EMPTY + i), 1); }
-    for (int i = 0; i < NS; ++i) { mbar_init(cta.bar(B_RING_FULL + i), 2 * M::WPS); mbar_init(cta.bar(B_RING_EMPTY + i), 1); }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(cta.bar(B_RING_FULL + i), 2 * M::WPS);
+      mbar_init(cta.bar(B_RING_EMPTY + i), 1);
+    }
     for (int i = 0; i < NACC; ++i) { mbar_init(cta.bar(B_ACC_FULL + i), 1); mbar_init(cta.bar(B_ACC_EMPTY + i), 8); }
     for (int i = 0; i < 2; ++i) mbar_init(cta.bar(B_SUMS + i), 1);
   }
@@ -343,7 +350,9 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const int first = static_cast<int>(blockIdx.x >> 1), stride = static_cast<int>(gridDim.x >> 1);
   const int splits = KL ? 1 : p.splits, items = p.T * splits;
   auto token = [&](int item) { return splits == 1 ? item : item / splits; };
-  auto span = [&](int item) { return tile_span(p.n_end[token(item)], 2 * NK, splits == 1 ? 0 : item % splits, splits); };
+  auto span = [&](int item) {
+    return tile_span(p.n_end[token(item)], 2 * NK, splits == 1 ? 0 : item % splits, splits);
+  };
   bool ok = true;
   int n = 0;                              // items with tiles, walked so far
 
@@ -382,12 +391,12 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // ===================================================================== gathers (gather4: four rows x 64 dims)
     // One lane issues one gather4 of a stage; the warps that fill a stage share its 32 SC of them, and stages go round
     // the groups of such warps.  The entries of the next tile are read while this one is gathered.
-    // An empty or invalid slot reads row slot % S (any row would do, its P and dS are set to zero; one row for all would be
-    // one L2 line for the whole GPU: 30 us against 18 for 96 short tokens); a CTA whose keys of a tile are all behind the
-    // token's last entry reads nothing.
+    // An empty or invalid slot reads row slot % S (any row would do, its P and dS are set to zero; one row for all
+    // would be one L2 line for the whole GPU: 30 us against 18 for 96 short tokens); a CTA whose keys of a tile are all
+    // behind the token's last entry reads nothing.
     constexpr int PER = SC * 32 / M::WPS, GROUPS = 8 / M::WPS;
-    // a group that comes to a stage again has seen the chunk before last of it consumed (its own last stage could not be
-    // filled before): the barrier's parity tells the two last phases apart
+    // a group that comes to a stage again has seen the chunk before last of it consumed (its own last stage could not
+    // be filled before): the barrier's parity tells the two last phases apart
     static_assert(GROUPS <= NS, "stages");
     const int gw = (warp < 8) ? warp - 2 : warp - 6;
     const int grp = gw / M::WPS, gi = (gw % M::WPS) * PER + lane, cc = gi / 32, rg = gi % 32;
@@ -470,9 +479,9 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
   } else {
     // ===================================================================== probabilities (one key a thread)
-    // Two groups of four warps take tiles in turn: the work on a tile is a chain of tensor-memory loads, exponentials and
-    // stores that takes longer than the tile's MMAs (the objective's gradient: 716 us for 2048 tokens with one group, 616
-    // with two).
+    // Two groups of four warps take tiles in turn: the work on a tile is a chain of tensor-memory loads, exponentials
+    // and stores that takes longer than the tile's MMAs (the objective's gradient: 716 us for 2048 tokens with one
+    // group, 616 with two).
     const int grp = warp >= 14 ? 1 : 0;
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
@@ -486,8 +495,8 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int i = (2 * (sp.j1 + grp) + rank) * NK + row; i < p.k; i += 4 * NK) p.dsel[base + i] = 0.f;
       }
       if (sp.j0 >= sp.j1) continue;
-      // the token's -lse (in log2 units) and -scale delta.  A head without any probability mass (lse = -inf) and the heads
-      // that only fill up the tile get -inf: P = 0.
+      // the token's -lse (in log2 units) and -scale delta.  A head without any probability mass (lse = -inf) and the
+      // heads that only fill up the tile get -inf: P = 0.
       float* hs = reinterpret_cast<float*>(cta.smem + OFF_HEADS) + (n & 1) * 256;
       if (grp == 0) {
         const long long at = static_cast<long long>(t) * p.H + row;
@@ -571,7 +580,8 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const float* hl = hs + 32 * c;
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const float4 l = *reinterpret_cast<const float4*>(hl + i), m = *reinterpret_cast<const float4*>(hl + 128 + i);
+              const float4 l = *reinterpret_cast<const float4*>(hl + i);
+              const float4 m = *reinterpret_cast<const float4*>(hl + 128 + i);
               const float p0 = ex2_approx(fmaf(__uint_as_float(s[i]), p.scale_log2, l.x));
               const float p1 = ex2_approx(fmaf(__uint_as_float(s[i + 1]), p.scale_log2, l.y));
               const float p2 = ex2_approx(fmaf(__uint_as_float(s[i + 2]), p.scale_log2, l.z));
@@ -583,9 +593,9 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               ds[i / 2 + 1] = pack_bf16(p2 * fmaf(__uint_as_float(d[i + 2]), p.scale, m.z),
                                         p3 * fmaf(__uint_as_float(d[i + 3]), p.scale, m.w)) & keep;
             }
-            // Straight from the lanes' own rows, a sector a store.  Turned in shared memory to 64-byte pieces the stores are
-            // as fast, but the 16 KB that takes are a ring stage (1274 us for 2048 tokens, against 1159 so); staged for TMA
-            // they were slower, and 16 bytes a store took 1466 in an earlier form against 1252.
+            // Straight from the lanes' own rows, a sector a store.  Turned in shared memory to 64-byte pieces the
+            // stores are as fast, but the 16 KB that takes are a ring stage (1274 us for 2048 tokens, against 1159 so);
+            // staged for TMA they were slower, and 16 bytes a store took 1466 in an earlier form against 1252.
             if (slot0 < p.kp) {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
@@ -663,12 +673,12 @@ mla_bwd_p_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   bwd_end<true>(cta);
 }
 
-// Contributions to dc: contrib[t kp + slot][d] = sum_h dS q[t][h][d] + P dout[t][h][d], one (token, 256 dims) per CTA pair and
-// item, the 64 position dims (dS q alone) as a third item.
+// Contributions to dc: contrib[t kp + slot][d] = sum_h dS q[t][h][d] + P dout[t][h][d], one (token, 256 dims) per CTA
+// pair and item, the 64 position dims (dS q alone) as a third item.
 //
-// M = 256 keys (128 in each CTA), N = 256 dims (128 of q and dout in each CTA, resident), K = heads of dS, then of P.  As
-// single CTAs with N = 192 each MMA read 10 KB of shared memory in 96 cycles, and a token's dS and P three times: 1426 us
-// for 2048 tokens, against 1407.  HBM: the contributions (2.3 MB a token) written, P and dS (1 MB) read.
+// M = 256 keys (128 in each CTA), N = 256 dims (128 of q and dout in each CTA, resident), K = heads of dS, then of P.
+// As single CTAs with N = 192 each MMA read 10 KB of shared memory in 96 cycles, and a token's dS and P three times:
+// 1426 us for 2048 tokens, against 1407.  HBM: the contributions (2.3 MB a token) written, P and dS (1 MB) read.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mbw::dc::THREADS, 1)
 mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_out,
@@ -788,8 +798,8 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
               for (int i = 0; i < hb; ++i) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  mma2_bf16_ss(tmem + 256 * ab, ad + ((i * CHUNK) >> 4) + 2 * k, bd + ((i * UNIT + k * 2048) >> 4), idesc,
-                               (half | i | k) ? 1u : 0u);
+                  mma2_bf16_ss(tmem + 256 * ab, ad + ((i * CHUNK) >> 4) + 2 * k, bd + ((i * UNIT + k * 2048) >> 4),
+                               idesc, (half | i | k) ? 1u : 0u);
                 if (last) mma2_commit(cta.bar(B_RES_EMPTY + half * hb + i));
               }
               mma2_commit(cta.bar(B_RING_EMPTY + rp.stage));
@@ -834,8 +844,8 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
           }
           if (!any) continue;
           scatter_pack64(v, w);
-          // the warp's 32 rows of 64 dims (128-byte swizzled: 16-byte unit u of row r at unit u ^ (r % 8)) go out by TMA, the
-          // previous piece's area being read meanwhile
+          // the warp's 32 rows of 64 dims (128-byte swizzled: 16-byte unit u of row r at unit u ^ (r % 8)) go out by
+          // TMA, the previous piece's area being read meanwhile
           const int area = OFF_OUT + ((2 * (4 * grp + quad)) + (put & 1)) * 4096;
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
@@ -860,8 +870,8 @@ mla_bwd_dc_kernel(const __grid_constant__ CUtensorMap tm_pds, const __grid_const
   bwd_end<true>(cta);
 }
 
-// dq[t][:, 192 dims] = dS^T . C per item, accumulated over the token's keys (or, with splits, over the split's) in tensor
-// memory (lane = head).
+// dq[t][:, 192 dims] = dS^T . C per item, accumulated over the token's keys (or, with splits, over the split's) in
+// tensor memory (lane = head).
 __global__ void __launch_bounds__(mbw::dq::THREADS, 1)
 mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams p) {
   using namespace mbw;
@@ -888,7 +898,8 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
   auto part = [&](int item, int& ts, int& d3) {        // item: (token, split, 192 dims)
     d3 = item % 3;
     ts = item / 3;
-    return p.splits == 1 ? tile_span(p.n_end[ts], KT, 0, 1) : tile_span(p.n_end[ts / p.splits], KT, ts % p.splits, p.splits);
+    return p.splits == 1 ? tile_span(p.n_end[ts], KT, 0, 1)
+                         : tile_span(p.n_end[ts / p.splits], KT, ts % p.splits, p.splits);
   };
   auto token = [&](int ts) { return p.splits == 1 ? ts : ts / p.splits; };
   bool ok = true;
@@ -974,7 +985,8 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
-            mma_bf16_ss(tmem + 256 * ab, ad + ((k * 2048) >> 4), bd + ((k * 2048) >> 4), idesc, (j > sp.j0 || k) ? 1u : 0u);
+            mma_bf16_ss(tmem + 256 * ab, ad + ((k * 2048) >> 4), bd + ((k * 2048) >> 4), idesc,
+                        (j > sp.j0 || k) ? 1u : 0u);
           mma_commit(cta.bar(B_RING_EMPTY + rp.stage));
         }
         __syncwarp();
@@ -1010,7 +1022,9 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
           uint4* dst = reinterpret_cast<uint4*>(p.dq + at + 32 * c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            auto pk = [&](int q) { return pack_bf16(__uint_as_float(v[8 * i + 2 * q]), __uint_as_float(v[8 * i + 2 * q + 1])); };
+            auto pk = [&](int q) {
+              return pack_bf16(__uint_as_float(v[8 * i + 2 * q]), __uint_as_float(v[8 * i + 2 * q + 1]));
+            };
             dst[i] = make_uint4(pk(0), pk(1), pk(2), pk(3));
           }
         } else {
@@ -1029,8 +1043,8 @@ mla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_ds, const MlaBwdParams 
   bwd_end(cta);
 }
 
-// The splits' sums of a token joined in order: out[t][i] = sum over its splits of part[t splits + sp][i], i < width (bf16),
-// and the last `tail` values of a part (fp32 results).  width and tail are multiples of 4.
+// The splits' sums of a token joined in order: out[t][i] = sum over its splits of part[t splits + sp][i], i < width
+// (bf16), and the last `tail` values of a part (fp32 results).  width and tail are multiples of 4.
 __global__ void __launch_bounds__(256) join_splits_kernel(const float* part, const int* n_end, int keys, int splits,
                                                           int width, int tail, uint16_t* out, float* out_tail) {
   pdl_allow_next();
@@ -1046,15 +1060,16 @@ __global__ void __launch_bounds__(256) join_splits_kernel(const float* part, con
     s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
   }
   if (i < width)
-    *reinterpret_cast<uint2*>(out + static_cast<long long>(t) * width + i) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+    *reinterpret_cast<uint2*>(out + static_cast<long long>(t) * width + i) =
+        make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
   else {
     float* to = out_tail + static_cast<long long>(t) * tail + i - width;   // a caller's array: aligned to its type only
     to[0] = s.x; to[1] = s.y; to[2] = s.z; to[3] = s.w;
   }
 }
 
-// What the other kernels of a chunk start from: delta[t][h] = dout . out over the 512 value dims (one warp a row, eight rows
-// a block) and the scatter table, cleared in equal shares by all blocks.
+// What the other kernels of a chunk start from: delta[t][h] = dout . out over the 512 value dims (one warp a row, eight
+// rows a block) and the scatter table, cleared in equal shares by all blocks.
 __global__ void __launch_bounds__(256) mla_bwd_begin_kernel(const uint16_t* dout, const uint16_t* out, long long rows,
                                                             float* delta, uint4* table, long long n) {
   pdl_allow_next();
